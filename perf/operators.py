@@ -350,7 +350,7 @@ def run(state):
             cf.kv4_append(cache, s["k"], s["v"], s["slots"])
             return list(cf.kv4_read(cache, s["slots"], s["k"].dtype))
         lse = torch.empty(s["q"].shape[:2], dtype=torch.float32, device=s["q"].device)
-        return [cf.kv4_attention(s["q"], cache, s["kv_lens"], table=s["table"], q_starts=s["q_starts"], max_q=c["max_q"], max_kv=c["max_kv"],
+        return [cf.kv4_attention(s["q"], cache, s["kv_lens"], table=s["table"], q_starts=s["q_starts"], max_q=c["max_q"],
                                  causal=c["causal"], window=c["window"], scale=s["scale"], lse=lse), lse]
     return {"norm": _norm_plain, "store": _store_plain, "attn": _attn_plain}[c["op"]](s)
 
