@@ -18,6 +18,9 @@ LIB_PATH = os.path.join(_PKG, "libcf.so")
 
 CF_BF16, CF_F32 = 0, 1
 CF_MODE_NOEF, CF_MODE_NAIVE = 1, 2
+CF_NORM_NONE, CF_NORM_RMS, CF_NORM_LAYER = 0, 1, 2
+CF_ROPE_NONE, CF_ROPE_INTERLEAVED, CF_ROPE_HALF = 0, 1, 2
+CF_ATTN_CAUSAL = 1
 GROUP = 128
 
 STATUS = {0: "CF_OK", -1: "CF_E_NULL", -2: "CF_E_SHAPE", -3: "CF_E_ALIGN", -4: "CF_E_ARG",
@@ -38,10 +41,24 @@ _SIG = {
     "cf_lowrank_decompress": ("i", "ipppp" "pllii" "p"),
     "cf_lowrank_workspace_bytes": ("z", "llii"),
     "cf_codes_bytes": ("l", "li"),
+    "cf_qk_norm_rope": ("i", "iliii" "rrrr" "ipppp" "fi" "ppli" "pp"),
+    "cf_kv4_cache_bytes": ("l", "liii"),
+    "cf_kv4_append": ("i", "irrpl" "pliii" "p"),
+    "cf_kv4_read": ("i", "ipliii" "plrr" "p"),
+    "cf_kv4_attention": ("i", "irli" "pliii" "ipipp" "liif" "rppzp"),
+    "cf_kv4_attention_workspace_bytes": ("z", "iliii"),
     "cf_strerror": ("s", "i"),
     "cf_abi_version": ("i", ""),
 }
-_CT = {"i": ctypes.c_int, "l": ctypes.c_int64, "p": ctypes.c_void_p, "z": ctypes.c_size_t,
+
+
+class Rows(ctypes.Structure):
+    """cf_rows: where the rows of a (tokens, heads, head_dim) tensor start."""
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+# r: a pointer to cf_rows, f: float
+_CT = {"r": ctypes.POINTER(Rows), "f": ctypes.c_float, "i": ctypes.c_int, "l": ctypes.c_int64, "p": ctypes.c_void_p, "z": ctypes.c_size_t,
        "s": ctypes.c_char_p}
 
 
@@ -448,3 +465,186 @@ def lowrank_decompress(factor_bits: int, payload, ahat: torch.Tensor, rank: int,
     _check("cf_lowrank_decompress", lib.cf_lowrank_decompress(
         factor_bits, _ptr(u), _ptr(us), _ptr(v), _ptr(vs), _ptr(ahat), m, n, rank, batch,
         _stream(stream)))
+
+
+def _rows(name: str, t: torch.Tensor) -> Rows:
+    """The rows of a (tokens, heads, head_dim) tensor, of any strides but the last."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} has {t.dim()} axes; libcf wants (tokens, heads, head_dim)")
+    if not t.is_cuda:
+        raise ValueError("libcf takes device tensors (a host pointer would fault the kernel)")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} on {t.device}, but the current device is cuda:{torch.cuda.current_device()} "
+                         "(libcf launches on the current device)")
+    st, sh, sd = t.stride()
+    if sd != 1 and t.shape[2] > 1:
+        raise ValueError(f"{name}: the channels of a row must be consecutive")
+    return Rows(t.data_ptr(), st, sh)
+
+
+def _shaped(name: str, t: torch.Tensor | None, *shape):
+    if t is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} is {tuple(t.shape)}, the call needs {shape}")
+
+
+def qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, norm: int = CF_NORM_RMS,
+                 q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None,
+                 q_bias: torch.Tensor | None = None, k_bias: torch.Tensor | None = None, eps: float = 1e-6,
+                 rope: int = CF_ROPE_NONE, cos: torch.Tensor | None = None, sin: torch.Tensor | None = None,
+                 positions: torch.Tensor | None = None, q_out: torch.Tensor | None = None,
+                 k_out: torch.Tensor | None = None, stream=None):
+    """Per-head norms of q and k (tokens, heads, head_dim) and the position rotation, in one
+    pass; returns (q_out, k_out).  Either side may be None.  Slices of a packed projection and
+    head-major views are taken as they are; q_out may be q itself, and k_out k.  cos and sin
+    are (positions, rot_dim / 2) fp32, weights and biases (head_dim,) fp32, positions
+    (tokens,) int32 (negative: a padding token, whose output rows stay as they are)."""
+    a = q if q is not None else k
+    if a is None or a.dim() != 3:
+        raise ValueError("q or k must be a (tokens, heads, head_dim) tensor")
+    tokens, _, dim = a.shape
+    dt = _act_dtype(a)
+    sides, outs, rows = (("q", q), ("k", k)), [q_out, k_out], []
+    heads = [0 if t is None else t.shape[1] if t.dim() == 3 else -1 for _, t in sides]
+    for (nm, t), o, h in zip(sides, outs, heads):
+        if t is not None:
+            _dtype(nm, t, a.dtype)
+            _shaped(nm, t, tokens, h, dim)
+            _dtype(nm + "_out", o, a.dtype)
+            _shaped(nm + "_out", o, tokens, h, dim)
+    for i, (nm, t) in enumerate(sides):
+        if t is None:
+            rows += [None, None]
+            continue
+        if outs[i] is None:
+            outs[i] = _keep_for(torch.empty(t.shape, dtype=t.dtype, device=t.device), stream)
+        rows += [_rows(nm, t), _rows(nm + "_out", outs[i])]
+    for nm, t in (("q_weight", q_weight), ("q_bias", q_bias), ("k_weight", k_weight), ("k_bias", k_bias)):
+        _dtype(nm, t, _F32)
+        _shaped(nm, t, dim)
+    n_pos = rot = 0
+    if rope != CF_ROPE_NONE:
+        if cos is None or sin is None or cos.dim() != 2:
+            raise ValueError("a rotation needs cos and sin, (positions, rot_dim / 2) fp32")
+        n_pos, rot = cos.shape[0], 2 * cos.shape[1]
+        _dtype("cos", cos, _F32)
+        _dtype("sin", sin, _F32)
+        _shaped("sin", sin, *cos.shape)
+        _dtype("positions", positions, torch.int32)
+        _shaped("positions", positions, tokens)
+    else:
+        cos = sin = positions = None
+    _check("cf_qk_norm_rope", lib.cf_qk_norm_rope(
+        dt, tokens, heads[0], heads[1], dim, rows[0], rows[2], rows[1], rows[3], norm, _ptr(q_weight), _ptr(q_bias),
+        _ptr(k_weight), _ptr(k_bias), eps, rope, _ptr(cos), _ptr(sin), n_pos, rot, _ptr(positions), _stream(stream)))
+    return outs[0], outs[1]
+
+
+@dataclass
+class KV4Cache:
+    """A paged K/V cache of 4-bit codes: ``data`` is (pages, kv_heads, page_size * head_dim *
+    17 / 16) uint8.  A copy of ``data`` is a checkpoint of it."""
+    data: torch.Tensor
+    page_size: int
+    head_dim: int
+
+    @staticmethod
+    def create(pages: int, page_size: int, kv_heads: int, head_dim: int, device=None) -> "KV4Cache":
+        nb = lib.cf_kv4_cache_bytes(pages, page_size, kv_heads, head_dim)
+        if nb < 0:
+            raise CFError("cf_kv4_cache_bytes", nb)
+        return KV4Cache(torch.zeros((pages, kv_heads, nb // pages // kv_heads), dtype=torch.uint8,
+                                    device=device or require_device()), page_size, head_dim)
+
+    def _args(self):
+        d = self.data
+        _dtype("cache", d, _U8)
+        if d.dim() != 3 or d.shape[2] * 16 != self.page_size * self.head_dim * 17:
+            raise ValueError(f"cache data is {tuple(d.shape)}: want (pages, kv_heads, page_size * head_dim * 17 / 16)")
+        return _ptr(d), d.shape[0], self.page_size, d.shape[1], self.head_dim
+
+
+def kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, stream=None):
+    """Quantize rows k, v (tokens, kv_heads, head_dim) into the cache's slots (tokens,) int64,
+    page * page_size + place; a negative slot takes nothing."""
+    want = (k.shape[0] if k.dim() else 0, cache.data.shape[1], cache.head_dim)
+    _shaped("k", k, *want)
+    _shaped("v", v, *want)
+    _dtype("v", v, k.dtype)
+    _dtype("slots", slots, torch.int64)
+    _shaped("slots", slots, want[0])
+    dt = _act_dtype(k)
+    _check("cf_kv4_append", lib.cf_kv4_append(dt, _rows("k", k), _rows("v", v), _ptr(slots), want[0], *cache._args(),
+                                              _stream(stream)))
+
+
+def kv4_read(cache: KV4Cache, slots: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
+             k: torch.Tensor | None = None, v: torch.Tensor | None = None, stream=None):
+    """The rows that the cache holds in slots (tokens,) int64, as (k, v) of (tokens, kv_heads,
+    head_dim); zeros for slots that are not in the cache."""
+    if slots.dim() != 1:
+        raise ValueError("slots must be (tokens,)")
+    want = (slots.shape[0], cache.data.shape[1], cache.head_dim)
+    _dtype("slots", slots, torch.int64)
+    if k is None:
+        k = _keep_for(torch.empty(want, dtype=dtype, device=cache.data.device), stream)
+    if v is None:
+        v = _keep_for(torch.empty(want, dtype=k.dtype, device=cache.data.device), stream)
+    _shaped("k", k, *want)
+    _shaped("v", v, *want)
+    _dtype("v", v, k.dtype)
+    dt = _act_dtype(k)
+    _check("cf_kv4_read", lib.cf_kv4_read(dt, *cache._args(), _ptr(slots), want[0], _rows("k", k), _rows("v", v),
+                                          _stream(stream)))
+    return k, v
+
+
+def kv4_attention_workspace_bytes(dtype: torch.dtype, max_q: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
+    dt = CF_BF16 if dtype == torch.bfloat16 else CF_F32 if dtype == torch.float32 else -1
+    nb = lib.cf_kv4_attention_workspace_bytes(dt, max_q, q_heads, kv_heads, head_dim)
+    if nb == 0:
+        raise CFError("cf_kv4_attention_workspace_bytes", -2)
+    return nb
+
+
+def kv4_attention(q: torch.Tensor, cache: KV4Cache, kv_lens: torch.Tensor, table: torch.Tensor | None = None,
+                  q_starts: torch.Tensor | None = None, max_q: int = 0, causal: bool = False, window: int = 0,
+                  scale: float | None = None, table_width: int = 0, out: torch.Tensor | None = None,
+                  lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """Attention of q (total_q, q_heads, head_dim) over the cache; returns out.  kv_lens
+    (batch,), table (batch, pages) and q_starts (batch + 1,) are int32; without a table
+    sequence b has pages b * table_width and on, without q_starts every sequence has
+    total_q / batch queries.  lse (total_q, q_heads) fp32 is written where it is given.  Rows
+    that belong to no sequence stay as they are.  max_q: the most queries of a sequence, if
+    known; scale: head_dim ** -0.5 if None."""
+    if q.dim() != 3:
+        raise ValueError("q must be (total_q, q_heads, head_dim)")
+    total, heads, dim = q.shape
+    if dim != cache.head_dim:
+        raise ValueError(f"q has rows of {dim}, the cache of {cache.head_dim}")
+    dt = _act_dtype(q)
+    batch = kv_lens.shape[0] if kv_lens.dim() == 1 else -1
+    for nm, t, shape in (("kv_lens", kv_lens, (batch,)), ("q_starts", q_starts, (batch + 1,))):
+        _dtype(nm, t, torch.int32)
+        _shaped(nm, t, *shape)
+    if table is not None:
+        _dtype("table", table, torch.int32)
+        table_width = table.shape[-1]
+        _shaped("table", table, batch, table_width)
+    if out is None:
+        out = _keep_for(torch.empty((total, heads, dim), dtype=q.dtype, device=q.device), stream)
+    _dtype("out", out, q.dtype)
+    _shaped("out", out, total, heads, dim)
+    _dtype("lse", lse, _F32)
+    _shaped("lse", lse, total, heads)
+    if workspace is None:
+        most = max_q or (total if q_starts is not None else total // max(batch, 1))
+        need = lib.cf_kv4_attention_workspace_bytes(dt, most, heads, cache.data.shape[1], dim)
+        if need and total:
+            # freed when this call returns, possibly before the launch stream has used it
+            workspace = _keep_for(torch.empty(need, dtype=_U8, device=q.device), stream)
+    _check("cf_kv4_attention", lib.cf_kv4_attention(
+        dt, _rows("q", q), total, heads, *cache._args(), batch, _ptr(table), table_width, _ptr(kv_lens),
+        _ptr(q_starts), max_q, CF_ATTN_CAUSAL if causal else 0, window, dim ** -0.5 if scale is None else scale,
+        _rows("out", out), _ptr(lse), _ptr(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)))
+    return out

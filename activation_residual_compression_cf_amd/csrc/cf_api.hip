@@ -128,6 +128,99 @@ int check_lowrank_compress(int a_dtype, const void* a, float* ahat, float* err, 
     return CF_OK;
 }
 
+// ---- rows of heads -------------------------------------------------------------------
+
+typedef __int128 wide;  // extents of rows are formed before they are known to be small
+
+// Rows of a cf_rows: tokens x heads rows of dim elements of esz bytes.
+struct RowsOf {
+    cf_rows r;
+    int64_t tokens, heads, dim, esz;
+    bool none() const { return tokens == 0 || heads == 0; }
+    wide extent() const {  // elements from the first row's start to the last row's end
+        return wide(tokens - 1) * r.token_stride + wide(heads - 1) * r.head_stride + dim;
+    }
+    Range range() const { return range_of(r.data, none() ? 0 : static_cast<int64_t>(extent() * esz)); }
+};
+
+constexpr wide kMaxExtent = wide(1) << 46;  // bytes: beyond any device's memory
+
+// NULL, strides, alignment of one operand's rows, in this order.
+int check_rows(const cf_rows* r, int64_t tokens, int64_t heads, int64_t dim, int64_t esz, bool written, RowsOf* x) {
+    *x = RowsOf{r ? *r : cf_rows{nullptr, 0, 0}, tokens, heads, dim, esz};
+    if (x->none()) return CF_OK;
+    if (!r || !r->data) return CF_E_NULL;
+    if (tokens == 1) x->r.token_stride = 0;  // strides that nothing is multiplied with do not matter
+    if (heads == 1) x->r.head_stride = 0;
+    const int64_t ts = x->r.token_stride, hs = x->r.head_stride;
+    if (ts < 0 || hs < 0 || x->extent() * esz > kMaxExtent) return CF_E_SHAPE;
+    if (written) {
+        const bool by_token = (heads == 1 || hs >= dim) && (tokens == 1 || ts >= wide(heads - 1) * hs + dim);
+        const bool by_head = (tokens == 1 || ts >= dim) && (heads == 1 || hs >= wide(tokens - 1) * ts + dim);
+        if (!by_token && !by_head) return CF_E_SHAPE;
+    }
+    if (!aligned16(r->data) || ts * esz % 16 || hs * esz % 16) return CF_E_ALIGN;
+    return CF_OK;
+}
+
+// Whether two sets of rows surely share no byte: their ranges are apart, or they are two
+// slices of the heads of one packed token-major buffer.
+bool apart(const RowsOf& a, const RowsOf& b) {
+    if (a.none() || b.none() || !overlap(a.range(), b.range())) return true;
+    const int64_t ts = a.r.token_stride;
+    if (a.esz != b.esz || ts != b.r.token_stride || ts <= 0) return false;
+    const wide wa = wide(a.heads - 1) * a.r.head_stride + a.dim, wb = wide(b.heads - 1) * b.r.head_stride + b.dim;
+    if (wa > ts || wb > ts) return false;
+    const wide bytes = wide(reinterpret_cast<uintptr_t>(b.r.data)) - wide(reinterpret_cast<uintptr_t>(a.r.data));
+    const wide period = wide(ts) * a.esz;
+    wide d = bytes % period;
+    if (d < 0) d += period;
+    return d >= wa * a.esz && d + wb * b.esz <= period;
+}
+
+bool same_rows(const RowsOf& a, const RowsOf& b) {
+    return a.r.data == b.r.data && a.tokens == b.tokens && a.heads == b.heads && a.esz == b.esz &&
+           a.r.token_stride == b.r.token_stride && a.r.head_stride == b.r.head_stride;
+}
+
+int64_t elem_bytes(int a_dtype) { return a_dtype == CF_BF16 ? 2 : 4; }
+
+// ---- the 4-bit cache -----------------------------------------------------------------
+
+bool kv4_dims(int page_size, int kv_heads, int head_dim) {
+    return (head_dim == 64 || head_dim == 128) && page_size >= 16 && page_size <= 256 &&
+           (page_size & (page_size - 1)) == 0 && kv_heads >= 1 && kv_heads <= 65535;
+}
+
+cf::KvCache kv4_cache(const uint8_t* cache, int64_t pages, int page_size, int kv_heads, int head_dim) {
+    return {const_cast<uint8_t*>(cache), pages, kv_heads, {page_size, head_dim}, __builtin_ctz(page_size)};
+}
+
+// cf_kv4_append, and cf_kv4_read, whose rows are written.
+int kv4_rows(bool read, int a_dtype, const cf_rows* k, const cf_rows* v, const int64_t* slots, int64_t tokens,
+             const uint8_t* cache, int64_t pages, int page_size, int kv_heads, int head_dim, void* stream) {
+    if (a_dtype != CF_BF16 && a_dtype != CF_F32) return CF_E_ARG;
+    const int64_t bytes = cf_kv4_cache_bytes(pages, page_size, kv_heads, head_dim);
+    if (bytes < 0) return CF_E_SHAPE;
+    if (tokens < 0 || tokens > kMaxNumel / head_dim / kv_heads) return CF_E_SHAPE;
+    if (tokens == 0) return CF_OK;
+    if (!cache || !slots) return CF_E_NULL;
+    RowsOf x[2];
+    if (int rc = check_rows(k, tokens, kv_heads, head_dim, elem_bytes(a_dtype), read, &x[0])) return rc;
+    if (int rc = check_rows(v, tokens, kv_heads, head_dim, elem_bytes(a_dtype), read, &x[1])) return rc;
+    if (!aligned16(cache) || (reinterpret_cast<uintptr_t>(slots) & 7u)) return CF_E_ALIGN;
+    const Range rc = range_of(cache, bytes), rs = range_of(slots, tokens * 8);
+    if (read ? !apart(x[0], x[1]) || overlap(x[0].range(), rs) || overlap(x[1].range(), rs) : overlap(rc, rs))
+        return CF_E_ALIAS;
+    if (overlap(x[0].range(), rc) || overlap(x[1].range(), rc)) return CF_E_ALIAS;
+    if (int e = check_device()) return e;
+    const auto f = read ? cf::launch_kv4_read : cf::launch_kv4_append;
+    return f(a_dtype, x[0].r, x[1].r, slots, tokens, kv4_cache(cache, pages, page_size, kv_heads, head_dim),
+             static_cast<hipStream_t>(stream)) == hipSuccess
+               ? CF_OK
+               : CF_E_HIP;
+}
+
 }  // namespace
 
 extern "C" {
@@ -348,6 +441,139 @@ int cf_lowrank_decompress(int factor_bits, const void* u, const float* u_scales,
     if (int rc = check_device()) return rc;
     return cf::launch_lowrank_decompress(factor_bits, u, u_scales, v, v_scales, ahat, m, n, rank, batch,
                                          static_cast<hipStream_t>(stream)) == hipSuccess
+               ? CF_OK
+               : CF_E_HIP;
+}
+
+int cf_qk_norm_rope(int a_dtype, int64_t tokens, int q_heads, int k_heads, int head_dim, const cf_rows* q,
+                    const cf_rows* k, const cf_rows* q_out, const cf_rows* k_out, int norm,
+                    const float* q_weight, const float* q_bias, const float* k_weight, const float* k_bias,
+                    float eps, int rope, const float* cos, const float* sin, int64_t n_pos, int rot_dim,
+                    const int32_t* positions, void* stream) {
+    if (a_dtype != CF_BF16 && a_dtype != CF_F32) return CF_E_ARG;
+    if (norm < CF_NORM_NONE || norm > CF_NORM_LAYER || rope < CF_ROPE_NONE || rope > CF_ROPE_HALF) return CF_E_ARG;
+    if (!(eps >= 0.f) || eps > 3.4e38f) return CF_E_ARG;
+    if (tokens < 0 || q_heads < 0 || k_heads < 0 || q_heads > 65535 || k_heads > 65535 || head_dim <= 0 ||
+        head_dim % 8 || head_dim > 256)
+        return CF_E_SHAPE;
+    const int64_t heads = int64_t(q_heads) + k_heads;
+    if (heads == 0 || tokens > kMaxNumel / head_dim / heads) return CF_E_SHAPE;
+    const bool turn = rope != CF_ROPE_NONE;
+    if (turn && (rot_dim <= 0 || rot_dim % 16 || rot_dim > head_dim || n_pos <= 0 || n_pos > kMaxNumel / rot_dim ||
+                 (!positions && tokens > n_pos)))
+        return CF_E_SHAPE;
+    if (tokens == 0) return CF_OK;
+    if (turn && (!cos || !sin)) return CF_E_NULL;
+    const int64_t esz = elem_bytes(a_dtype);
+    RowsOf x[4];
+    if (int rc = check_rows(q, tokens, q_heads, head_dim, esz, false, &x[0])) return rc;
+    if (int rc = check_rows(k, tokens, k_heads, head_dim, esz, false, &x[1])) return rc;
+    if (int rc = check_rows(q_out, tokens, q_heads, head_dim, esz, true, &x[2])) return rc;
+    if (int rc = check_rows(k_out, tokens, k_heads, head_dim, esz, true, &x[3])) return rc;
+    const float* const par[4] = {q_heads ? q_weight : nullptr, q_heads ? q_bias : nullptr,
+                                 k_heads ? k_weight : nullptr, k_heads ? k_bias : nullptr};
+    for (const float* w : par)
+        if (!aligned16(w)) return CF_E_ALIGN;
+    if (turn && (!aligned16(cos) || !aligned16(sin) || !aligned4(positions))) return CF_E_ALIGN;
+    if ((!same_rows(x[0], x[2]) && !apart(x[0], x[2])) || (!same_rows(x[1], x[3]) && !apart(x[1], x[3])) ||
+        !apart(x[0], x[3]) || !apart(x[1], x[2]) || !apart(x[2], x[3]))
+        return CF_E_ALIAS;
+    const int64_t table = turn ? n_pos * (rot_dim / 2) * 4 : 0;
+    const Range read[7] = {range_of(par[0], par[0] ? head_dim * 4 : 0), range_of(par[1], par[1] ? head_dim * 4 : 0),
+                           range_of(par[2], par[2] ? head_dim * 4 : 0), range_of(par[3], par[3] ? head_dim * 4 : 0),
+                           range_of(cos, table), range_of(sin, table),
+                           range_of(positions, turn && positions ? tokens * 4 : 0)};
+    for (const Range& r : read)
+        for (const RowsOf* o : {&x[2], &x[3]})
+            if (r.hi > r.lo && !o->none() && overlap(r, o->range())) return CF_E_ALIAS;
+    if (int rc = check_device()) return rc;
+    return cf::launch_qk_norm_rope(a_dtype, tokens, q_heads, k_heads, head_dim, x[0].r, x[1].r, x[2].r, x[3].r, norm,
+                                   par[0], par[1], par[2], par[3], eps, rope, cos, sin, n_pos, rot_dim, positions,
+                                   static_cast<hipStream_t>(stream)) == hipSuccess
+               ? CF_OK
+               : CF_E_HIP;
+}
+
+int64_t cf_kv4_cache_bytes(int64_t pages, int page_size, int kv_heads, int head_dim) {
+    if (!kv4_dims(page_size, kv_heads, head_dim) || pages < 1) return CF_E_SHAPE;
+    const wide bytes = wide(pages) * kv_heads * page_size * head_dim * 17 / 16;
+    return bytes <= kMaxExtent ? static_cast<int64_t>(bytes) : CF_E_SHAPE;
+}
+
+int cf_kv4_append(int a_dtype, const cf_rows* k, const cf_rows* v, const int64_t* slots, int64_t tokens,
+                  uint8_t* cache, int64_t pages, int page_size, int kv_heads, int head_dim, void* stream) {
+    return kv4_rows(false, a_dtype, k, v, slots, tokens, cache, pages, page_size, kv_heads, head_dim, stream);
+}
+
+int cf_kv4_read(int a_dtype, const uint8_t* cache, int64_t pages, int page_size, int kv_heads, int head_dim,
+                const int64_t* slots, int64_t tokens, const cf_rows* k, const cf_rows* v, void* stream) {
+    return kv4_rows(true, a_dtype, k, v, slots, tokens, cache, pages, page_size, kv_heads, head_dim, stream);
+}
+
+size_t cf_kv4_attention_workspace_bytes(int a_dtype, int64_t max_q, int q_heads, int kv_heads, int head_dim) {
+    if ((a_dtype != CF_BF16 && a_dtype != CF_F32) || !kv4_dims(16, kv_heads, head_dim) || q_heads < 1 ||
+        q_heads > 65535 || q_heads % kv_heads || max_q < 1 || max_q > INT32_MAX / q_heads)
+        return 0;
+    return cf::kv4_attention_workspace(a_dtype, head_dim, max_q * (q_heads / kv_heads));
+}
+
+int cf_kv4_attention(int a_dtype, const cf_rows* q, int64_t total_q, int q_heads, const uint8_t* cache,
+                     int64_t pages, int page_size, int kv_heads, int head_dim, int batch, const int32_t* table,
+                     int table_width, const int32_t* kv_lens, const int32_t* q_starts, int64_t max_q, int flags,
+                     int window, float scale, const cf_rows* out, float* lse, void* workspace, size_t ws_bytes,
+                     void* stream) {
+    if (a_dtype != CF_BF16 && a_dtype != CF_F32) return CF_E_ARG;
+    if ((flags & ~CF_ATTN_CAUSAL) || window < 0 || (window && !(flags & CF_ATTN_CAUSAL))) return CF_E_ARG;
+    if (!(scale > 0.f) || scale > 3.4e38f) return CF_E_ARG;
+    const int64_t cache_bytes = cf_kv4_cache_bytes(pages, page_size, kv_heads, head_dim);
+    if (cache_bytes < 0) return CF_E_SHAPE;
+    if (q_heads < 1 || q_heads > 65535 || q_heads % kv_heads || total_q < 0 || total_q > INT32_MAX / q_heads ||
+        max_q < 0 || max_q > total_q)
+        return CF_E_SHAPE;
+    if (total_q == 0) return CF_OK;
+    if (batch < 1 || table_width < 1 || int64_t(table_width) * page_size > INT32_MAX - 256 ||
+        (!table && int64_t(batch) * table_width > pages) || (!q_starts && total_q % batch))
+        return CF_E_SHAPE;
+    if (!cache || !kv_lens || !workspace) return CF_E_NULL;
+    const int64_t esz = elem_bytes(a_dtype);
+    RowsOf x[2];
+    if (int rc = check_rows(q, total_q, q_heads, head_dim, esz, false, &x[0])) return rc;
+    if (int rc = check_rows(out, total_q, q_heads, head_dim, esz, true, &x[1])) return rc;
+    if (!aligned16(cache) || !aligned4(table) || !aligned4(kv_lens) || !aligned4(q_starts) || !aligned4(lse) ||
+        (reinterpret_cast<uintptr_t>(workspace) & 255u))
+        return CF_E_ALIGN;
+    if (max_q == 0) max_q = q_starts ? total_q : total_q / batch;
+    const size_t need = cf_kv4_attention_workspace_bytes(a_dtype, max_q, q_heads, kv_heads, head_dim);
+    if (ws_bytes < need) return CF_E_WORKSPACE;
+    if (!apart(x[0], x[1])) return CF_E_ALIAS;
+    const Range r[8] = {x[0].range(),
+                        range_of(cache, cache_bytes),
+                        range_of(table, table ? int64_t(batch) * table_width * 4 : 0),
+                        range_of(kv_lens, int64_t(batch) * 4),
+                        range_of(q_starts, q_starts ? (int64_t(batch) + 1) * 4 : 0),
+                        x[1].range(),
+                        range_of(lse, lse ? total_q * q_heads * 4 : 0),
+                        range_of(workspace, static_cast<int64_t>(need))};
+    for (int i = 5; i < 8; ++i)
+        for (int j = i == 5 ? 1 : 0; j < i; ++j)  // q and out were looked at row by row
+            if (r[i].hi > r[i].lo && r[j].hi > r[j].lo && overlap(r[i], r[j])) return CF_E_ALIAS;
+    if (int rc = check_device()) return rc;
+    const cf::Kv4Attention call{x[0].r,
+                                x[1].r,
+                                kv4_cache(cache, pages, page_size, kv_heads, head_dim),
+                                table,
+                                kv_lens,
+                                q_starts,
+                                lse,
+                                total_q,
+                                max_q,
+                                batch,
+                                table_width,
+                                q_heads,
+                                flags & CF_ATTN_CAUSAL,
+                                window,
+                                scale};
+    return cf::launch_kv4_attention(a_dtype, call, workspace, static_cast<hipStream_t>(stream)) == hipSuccess
                ? CF_OK
                : CF_E_HIP;
 }

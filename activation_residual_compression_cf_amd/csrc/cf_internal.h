@@ -5,6 +5,9 @@
 
 #include <cstdint>
 
+#include "cf.h"
+#include "cf_kv4.h"
+
 namespace cf {
 
 // Groups of 128 contiguous elements are the unit of every 1/2-bit kernel.
@@ -61,5 +64,35 @@ hipError_t launch_lowrank_compress(int a_dtype, const void* a, float* ahat, floa
 hipError_t launch_lowrank_decompress(int factor_bits, const void* u, const float* u_scales,
                                      const void* v, const float* v_scales, float* ahat, int64_t m,
                                      int64_t n, int rank, int64_t batch, hipStream_t stream);
+
+// Rows of heads: row (t, h) starts at data + t * token_stride + h * head_stride elements.
+using RowSet = cf_rows;
+
+hipError_t launch_qk_norm_rope(int a_dtype, int64_t tokens, int q_heads, int k_heads, int head_dim, const RowSet& q,
+                               const RowSet& k, const RowSet& q_out, const RowSet& k_out, int norm,
+                               const float* q_weight, const float* q_bias, const float* k_weight,
+                               const float* k_bias, float eps, int rope, const float* cos, const float* sin,
+                               int64_t n_pos, int rot_dim, const int32_t* positions, hipStream_t stream);
+
+hipError_t launch_kv4_append(int a_dtype, const RowSet& k, const RowSet& v, const int64_t* slots, int64_t tokens,
+                             const KvCache& cache, hipStream_t stream);
+hipError_t launch_kv4_read(int a_dtype, const RowSet& k, const RowSet& v, const int64_t* slots, int64_t tokens,
+                           const KvCache& cache, hipStream_t stream);
+
+// One attention call over the 4-bit cache.
+struct Kv4Attention {
+    RowSet q, out;
+    KvCache cache;
+    const int32_t* table;     // batch x table_width, or null: sequence b has pages b * table_width ..
+    const int32_t* kv_lens;   // batch
+    const int32_t* q_starts;  // batch + 1, or null: total_q / batch queries each
+    float* lse;               // total_q x q_heads, or null
+    int64_t total_q, max_q;
+    int batch, table_width, q_heads, causal, window;
+    float scale;
+};
+// max_rows: the most query tokens of a sequence times the query heads of a K/V head.
+size_t kv4_attention_workspace(int a_dtype, int head_dim, int64_t max_rows);
+hipError_t launch_kv4_attention(int a_dtype, const Kv4Attention& call, void* workspace, hipStream_t stream);
 
 }  // namespace cf

@@ -1,0 +1,745 @@
+// cf_kv4_attn.hip - attention over the 4-bit K/V cache.
+//
+//   o_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = exp(scale q_i k_j - m_i),  lse_i = m_i + log sum_j p_ij
+// over the keys j that row i may see, in one pass over the keys with a running reference m
+// and sum.  A row of the product is one (query token, query head); the rows of the query
+// heads that share a K/V head are worked on together.
+//
+// What one wave does with 32 keys and 16 rows (matrix products of 16 x 16 with 32 terms;
+// lane = 16 g + n):
+//   S^T = K Q^T   K rows are keys; lane (g, n) holds a quarter of key row n's channels, which
+//                 is one load of codes, and the codes become bf16 by the hardware's
+//                 conversion with the group's scale.  Rows are keys in such an order that
+//                 lane (g, n) ends up with the scores of keys 8g .. 8g+7 for row n.
+//   O^T = V^T P^T the terms are keys: lane (g, n) needs keys 8g .. 8g+7 of its rows, which it
+//                 has, and of channel piece n, which is how the cache lays V out: one load.
+//                 Conversions give pairs of channels of one key; a byte permutation makes
+//                 pairs of keys of them.
+// So nothing passes through shared memory, and m, the sum and the rescaling of O are a
+// lane's own.  K is exact in bf16 and V in fp16 (the cache's exponents see to that), and so are
+// bf16 queries; fp32 queries are split into three bf16 parts that add up to them.  P is
+// rounded to fp16 (11 bits: half a step is 2^-12), from fp32 queries to a sum of two fp16.
+// All sums are fp32.
+//
+// The work is cut into units of 32 keys of one item, an item being up to kRows rows of one
+// sequence and K/V head.  Every workgroup takes an equal run of units, whatever items they
+// are of: a batch of unequal lengths, and causal rows, leave no workgroup behind.  Items that
+// end up in several workgroups leave partial results in the workspace, which a second kernel
+// joins in the order of the keys.
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "cf.h"
+#include "cf_internal.h"
+#include "cf_kv4.h"
+#include "cf_rows.h"
+
+namespace cf {
+namespace {
+
+typedef _Float16 vh2 __attribute__((ext_vector_type(2)));
+typedef _Float16 vh8 __attribute__((ext_vector_type(8)));
+typedef uint32_t vu4 __attribute__((ext_vector_type(4)));
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+constexpr int kUnit = 32;  // keys
+// Workgroups of a call: what is resident on 256 compute units, more where a workgroup's
+// registers allow it.
+constexpr int kGroupsSmall = 1024, kGroupsLarge = 256;
+// A workgroup takes at least so many units, or joining would cost more than it saves.
+constexpr int kMinUnits = 8;
+// p = 2^(x - m + kLift) where m is at most kSlack below the row's largest score so far: the
+// reference moves, and O is rescaled, only when a score exceeds it by more.  p stays below
+// 2^(kLift + kSlack) < 65504, and the lift keeps the fp16 of small p off the subnormals.
+constexpr float kLift = 7.f, kSlack = 8.f;
+constexpr float kNone = -__builtin_inff();
+
+struct AttnArgs {
+    RowSet q, out;
+    KvCache cache;
+    const int32_t* table;
+    int width;  // pages of a table row
+    const int32_t* kv_lens;
+    const int32_t* q_starts;  // or null: rows_each queries for each sequence
+    int64_t total_q, q_each;
+    int batch, q_heads, share;  // share: query heads of a K/V head
+    int causal, window;
+    float scale_log2;
+    float* lse;
+    float* part;    // partial O, m and sum
+    int32_t* joins; // what each workgroup leaves to be joined
+    int groups;
+};
+
+// What an item's rows have to be joined from, written by the workgroup with its last keys.
+struct Join {
+    int32_t first;      // workgroup with its first keys; -1: nothing to join
+    int32_t batch, head, tile;
+};
+
+// One sequence's rows and keys.
+struct Seq {
+    int64_t q0;
+    int64_t len;  // keys
+    int64_t nq;   // query tokens
+    __device__ __forceinline__ int64_t offset() const { return len - nq; }
+};
+
+__device__ __forceinline__ Seq seq_of(const AttnArgs& p, int b) {
+    Seq s;
+    int64_t len = p.kv_lens[b];
+    const int64_t most = int64_t(p.width) << p.cache.shift;
+    s.len = len < 0 ? 0 : len > most ? most : len;
+    if (p.q_starts) {
+        int64_t lo = p.q_starts[b], hi = p.q_starts[b + 1];
+        lo = lo < 0 ? 0 : lo > p.total_q ? p.total_q : lo;
+        hi = hi < lo ? lo : hi > p.total_q ? p.total_q : hi;
+        s.q0 = lo;
+        s.nq = hi - lo;
+    } else {
+        s.q0 = b * p.q_each;
+        s.nq = p.q_each;
+    }
+    return s;
+}
+
+// Keys [lo, hi) that a query token sees.
+__device__ __forceinline__ void seen(const AttnArgs& p, const Seq& s, int64_t token, int64_t* lo, int64_t* hi) {
+    *lo = 0;
+    *hi = s.len;
+    if (p.causal) {
+        const int64_t at = s.offset() + token;
+        *hi = at + 1 < s.len ? at + 1 : s.len;
+        if (p.window && at - p.window + 1 > 0) *lo = at - p.window + 1;
+    }
+}
+
+// Units [u0, u0 + n) of the item with rows [r0, r1); at least one, so that rows that see
+// nothing are written too.
+template <int ROWS>
+__device__ __forceinline__ int units_of(const AttnArgs& p, const Seq& s, int64_t tile, int* u0) {
+    const int64_t r0 = tile * ROWS, rows = s.nq * p.share;
+    const int64_t r1 = r0 + ROWS < rows ? r0 + ROWS : rows;
+    int64_t lo, hi, x;
+    seen(p, s, r0 / p.share, &lo, &x);
+    seen(p, s, (r1 - 1) / p.share, &x, &hi);
+    *u0 = static_cast<int>(lo / kUnit);
+    const int64_t end = (hi + kUnit - 1) / kUnit;
+    return end > *u0 ? static_cast<int>(end - *u0) : 1;
+}
+
+template <int ROWS>
+__device__ __forceinline__ int64_t tiles_of(const AttnArgs& p, const Seq& s) {
+    return (s.nq * p.share + ROWS - 1) / ROWS;
+}
+
+// Units of one K/V head of a sequence.
+template <int ROWS>
+__device__ int64_t head_units(const AttnArgs& p, const Seq& s) {
+    const int64_t tiles = tiles_of<ROWS>(p, s);
+    int u0;
+    if (tiles == 0) return 0;
+    if (!p.causal) return tiles * units_of<ROWS>(p, s, 0, &u0);
+    int64_t n = 0;
+    for (int64_t i = 0; i < tiles; ++i) n += units_of<ROWS>(p, s, i, &u0);
+    return n;
+}
+
+// v over the lanes n, n + 16, n + 32, n + 48 that hold a row.
+__device__ __forceinline__ float across_max(float v) {
+    v = fmaxf(v, __shfl_xor(v, 16, 64));
+    return fmaxf(v, __shfl_xor(v, 32, 64));
+}
+__device__ __forceinline__ float across_sum(float v) {
+    v += __shfl_xor(v, 16, 64);
+    return v + __shfl_xor(v, 32, 64);
+}
+
+// bf16 pair of byte B of codes c.
+template <int B>
+__device__ __forceinline__ uint32_t to_bf16(uint32_t c, float s) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, B));
+}
+template <int B>
+__device__ __forceinline__ uint32_t to_f16(uint32_t c, float s) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, s, B));
+}
+
+__device__ __forceinline__ float scale_of(uint32_t byte) { return __uint_as_float(byte << 23); }
+
+// One wave's share of 32 keys, as loaded.
+template <int D>
+struct Keys {
+    uint32_t k[2][D / 32];  // two rows of keys, a quarter of the channels each
+    uint32_t ks[2];         // their scale bytes
+    uint32_t v[D / 16];     // eight keys of a channel piece
+    uint32_t vs[2];         // their scale bytes
+    bool ok;                // the lane's eight V keys have a page
+};
+
+template <int D>
+__device__ __forceinline__ void load_keys(Keys<D>& x, const AttnArgs& p, const Seq& s, int b, int head, int unit) {
+    const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+    const KvBlock blk{p.cache.block.page, D};
+    const int mask = blk.page - 1;
+    const int last = s.len > 0 ? static_cast<int>(s.len - 1) : 0;
+    // keys behind the last are read from its page (and masked later): always inside the cache
+    const auto page_of = [&](int key, bool* ok) -> int64_t {
+        int64_t at = -1;
+        if (s.len > 0) {
+            at = int64_t(b) * p.width + (min(key, last) >> p.cache.shift);
+            if (p.table) at = p.table[at];
+        }
+        *ok = at >= 0 && at < p.cache.pages;
+        return *ok ? at : 0;
+    };
+    bool ok;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int key = unit * kUnit + 8 * (n >> 2) + (n & 3) + 4 * h;
+        const uint8_t* const base = p.cache.at(page_of(key, &ok), head);
+        const uint8_t* const c = base + blk.k_code(key & mask) + g * (D / 8);
+        if constexpr (D == 128) {
+            const vu4 w = *reinterpret_cast<const vu4*>(c);
+            x.k[h][0] = w.x, x.k[h][1] = w.y, x.k[h][2] = w.z, x.k[h][3] = w.w;
+        } else {
+            const vu2 w = *reinterpret_cast<const vu2*>(c);
+            x.k[h][0] = w.x, x.k[h][1] = w.y;
+        }
+        x.ks[h] = base[blk.k_scale(key & mask, g * (D / 4) / kKvGroup)];
+    }
+    const int key = unit * kUnit + 8 * g;
+    const uint8_t* const base = p.cache.at(page_of(key, &x.ok), head);
+    const uint8_t* const c = base + blk.v_code(key & mask, n);
+#pragma unroll
+    for (int i = 0; i < D / 16; i += 4) {
+        const vu4 w = *reinterpret_cast<const vu4*>(c + 4 * i);
+        x.v[i] = w.x, x.v[i + 1] = w.y, x.v[i + 2] = w.z, x.v[i + 3] = w.w;
+    }
+    const vu2 w = *reinterpret_cast<const vu2*>(base + blk.v_scale(key & mask, n * (D / 16) / kKvGroup));
+    x.vs[0] = w.x, x.vs[1] = w.y;
+}
+
+// Queries of 16 rows: bf16 parts that add up to them, channel order as in K's codes.
+template <int D, int PARTS>
+struct Rows {
+    vb8 q[PARTS][D / 32];
+};
+
+template <typename T, int D, int PARTS>
+__device__ __forceinline__ void load_rows(Rows<D, PARTS>& x, const AttnArgs& p, const Seq& s, int head, int64_t row,
+                                          bool on) {
+    const int g = (threadIdx.x & 63) >> 4;
+    const int64_t token = on ? row / p.share : 0;
+    const T* const q = row_ptr<T>(p.q, s.q0 + token, head * p.share + static_cast<int>(on ? row - token * p.share : 0));
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+        float f[8];
+        Row8<T> r;
+        if (on) {
+            r.load(q + g * (D / 4) + 8 * i);
+            r.get(f);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float rest = on ? f[j] : 0.f;
+#pragma unroll
+            for (int k = 0; k < PARTS; ++k) {
+                const __bf16 h = static_cast<__bf16>(rest);
+                x.q[k][i][j] = h;
+                rest -= static_cast<float>(h);
+            }
+        }
+    }
+}
+
+// PARTS: bf16 parts of a query (1 or 3); PP: fp16 parts of a probability.  NQ: sixteens of
+// rows a wave holds.  SPLIT: the four waves share the item's rows and split its units;
+// otherwise each has rows of its own.
+template <typename T, int D, int NQ, bool SPLIT>
+struct Shape {
+    static constexpr int kParts = sizeof(T) == 4 ? 3 : 1;
+    static constexpr int kP = sizeof(T) == 4 ? 2 : 1;
+    static constexpr int kRows = 16 * NQ * (SPLIT ? 1 : kWaves);
+};
+
+// Floats of one partial result: rows x (D values, the reference, the sum).
+template <int D>
+__host__ __device__ constexpr int64_t part_floats(int rows) {
+    return int64_t(rows) * (D + 2);
+}
+
+template <typename T>
+__device__ __forceinline__ void store_out(T* o, const float (&x)[8]) {
+    Row8<T> r;
+    r.set(x);
+    r.store(o);
+}
+
+template <typename T, int D, int NQ, bool SPLIT>
+__global__ __launch_bounds__(kThreads, NQ == 1 ? 2 : 1) void attn_kernel(const AttnArgs p) {
+    using S = Shape<T, D, NQ, SPLIT>;
+    constexpr int kRows = S::kRows, kParts = S::kParts, kP = S::kP;
+    constexpr int kJ = D / 16;  // O^T tiles of 16 channel pieces
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
+    // neighbours in the order of the work share keys: let them share an XCD's L2
+    const int me = (blockIdx.x & 7) * (p.groups >> 3) + (blockIdx.x >> 3);
+
+    __shared__ int64_t scan[kThreads];
+    __shared__ int64_t found[2];
+    __shared__ float stage[SPLIT ? kWaves * 16 * (D + 4) : 1];
+    __shared__ float stage_m[SPLIT ? kWaves * 16 : 1], stage_l[SPLIT ? kWaves * 16 : 1];
+
+    // total units, and a workgroup's run of them
+    int64_t mine = 0;
+    for (int b = threadIdx.x; b < p.batch; b += kThreads) mine += head_units<kRows>(p, seq_of(p, b)) * p.cache.heads;
+    scan[threadIdx.x] = mine;
+    __syncthreads();
+    for (int d = kThreads / 2; d > 0; d >>= 1) {
+        if (threadIdx.x < d) scan[threadIdx.x] += scan[threadIdx.x + d];
+        __syncthreads();
+    }
+    const int64_t total = scan[0];
+    int64_t chunk = (total + p.groups - 1) / p.groups;
+    chunk = chunk < kMinUnits ? kMinUnits : chunk;
+    int64_t at = me * chunk;
+    const int64_t end = at + chunk < total ? at + chunk : total;
+    if (threadIdx.x == 0) p.joins[me * 4] = -1;
+    if (at >= end) return;
+
+    // the sequence of the first unit
+    int64_t before = 0;
+    for (int b0 = 0;; b0 += kThreads) {
+        __syncthreads();
+        const int b = b0 + threadIdx.x;
+        const int64_t own = b < p.batch ? head_units<kRows>(p, seq_of(p, b)) * p.cache.heads : 0;
+        scan[threadIdx.x] = own;
+        __syncthreads();
+        for (int d = 1; d < kThreads; d <<= 1) {
+            const int64_t x = threadIdx.x >= d ? scan[threadIdx.x - d] : 0;
+            __syncthreads();
+            scan[threadIdx.x] += x;
+            __syncthreads();
+        }
+        const int64_t hi = before + scan[threadIdx.x], lo = hi - own;
+        if (at >= lo && at < hi) found[0] = b, found[1] = lo;
+        const int64_t all = before + scan[kThreads - 1];
+        __syncthreads();
+        if (at < all) break;  // total > at, so some round gets here
+        before = all;
+    }
+    int b = static_cast<int>(found[0]);
+    Seq s = seq_of(p, b);
+    int64_t per_head = head_units<kRows>(p, s);
+    int64_t rest = at - found[1];
+    int head = static_cast<int>(rest / per_head);
+    rest -= head * per_head;
+    int64_t tile = 0;
+    int u0, count;
+    for (;; ++tile) {
+        count = units_of<kRows>(p, s, tile, &u0);
+        if (rest < count) break;
+        rest -= count;
+    }
+
+    while (at < end) {
+        // units [a, z) of this item
+        const int a = static_cast<int>(rest);
+        const int z = count - a < end - at ? count : a + static_cast<int>(end - at);
+        const int64_t rows = s.nq * p.share;
+        const int64_t row0 = tile * kRows + (SPLIT ? 0 : wave * 16 * NQ);
+
+        Rows<D, kParts> q[NQ];
+        int lo[NQ], hi[NQ];                   // keys that row n of each sixteen sees
+        int full_lo = 0, full_hi = INT32_MAX; // keys that all of the wave's rows see
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) {
+            const int64_t row = row0 + i * 16 + n;
+            const bool on = row < rows;
+            load_rows<T, D, kParts>(q[i], p, s, head, row, on);
+            int64_t l = 0, h = 0;
+            if (on) seen(p, s, row / p.share, &l, &h);
+            lo[i] = static_cast<int>(l);
+            hi[i] = h > 0 ? static_cast<int>(h) : 0;
+            int fl = on ? lo[i] : 0, fh = on ? hi[i] : INT32_MAX;
+#pragma unroll
+            for (int d = 1; d < 16; d <<= 1) {
+                fl = max(fl, __shfl_xor(fl, d, 64));
+                fh = min(fh, __shfl_xor(fh, d, 64));
+            }
+            full_lo = max(full_lo, fl);
+            full_hi = min(full_hi, fh);
+        }
+
+        vf4 o[NQ][kJ];
+        float m[NQ], sum[NQ];  // m: reference in units of log2, raised by kLift
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) {
+            m[i] = kNone, sum[i] = 0.f;
+#pragma unroll
+            for (int j = 0; j < kJ; ++j) o[i][j] = vf4{0.f, 0.f, 0.f, 0.f};
+        }
+
+        constexpr int kStep = SPLIT ? kWaves : 1;
+        const int first = a + (SPLIT ? wave : 0);
+        Keys<D> next;
+        if (first < z) load_keys<D>(next, p, s, b, head, u0 + first);
+        for (int u = first; u < z; u += kStep) {
+            Keys<D> x = next;
+            if (u + kStep < z) load_keys<D>(next, p, s, b, head, u0 + u + kStep);
+            const int key0 = (u0 + u) * kUnit;
+            // the lane's own eight keys
+            const int mine0 = key0 + 8 * g;
+            const bool edge = __any(key0 < full_lo || key0 + kUnit > full_hi || !x.ok);
+            uint32_t bad = 0;  // V groups of the lane's keys that read NaN, a bit a key
+            uint32_t kbad[2] = {0, 0};
+            if (edge) {
+                // V behind the sequence's last key is whatever an earlier owner of the page left
+#pragma unroll
+                for (int t = 0; t < 8; ++t) {
+                    if (x.ok && mine0 + t < s.len) continue;
+                    if constexpr (D == 128)
+                        x.v[t] = 0;
+                    else
+                        x.v[t / 2] &= t & 1 ? 0xffffu : 0xffff0000u;
+                    x.vs[t / 4] = (x.vs[t / 4] & ~(0xffu << (8 * (t & 3)))) | 127u << (8 * (t & 3));
+                }
+            }
+            const uint32_t odd = (x.vs[0] & x.vs[0] << 1) | (x.vs[1] & x.vs[1] << 1);
+            const bool nans = __any((odd & 0x80808080u) != 0 || max(x.ks[0], x.ks[1]) >= kKvNanFrom);
+            if (nans) {
+#pragma unroll
+                for (int t = 0; t < 8; ++t) {
+                    const uint32_t byte = (x.vs[t / 4] >> (8 * (t & 3))) & 0xffu;
+                    if (byte < kKvNanFrom) continue;
+                    bad |= 1u << t;
+                    x.vs[t / 4] = (x.vs[t / 4] & ~(0xffu << (8 * (t & 3)))) | 127u << (8 * (t & 3));
+                    if constexpr (D == 128)
+                        x.v[t] = 0;
+                    else
+                        x.v[t / 2] &= t & 1 ? 0xffffu : 0xffff0000u;
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint64_t w = __ballot(x.ks[h] >= kKvNanFrom);
+                    kbad[h] = static_cast<uint32_t>((w | w >> 16 | w >> 32 | w >> 48) & 0xffffu);
+                }
+            }
+
+            // scores: sc[i][t] is key mine0 + t, row n of the i-th sixteen
+            vf4 sc[NQ][2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float ks = scale_of(x.ks[h]);
+                vb8 kf[D / 32];
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    const vu4 w{to_bf16<0>(x.k[h][c], ks), to_bf16<1>(x.k[h][c], ks), to_bf16<2>(x.k[h][c], ks),
+                                to_bf16<3>(x.k[h][c], ks)};
+                    kf[c] = __builtin_bit_cast(vb8, w);
+                }
+#pragma unroll
+                for (int i = 0; i < NQ; ++i) {
+                    vf4 acc{0.f, 0.f, 0.f, 0.f};
+                    // the smallest parts first
+#pragma unroll
+                    for (int k = kParts - 1; k >= 0; --k)
+#pragma unroll
+                        for (int c = 0; c < D / 32; ++c)
+                            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[c], q[i].q[k][c], acc, 0, 0, 0);
+                    sc[i][h] = acc;
+                }
+            }
+
+            vh8 pf[NQ][kP];
+#pragma unroll
+            for (int i = 0; i < NQ; ++i) {
+                float w[8];
+#pragma unroll
+                for (int t = 0; t < 8; ++t) w[t] = sc[i][t >> 2][t & 3] * p.scale_log2;
+                uint32_t see = 0xff;
+                if (nans) {
+#pragma unroll
+                    for (int t = 0; t < 8; ++t)
+                        if (kbad[t >> 2] >> (4 * g + (t & 3)) & 1u) w[t] = __builtin_nanf("");
+                }
+                if (edge) {
+#pragma unroll
+                    for (int t = 0; t < 8; ++t)
+                        if (!x.ok || mine0 + t < lo[i] || mine0 + t >= hi[i]) w[t] = kNone, see &= ~(1u << t);
+                }
+                float top = kNone;
+#pragma unroll
+                for (int t = 0; t < 8; ++t) top = fmaxf(top, w[t]);
+                if (__any(top > m[i] + (kSlack + kLift))) {
+                    // the lanes of a row agree on its new reference
+                    const float r = fmaxf(across_max(top) - kLift, m[i]);
+                    const float f = m[i] == r ? 1.f : __builtin_amdgcn_exp2f(m[i] - r);
+                    m[i] = r;
+                    sum[i] *= f;
+#pragma unroll
+                    for (int j = 0; j < kJ; ++j) o[i][j] *= f;
+                }
+                const float ref = m[i] == kNone ? 0.f : m[i];
+#pragma unroll
+                for (int t = 0; t < 8; ++t) {
+                    w[t] = __builtin_amdgcn_exp2f(w[t] - ref);
+                    sum[i] += w[t];
+                    const _Float16 h = static_cast<_Float16>(w[t]);
+                    pf[i][0][t] = h;
+                    if constexpr (kP == 2) pf[i][1][t] = static_cast<_Float16>(w[t] - static_cast<float>(h));
+                }
+                if (nans) {
+                    // a NaN of V reaches the rows that see its key, and only those
+                    uint32_t hit = 0;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t bv = __shfl(static_cast<int>(bad), 16 * k + (D == 128 ? 4 * g : 8 * (g >> 1)), 64);
+                        hit |= bv & static_cast<uint32_t>(__shfl(static_cast<int>(see), 16 * k + n, 64));
+                    }
+                    if (hit)
+#pragma unroll
+                        for (int j = 0; j < kJ; ++j) o[i][j] = vf4{1.f, 1.f, 1.f, 1.f} * __builtin_nanf("");
+                }
+            }
+
+            float vs[8];
+#pragma unroll
+            for (int t = 0; t < 8; ++t) vs[t] = scale_of((x.vs[t / 4] >> (8 * (t & 3))) & 0xffu);
+            const auto pv = [&](int j, const uint32_t (&c)[8]) {
+                // c: channel pairs 2j, 2j + 1 of the eight keys
+                vu4 even, odd_;
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    even[t] = __builtin_amdgcn_perm(c[2 * t + 1], c[2 * t], 0x05040100u);
+                    odd_[t] = __builtin_amdgcn_perm(c[2 * t + 1], c[2 * t], 0x07060302u);
+                }
+#pragma unroll
+                for (int i = 0; i < NQ; ++i)
+#pragma unroll
+                    for (int k = kP - 1; k >= 0; --k) {
+                        o[i][2 * j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(vh8, even), pf[i][k],
+                                                                            o[i][2 * j], 0, 0, 0);
+                        o[i][2 * j + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(vh8, odd_),
+                                                                                pf[i][k], o[i][2 * j + 1], 0, 0, 0);
+                    }
+            };
+            if constexpr (D == 128) {
+                uint32_t c[8];
+#pragma unroll
+                for (int t = 0; t < 8; ++t) c[t] = to_f16<0>(x.v[t], vs[t]);
+                pv(0, c);
+#pragma unroll
+                for (int t = 0; t < 8; ++t) c[t] = to_f16<1>(x.v[t], vs[t]);
+                pv(1, c);
+#pragma unroll
+                for (int t = 0; t < 8; ++t) c[t] = to_f16<2>(x.v[t], vs[t]);
+                pv(2, c);
+#pragma unroll
+                for (int t = 0; t < 8; ++t) c[t] = to_f16<3>(x.v[t], vs[t]);
+                pv(3, c);
+            } else {
+                uint32_t c[8];
+#pragma unroll
+                for (int t = 0; t < 8; ++t)
+                    c[t] = t & 1 ? to_f16<2>(x.v[t / 2], vs[t]) : to_f16<0>(x.v[t / 2], vs[t]);
+                pv(0, c);
+#pragma unroll
+                for (int t = 0; t < 8; ++t)
+                    c[t] = t & 1 ? to_f16<3>(x.v[t / 2], vs[t]) : to_f16<1>(x.v[t / 2], vs[t]);
+                pv(1, c);
+            }
+        }
+
+        // this segment's results: the whole item, or a part for the second kernel
+        const bool whole = a == 0 && z == count;
+        float* const part = p.part + (2 * int64_t(me) + (a == 0)) * part_floats<D>(kRows);
+        const auto put = [&](int r, int c, float (&v)[8], float top, float l, bool first_piece) {
+            // eight channels from c of row r of the item
+            const int64_t row = tile * kRows + r;
+            if (row >= rows) return;
+            if (whole) {
+                const int64_t token = row / p.share;
+                const int qh = head * p.share + static_cast<int>(row - token * p.share);
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] *= inv;
+                store_out<T>(row_ptr<T>(p.out, s.q0 + token, qh) + c, v);
+                if (p.lse && first_piece)
+                    p.lse[(s.q0 + token) * p.q_heads + qh] =
+                        l == 0.f ? kNone : (top + __builtin_amdgcn_logf(l)) * 0.693147180559945309f;
+            } else {
+                float* const w = part + int64_t(r) * (D + 2);
+#pragma unroll
+                for (int k = 0; k < 8; k += 2) *reinterpret_cast<float2*>(w + c + k) = float2{v[k], v[k + 1]};
+                if (first_piece) *reinterpret_cast<float2*>(w + D) = float2{top, l};
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) {
+            sum[i] = across_sum(sum[i]);
+            if constexpr (!SPLIT) {
+                // a lane has D/4 consecutive channels of its row
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    float v[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) v[k] = o[i][(8 * c + k) % kJ][(8 * c + k) / kJ];
+                    put(wave * 16 * NQ + i * 16 + n, g * (D / 4) + 8 * c, v, m[i], sum[i], g == 0 && c == 0);
+                }
+            } else {
+                __syncthreads();
+                float* const w = stage + (wave * 16 + n) * (D + 4) + g * (D / 4);
+#pragma unroll
+                for (int c = 0; c < D / 4; c += 4)
+                    *reinterpret_cast<vf4*>(w + c) = vf4{o[i][c % kJ][c / kJ], o[i][(c + 1) % kJ][(c + 1) / kJ],
+                                                         o[i][(c + 2) % kJ][(c + 2) / kJ], o[i][(c + 3) % kJ][(c + 3) / kJ]};
+                if (g == 0) stage_m[wave * 16 + n] = m[i], stage_l[wave * 16 + n] = sum[i];
+                __syncthreads();
+                for (int x = threadIdx.x; x < 16 * (D / 8); x += kThreads) {
+                    const int r = x / (D / 8), c = x % (D / 8) * 8;
+                    float top = kNone;
+#pragma unroll
+                    for (int k = 0; k < kWaves; ++k) top = fmaxf(top, stage_m[k * 16 + r]);
+                    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, l = 0.f;
+#pragma unroll
+                    for (int k = 0; k < kWaves; ++k) {
+                        const float f = stage_m[k * 16 + r] == kNone ? 0.f
+                                                                     : __builtin_amdgcn_exp2f(stage_m[k * 16 + r] - top);
+                        // a wave without a reference has only zeros, or NaN that must show
+                        const float* const y = stage + (k * 16 + r) * (D + 4) + c;
+                        l = __builtin_fmaf(stage_l[k * 16 + r], f, l);
+#pragma unroll
+                        for (int d = 0; d < 8; ++d) v[d] = __builtin_fmaf(y[d], f, v[d]);
+                    }
+                    put(i * 16 + r, c, v, top, l, c == 0);
+                }
+            }
+        }
+        if (threadIdx.x == 0 && a > 0 && z == count) {
+            // units before this item: at - a
+            int32_t* const j = p.joins + me * 4;
+            j[1] = b, j[2] = head, j[3] = static_cast<int32_t>(tile);
+            j[0] = static_cast<int32_t>((at - a) / chunk);
+        }
+
+        // on to the next item
+        at += z - a;
+        rest = 0;
+        if (at >= end) break;
+        ++tile;
+        if (tile >= tiles_of<kRows>(p, s)) {
+            tile = 0;
+            if (++head >= p.cache.heads) {
+                head = 0;
+                do s = seq_of(p, ++b);  // at < end <= total: another sequence has units
+                while (s.nq == 0);
+            }
+        }
+        count = units_of<kRows>(p, s, tile, &u0);
+    }
+}
+
+// Joins the parts of the items that ended up in several workgroups: block (w, y) the rows
+// 8y .. of the item whose last keys were workgroup w's.
+template <typename T, int D, int ROWS>
+__global__ __launch_bounds__(kThreads) void join_kernel(const AttnArgs p) {
+    const int me = blockIdx.x;
+    const int first = p.joins[me * 4];
+    if (first < 0) return;
+    const int b = p.joins[me * 4 + 1], head = p.joins[me * 4 + 2], tile = p.joins[me * 4 + 3];
+    const Seq s = seq_of(p, b);
+    constexpr int kLanes = D / 4;
+    const int r = blockIdx.y * (kThreads / kLanes) + threadIdx.x / kLanes, c = threadIdx.x % kLanes * 4;
+    const int64_t row = int64_t(tile) * ROWS + r;
+    if (r >= ROWS || row >= s.nq * p.share) return;
+    const auto part = [&](int w) {
+        return p.part + (2 * int64_t(w) + (w == first)) * part_floats<D>(ROWS) + int64_t(r) * (D + 2);
+    };
+    float top = kNone;
+    for (int w = first; w <= me; ++w) top = fmaxf(top, part(w)[D]);
+    float v[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f;
+    for (int w = first; w <= me; ++w) {
+        const float* const x = part(w);
+        const float f = x[D] == kNone ? 0.f : __builtin_amdgcn_exp2f(x[D] - top);
+        l = __builtin_fmaf(x[D + 1], f, l);
+        const float2 a = *reinterpret_cast<const float2*>(x + c), d = *reinterpret_cast<const float2*>(x + c + 2);
+        v[0] = __builtin_fmaf(a.x, f, v[0]);
+        v[1] = __builtin_fmaf(a.y, f, v[1]);
+        v[2] = __builtin_fmaf(d.x, f, v[2]);
+        v[3] = __builtin_fmaf(d.y, f, v[3]);
+    }
+    const int64_t token = row / p.share;
+    const int qh = head * p.share + static_cast<int>(row - token * p.share);
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    T* const o = row_ptr<T>(p.out, s.q0 + token, qh) + c;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[k] = static_cast<T>(v[k] * inv);
+    if (p.lse && c == 0)
+        p.lse[(s.q0 + token) * p.q_heads + qh] =
+            l == 0.f ? kNone : (top + __builtin_amdgcn_logf(l)) * 0.693147180559945309f;
+}
+
+struct Plan {
+    int rows, groups;
+    size_t bytes;
+};
+
+// The kernel for a call: rows is the number of rows that the longest sequence has.
+Plan plan_of(int a_dtype, int head_dim, int64_t rows) {
+    const int large = a_dtype == CF_F32 ? 128 : 256;
+    Plan x;
+    x.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : large;
+    x.groups = x.rows == 16 ? kGroupsSmall : x.rows == 32 ? kGroupsSmall / 2 : kGroupsLarge;
+    const int64_t floats = head_dim == 64 ? part_floats<64>(x.rows) : part_floats<128>(x.rows);
+    x.bytes = size_t(x.groups) * (2 * floats * 4 + 16);
+    return x;
+}
+
+template <typename T, int D, int NQ, bool SPLIT>
+hipError_t launch(const AttnArgs& p, hipStream_t stream) {
+    constexpr int kRows = Shape<T, D, NQ, SPLIT>::kRows, kJoinRows = kThreads / (D / 4);
+    attn_kernel<T, D, NQ, SPLIT><<<p.groups, kThreads, 0, stream>>>(p);
+    if (hipError_t e = hipGetLastError()) return e;
+    join_kernel<T, D, kRows><<<dim3(p.groups, (kRows + kJoinRows - 1) / kJoinRows), kThreads, 0, stream>>>(p);
+    return hipGetLastError();
+}
+
+template <typename T, int D>
+hipError_t launch_rows(int rows, const AttnArgs& p, hipStream_t stream) {
+    constexpr int kWide = sizeof(T) == 4 ? 2 : 4;
+    if (rows == 16) return launch<T, D, 1, true>(p, stream);
+    if (rows == 32) return launch<T, D, 2, true>(p, stream);
+    return launch<T, D, kWide, false>(p, stream);
+}
+
+}  // namespace
+
+size_t kv4_attention_workspace(int a_dtype, int head_dim, int64_t max_rows) {
+    return plan_of(a_dtype, head_dim, max_rows).bytes;
+}
+
+hipError_t launch_kv4_attention(int a_dtype, const Kv4Attention& c, void* workspace, hipStream_t stream) {
+    const int share = c.q_heads / c.cache.heads;
+    const Plan x = plan_of(a_dtype, c.cache.block.dim, c.max_q * share);
+    AttnArgs p{};
+    p.q = c.q, p.out = c.out, p.cache = c.cache, p.table = c.table, p.width = c.table_width;
+    p.kv_lens = c.kv_lens, p.q_starts = c.q_starts, p.total_q = c.total_q;
+    p.q_each = c.q_starts ? 0 : c.total_q / c.batch;
+    p.batch = c.batch, p.q_heads = c.q_heads, p.share = share;
+    p.causal = c.causal, p.window = c.window;
+    p.scale_log2 = c.scale * 1.44269504088896341f;
+    p.lse = c.lse;
+    p.groups = x.groups;
+    p.joins = static_cast<int32_t*>(workspace);
+    p.part = reinterpret_cast<float*>(p.joins + 4 * x.groups);
+    const bool d64 = c.cache.block.dim == 64;
+    if (a_dtype == CF_BF16)
+        return d64 ? launch_rows<__bf16, 64>(x.rows, p, stream) : launch_rows<__bf16, 128>(x.rows, p, stream);
+    return d64 ? launch_rows<float, 64>(x.rows, p, stream) : launch_rows<float, 128>(x.rows, p, stream);
+}
+
+}  // namespace cf

@@ -247,6 +247,128 @@ int cf_lowrank_compress_noalloc(int a_dtype, const void* a, float* ahat, float* 
                                 int rank, int iters, int factor_bits, int batch, float* q_state, void* u,
                                 float* u_scales, void* v, float* v_scales, void* stream);
 
+/*
+ * Attention operators beside the compressors: what makes the queries and keys (their
+ * norms and position rotation), what keeps K and V in 4 bits, and what reads them.
+ *
+ * Rows of heads.  These entry points take activations of heads as cf_rows: row (t, h) of
+ * token t and head h is head_dim consecutive elements from data + t * token_stride +
+ * h * head_stride (strides in elements), so slices of a packed projection and head-major
+ * layouts pass without a copy.  Every row starts on 16 bytes (CF_E_ALIGN otherwise).
+ * Strides are not negative; rows that are written must not overlap each other: either
+ * head_stride >= head_dim and token_stride >= the heads' extent, or the reverse
+ * (CF_E_SHAPE).  tokens = 0 is a valid call that does nothing.
+ */
+typedef struct cf_rows {
+    void* data;
+    int64_t token_stride, head_stride;
+} cf_rows;
+
+/* Norms of cf_qk_norm_rope, and its rotation's pairs. */
+enum { CF_NORM_NONE = 0, CF_NORM_RMS = 1, CF_NORM_LAYER = 2 };
+enum { CF_ROPE_NONE = 0, CF_ROPE_INTERLEAVED = 1, CF_ROPE_HALF = 2 };
+
+/*
+ * Norms of queries and keys for each head, with the position rotation in the same pass.
+ * Per row x of D = head_dim channels, in fp32, rounded once to a_dtype at the end:
+ *   CF_NORM_NONE   n = x
+ *   CF_NORM_RMS    n = x / sqrt(mean(x^2) + eps)
+ *   CF_NORM_LAYER  n = (x - mean(x)) / sqrt(mean((x - mean(x))^2) + eps)
+ *   y = n * weight + bias  (head_dim fp32 each; NULL = ones / zeros)
+ *   the first rot_dim channels of y in pairs (i, j), pair p by the angle whose cosine and
+ *   sine are cos[pos * rot_dim/2 + p] and sin[pos * rot_dim/2 + p]:
+ *     y_i cos - y_j sin,  y_j cos + y_i sin
+ *   CF_ROPE_INTERLEAVED (2p, 2p + 1);  CF_ROPE_HALF (p, p + rot_dim/2);
+ *   CF_ROPE_NONE rotates nothing and reads neither tables nor positions.
+ *   positions: tokens int32, or NULL = token t has position t (then tokens <= n_pos).  A
+ *     token with a negative position is padding: its rows in q_out and k_out stay as they
+ *     are.  A position of n_pos or more gives rows of NaN.
+ *   cos, sin: n_pos x rot_dim/2 fp32.
+ * head_dim a multiple of 8, at most 256; rot_dim a multiple of 16, at most head_dim; eps
+ * finite and not negative.  q_heads or k_heads may be 0 (that side's pointers are then not
+ * used).  In place (q_out the same rows as q, k_out as k) is allowed; any other overlap of an
+ * output with another operand is not.
+ *   weights, biases, cos, sin: 16-byte aligned; positions 4.
+ */
+int cf_qk_norm_rope(int a_dtype, int64_t tokens, int q_heads, int k_heads, int head_dim, const cf_rows* q,
+                    const cf_rows* k, const cf_rows* q_out, const cf_rows* k_out, int norm,
+                    const float* q_weight, const float* q_bias, const float* k_weight, const float* k_bias,
+                    float eps, int rope, const float* cos, const float* sin, int64_t n_pos, int rot_dim,
+                    const int32_t* positions, void* stream);
+
+/*
+ * The 4-bit K/V cache: `pages` pages of `page_size` tokens for each of kv_heads heads, in one
+ * buffer of cf_kv4_cache_bytes bytes.  head_dim D is 64 or 128; page_size P is 16, 32, 64, 128
+ * or 256.  The block of page p and head h starts at (p * kv_heads + h) * P * D * 17/16 and
+ * holds, in this order:
+ *   K codes   [P][D/2]                   low nibble first
+ *   V codes   [P/8][16][8 tokens][D/32]  piece n of 16: channels n*D/16 .. of each token
+ *   K scales  [P][D/32]                  a byte for each 32 channels
+ *   V scales  [P/8][D/32][8 tokens]
+ * A code is E2M1: bit 3 the sign, the rest indexes {0, .5, 1, 1.5, 2, 3, 4, 6}; it stands for
+ * that times 2^(byte - 127).  The writer takes, for each 32 channels of a row,
+ *   e = the least integer with max|x| <= 6 * 2^e, but within [-22, 13]; byte = e + 127;
+ *   code = the nearest to x * 2^-e, ties to the even code, 6 above 6
+ * (so magnitudes up to 6 * 2^13 are held with an error of at most 2^e, and beyond that they
+ * saturate).  A group with a NaN or an infinity gets byte 255 and reads as NaN.  Bytes the
+ * writer never makes: 192 and up read as NaN, the others give unspecified values.
+ *
+ * cf_kv4_append writes row t of k and v (tokens x kv_heads rows) to slot slots[t] = page *
+ * page_size + place; a slot that is negative or behind the cache takes nothing (padding).
+ * Two tokens with the same slot leave it with unspecified values.  cf_kv4_read reads the rows
+ * of slots back into k and v (bf16, rounded, which is exact; or fp32): rows of slots that
+ * are not in the cache become zero.
+ *   cache: 16-byte aligned; slots: tokens int64, 8-byte aligned.
+ */
+int64_t cf_kv4_cache_bytes(int64_t pages, int page_size, int kv_heads, int head_dim);
+
+int cf_kv4_append(int a_dtype, const cf_rows* k, const cf_rows* v, const int64_t* slots, int64_t tokens,
+                  uint8_t* cache, int64_t pages, int page_size, int kv_heads, int head_dim, void* stream);
+
+int cf_kv4_read(int a_dtype, const uint8_t* cache, int64_t pages, int page_size, int kv_heads, int head_dim,
+                const int64_t* slots, int64_t tokens, const cf_rows* k, const cf_rows* v, void* stream);
+
+/*
+ * Attention of ragged queries over the cache.  Sequence b has kv_lens[b] keys, token j of
+ * it in page table[b * table_width + j / page_size], and the query tokens q_starts[b] ..
+ * q_starts[b+1] - 1 of the total_q rows of q.  Query head h reads K/V head
+ * h / (q_heads / kv_heads).  Query i of a sequence with n queries and len keys sees key j
+ *   CF_ATTN_CAUSAL not set:  j < len
+ *   CF_ATTN_CAUSAL set:      j <= at, and with window > 0 also j > at - window,
+ *                            at = len - n + i (the queries are the last tokens)
+ *   out = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * q.k_j),  lse = log sum_j p_j
+ * A row that sees no key gives zeros, and lse = -infinity.  What lies in the cache behind a
+ * sequence's last key does not matter, whatever its bytes; a NaN reaches only the rows that
+ * see it.  A page outside the cache holds no keys.
+ *   q, out: total_q x q_heads rows of a_dtype;  lse: total_q x q_heads fp32, or NULL;
+ *   table: batch x table_width int32, or NULL: sequence b has the pages b * table_width and
+ *     on (batch * table_width <= pages);
+ *   kv_lens: batch int32; lengths are cut to [0, table_width * page_size];
+ *   q_starts: batch + 1 int32, or NULL: total_q / batch queries each, without a rest.  Rows of
+ *     out and lse that belong to no sequence stay as they are.
+ *   max_q: the most query tokens of a sequence, a bound that the caller knows (0: total_q).
+ *     It chooses the kernel and the workspace; the results are right for any lengths.
+ *   workspace: cf_kv4_attention_workspace_bytes, 256-byte aligned; nothing in it has to be
+ *     set before a call, and nothing is kept in it for the next.
+ * scale > 0; window >= 0, and 0 unless causal; q_heads a multiple of kv_heads, at most 65535;
+ * total_q * q_heads < 2^31, table_width * page_size < 2^31 - 256.
+ * K and V enter the products exactly.  bf16: queries exactly, probabilities rounded to fp16;
+ * fp32: queries exactly, probabilities to 22 bits.  Scores, sums and results are fp32 up to
+ * the final rounding to a_dtype.  Results are deterministic for given lengths; a row's last
+ * bits depend on the batch it is computed in, which is split into equal parts.
+ */
+enum { CF_ATTN_CAUSAL = 1 };
+
+int cf_kv4_attention(int a_dtype, const cf_rows* q, int64_t total_q, int q_heads, const uint8_t* cache,
+                     int64_t pages, int page_size, int kv_heads, int head_dim, int batch, const int32_t* table,
+                     int table_width, const int32_t* kv_lens, const int32_t* q_starts, int64_t max_q, int flags,
+                     int window, float scale, const cf_rows* out, float* lse, void* workspace, size_t ws_bytes,
+                     void* stream);
+
+/* Workspace bytes of cf_kv4_attention (0 for arguments outside the limits): max_q as there, or
+ * total_q where that is 0. */
+size_t cf_kv4_attention_workspace_bytes(int a_dtype, int64_t max_q, int q_heads, int kv_heads, int head_dim);
+
 /* Workspace bytes cf_lowrank_compress needs (0 for arguments outside the limits). */
 size_t cf_lowrank_workspace_bytes(int64_t m, int64_t n, int rank, int batch);
 
