@@ -63,8 +63,8 @@ struct AttnArgs {
     const int32_t* table;
     int width;  // pages of a table row
     const int32_t* kv_lens;
-    const int32_t* q_starts;  // or null: rows_each queries for each sequence
-    int64_t total_q, q_each;
+    const int32_t* q_starts;  // or null: q_each queries for each sequence
+    int total_q, q_each;
     int batch, q_heads, share;  // share: query heads of a K/V head
     int causal, window;
     float scale_log2;
@@ -74,78 +74,161 @@ struct AttnArgs {
     int groups;
 };
 
-// What an item's rows have to be joined from, written by the workgroup with its last keys.
-struct Join {
-    int32_t first;      // workgroup with its first keys; -1: nothing to join
-    int32_t batch, head, tile;
-};
-
 // One sequence's rows and keys.
 struct Seq {
-    int64_t q0;
-    int64_t len;  // keys
-    int64_t nq;   // query tokens
-    __device__ __forceinline__ int64_t offset() const { return len - nq; }
+    int q0, nq;  // query tokens
+    int len;     // keys
 };
 
-__device__ __forceinline__ Seq seq_of(const AttnArgs& p, int b) {
+// Loads through the scalar cache: the address is the same in every lane, and nothing writes there
+// while the kernel runs.
+__device__ __forceinline__ int32_t scalar_load(const int32_t* p) {
+    return *reinterpret_cast<const __attribute__((address_space(4))) int32_t*>(reinterpret_cast<uintptr_t>(p));
+}
+
+__device__ __forceinline__ Seq cut_seq(const AttnArgs& p, int len, int lo, int hi) {
     Seq s;
-    int64_t len = p.kv_lens[b];
-    const int64_t most = int64_t(p.width) << p.cache.shift;
-    s.len = len < 0 ? 0 : len > most ? most : len;
-    if (p.q_starts) {
-        int64_t lo = p.q_starts[b], hi = p.q_starts[b + 1];
-        lo = lo < 0 ? 0 : lo > p.total_q ? p.total_q : lo;
-        hi = hi < lo ? lo : hi > p.total_q ? p.total_q : hi;
-        s.q0 = lo;
-        s.nq = hi - lo;
-    } else {
-        s.q0 = b * p.q_each;
-        s.nq = p.q_each;
-    }
+    s.len = min(max(len, 0), p.width << p.cache.shift);
+    s.q0 = min(max(lo, 0), p.total_q);
+    s.nq = min(max(hi, s.q0), p.total_q) - s.q0;
     return s;
 }
 
-// Keys [lo, hi) that a query token sees.
-__device__ __forceinline__ void seen(const AttnArgs& p, const Seq& s, int64_t token, int64_t* lo, int64_t* hi) {
-    *lo = 0;
-    *hi = s.len;
-    if (p.causal) {
-        const int64_t at = s.offset() + token;
-        *hi = at + 1 < s.len ? at + 1 : s.len;
-        if (p.window && at - p.window + 1 > 0) *lo = at - p.window + 1;
-    }
+// b differs from lane to lane.
+__device__ __forceinline__ Seq seq_of(const AttnArgs& p, int b) {
+    const int len = p.kv_lens[b];
+    if (p.q_starts) return cut_seq(p, len, p.q_starts[b], p.q_starts[b + 1]);
+    return cut_seq(p, len, b * p.q_each, (b + 1) * p.q_each);
 }
 
-// Units [u0, u0 + n) of the item with rows [r0, r1); at least one, so that rows that see
-// nothing are written too.
+// b is the same in every lane.
+__device__ __forceinline__ Seq seq_at(const AttnArgs& p, int b) {
+    const int len = scalar_load(p.kv_lens + b);
+    if (p.q_starts) return cut_seq(p, len, scalar_load(p.q_starts + b), scalar_load(p.q_starts + b + 1));
+    return cut_seq(p, len, b * p.q_each, (b + 1) * p.q_each);
+}
+
+// Keys [lo, hi) that a query token sees; hi may be below lo.
+__device__ __forceinline__ int seen_lo(const AttnArgs& p, const Seq& s, int token) {
+    return p.window ? max(s.len - s.nq + token - p.window + 1, 0) : 0;
+}
+__device__ __forceinline__ int seen_hi(const AttnArgs& p, const Seq& s, int token) {
+    return p.causal ? min(s.len - s.nq + token + 1, s.len) : s.len;
+}
+
+// Row r of a sequence's rows for one K/V head: query token and query head.
+__device__ __forceinline__ int token_of(const AttnArgs& p, int row) {
+    return p.share == 1 ? row : static_cast<int>(static_cast<uint32_t>(row) / static_cast<uint32_t>(p.share));
+}
+
+// Units [u0, u0 + n) of an item; at least one, so that rows that see nothing are written too.
 template <int ROWS>
-__device__ __forceinline__ int units_of(const AttnArgs& p, const Seq& s, int64_t tile, int* u0) {
-    const int64_t r0 = tile * ROWS, rows = s.nq * p.share;
-    const int64_t r1 = r0 + ROWS < rows ? r0 + ROWS : rows;
-    int64_t lo, hi, x;
-    seen(p, s, r0 / p.share, &lo, &x);
-    seen(p, s, (r1 - 1) / p.share, &x, &hi);
-    *u0 = static_cast<int>(lo / kUnit);
-    const int64_t end = (hi + kUnit - 1) / kUnit;
-    return end > *u0 ? static_cast<int>(end - *u0) : 1;
+__device__ __forceinline__ int units_of(const AttnArgs& p, const Seq& s, int tile, int* u0) {
+    const int rows = s.nq * p.share;
+    const int lo = seen_lo(p, s, token_of(p, tile * ROWS));
+    const int hi = seen_hi(p, s, token_of(p, min(tile * ROWS + ROWS, rows) - 1));
+    *u0 = lo / kUnit;
+    return max((hi + kUnit - 1) / kUnit - *u0, 1);
 }
 
 template <int ROWS>
-__device__ __forceinline__ int64_t tiles_of(const AttnArgs& p, const Seq& s) {
+__device__ __forceinline__ int tiles_of(const AttnArgs& p, const Seq& s) {
     return (s.nq * p.share + ROWS - 1) / ROWS;
 }
 
-// Units of one K/V head of a sequence.
-template <int ROWS>
-__device__ int64_t head_units(const AttnArgs& p, const Seq& s) {
-    const int64_t tiles = tiles_of<ROWS>(p, s);
-    int u0;
-    if (tiles == 0) return 0;
-    if (!p.causal) return tiles * units_of<ROWS>(p, s, 0, &u0);
-    int64_t n = 0;
-    for (int64_t i = 0; i < tiles; ++i) n += units_of<ROWS>(p, s, i, &u0);
-    return n;
+__device__ __forceinline__ int64_t uniform(int64_t v) { return wave_uniform(v); }
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+__device__ __forceinline__ int64_t shfl64(int64_t v, int lane) {
+    const int lo = __shfl(static_cast<int>(v), lane, 64), hi = __shfl(static_cast<int>(v >> 32), lane, 64);
+    return static_cast<int64_t>(static_cast<uint64_t>(static_cast<uint32_t>(hi)) << 32 | static_cast<uint32_t>(lo));
+}
+
+// Inclusive sums over the wave's lanes.
+__device__ __forceinline__ int64_t wave_scan(int64_t v) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int64_t x = shfl64(v, lane - d);
+        if (lane >= d) v += x;
+    }
+    return v;
+}
+
+// Where a workgroup's run of the work begins, and its length.  An item costs its units and PAD
+// more: what starting and finishing one takes, in units.
+struct Place {
+    int64_t at, end, chunk;
+    int b, head, tile;
+    int64_t rest;  // of at, from the item's start
+};
+
+// Every wave works it out by itself: a group of lanes takes a sequence and shares its tiles.
+template <int ROWS, int PAD>
+__device__ __forceinline__ bool place_of(const AttnArgs& p, int me, Place* x) {
+    const int lane = threadIdx.x & 63;
+    int sub = 64;  // lanes of a sequence
+    while (sub > 1 && 64 / sub < p.batch) sub >>= 1;
+    const int each = 64 / sub;
+    const auto head_cost = [&](int b) -> int64_t {
+        int64_t n = 0;
+        if (b < p.batch) {
+            const Seq s = seq_of(p, b);
+            const int tiles = tiles_of<ROWS>(p, s);
+            int u0;
+            for (int i = lane & (sub - 1); i < tiles; i += sub) n += units_of<ROWS>(p, s, i, &u0) + PAD;
+        }
+        for (int d = 1; d < sub; d <<= 1) n += shfl64(n, lane ^ d);
+        return n;
+    };
+    // with up to 64 sequences one round does it, and its sums are kept
+    int64_t total = 0, own = 0, sum = 0;
+    for (int b0 = 0; b0 < p.batch; b0 += each) {
+        own = head_cost(b0 + lane / sub);
+        sum = wave_scan((lane & (sub - 1)) == 0 ? own * p.cache.heads : 0);
+        total += uniform(shfl64(sum, 63));
+    }
+    int64_t chunk = (total + p.groups - 1) / p.groups;
+    chunk = max(chunk, int64_t(kMinUnits + PAD));
+    x->chunk = chunk;
+    x->at = me * chunk;
+    x->end = min(x->at + chunk, total);
+    if (x->at >= x->end) return false;
+    int64_t before = 0;
+    int b0 = 0;
+    if (p.batch > each) {
+        for (;; b0 += each) {
+            own = head_cost(b0 + lane / sub);
+            sum = wave_scan((lane & (sub - 1)) == 0 ? own * p.cache.heads : 0);
+            const int64_t all = before + uniform(shfl64(sum, 63));
+            if (x->at < all) break;  // at < total, so some round gets here
+            before = all;
+        }
+    }
+    const int at_lane = __builtin_ctzll(__ballot(x->at < before + sum));  // a sequence's first lane
+    x->b = uniform(b0 + at_lane / sub);
+    const int64_t per_head = uniform(shfl64(own, at_lane));
+    int64_t rest = x->at - before - uniform(shfl64(sum, at_lane)) + per_head * p.cache.heads;
+    if ((rest | per_head) >> 31 == 0)
+        x->head = uniform(static_cast<int>(static_cast<uint32_t>(rest) / static_cast<uint32_t>(per_head)));
+    else
+        x->head = uniform(static_cast<int>(rest / per_head));
+    rest -= x->head * per_head;
+    const Seq s = seq_at(p, x->b);
+    const int tiles = tiles_of<ROWS>(p, s);
+    for (int t0 = 0;; t0 += 64) {
+        int u0;
+        const int cost = t0 + lane < tiles ? units_of<ROWS>(p, s, t0 + lane, &u0) + PAD : 0;
+        const int64_t upto = wave_scan(cost);
+        const int64_t all = uniform(shfl64(upto, 63));
+        if (rest < all) {
+            const int i = __builtin_ctzll(__ballot(rest < upto));
+            x->tile = uniform(t0 + i);
+            x->rest = rest - uniform(shfl64(upto - cost, i));
+            return true;
+        }
+        rest -= all;
+    }
 }
 
 // v over the lanes n, n + 16, n + 32, n + 48 that hold a row.
@@ -177,49 +260,78 @@ struct Keys {
     uint32_t ks[2];         // their scale bytes
     uint32_t v[D / 16];     // eight keys of a channel piece
     uint32_t vs[2];         // their scale bytes
-    bool ok;                // the lane's eight V keys have a page
+    bool ok[2];             // the first and the last 16 keys have a page
+};
+
+// The two pages of a unit's first and last 16 keys (one page, where it has 32 tokens or more).
+struct Pages {
+    int64_t at[2];
+};
+
+__device__ __forceinline__ Pages pages_of(const AttnArgs& p, const Seq& s, int b, int unit) {
+    Pages x;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        // keys behind the last are read from its page (and masked later): always inside the cache
+        const int i = min(unit * kUnit + 16 * h, max(s.len - 1, 0)) >> p.cache.shift;
+        const int64_t at = int64_t(b) * p.width + i;
+        x.at[h] = p.table ? scalar_load(p.table + at) : at;
+    }
+    return x;
+}
+
+// Where a lane's loads lie in a page's block, from the unit's first key on.
+struct Offsets {
+    uint32_t k, ks, v, vs;
 };
 
 template <int D>
-__device__ __forceinline__ void load_keys(Keys<D>& x, const AttnArgs& p, const Seq& s, int b, int head, int unit) {
+__device__ __forceinline__ Offsets offsets_of(const AttnArgs& p) {
     const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
     const KvBlock blk{p.cache.block.page, D};
-    const int mask = blk.page - 1;
-    const int last = s.len > 0 ? static_cast<int>(s.len - 1) : 0;
-    // keys behind the last are read from its page (and masked later): always inside the cache
-    const auto page_of = [&](int key, bool* ok) -> int64_t {
-        int64_t at = -1;
-        if (s.len > 0) {
-            at = int64_t(b) * p.width + (min(key, last) >> p.cache.shift);
-            if (p.table) at = p.table[at];
-        }
-        *ok = at >= 0 && at < p.cache.pages;
-        return *ok ? at : 0;
-    };
-    bool ok;
+    const int mask = min(blk.page, kUnit) - 1;
+    const int row = 8 * (n >> 2) + (n & 3);
+    Offsets o;
+    o.k = blk.k_code(row & mask) + g * (D / 8);
+    o.ks = blk.k_scale(row & mask, g * (D / 4) / kKvGroup);
+    o.v = blk.v_code(8 * g & mask, n);
+    o.vs = blk.v_scale(8 * g & mask, n * (D / 16) / kKvGroup);
+    return o;
+}
+
+template <int D>
+__device__ __forceinline__ void load_keys(Keys<D>& x, const AttnArgs& p, const Seq& s, const Pages& pages,
+                                          const Offsets& o, int head, int unit) {
+    const int lane = threadIdx.x & 63;
+    const KvBlock blk{p.cache.block.page, D};
+    const int in = unit * kUnit & (blk.page - 1);
+    const uint8_t* base[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const int key = unit * kUnit + 8 * (n >> 2) + (n & 3) + 4 * h;
-        const uint8_t* const base = p.cache.at(page_of(key, &ok), head);
-        const uint8_t* const c = base + blk.k_code(key & mask) + g * (D / 8);
+        x.ok[h] = s.len > 0 && pages.at[h] >= 0 && pages.at[h] < p.cache.pages;
+        base[h] = p.cache.at(x.ok[h] ? pages.at[h] : 0, head);
+    }
+    const uint8_t* const kb = lane & 8 ? base[1] : base[0];
+    const uint8_t* const vb = lane & 32 ? base[1] : base[0];
+    const uint8_t* const kc = kb + (o.k + in * (D / 2));
+    const uint8_t* const vc = vb + (o.v + in * (D / 2));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {  // four tokens further
         if constexpr (D == 128) {
-            const vu4 w = *reinterpret_cast<const vu4*>(c);
+            const vu4 w = *reinterpret_cast<const vu4*>(kc + 4 * h * (D / 2));
             x.k[h][0] = w.x, x.k[h][1] = w.y, x.k[h][2] = w.z, x.k[h][3] = w.w;
         } else {
-            const vu2 w = *reinterpret_cast<const vu2*>(c);
+            const vu2 w = *reinterpret_cast<const vu2*>(kc + 4 * h * (D / 2));
             x.k[h][0] = w.x, x.k[h][1] = w.y;
         }
-        x.ks[h] = base[blk.k_scale(key & mask, g * (D / 4) / kKvGroup)];
+        x.ks[h] = kb[o.ks + in * (D / 32) + 4 * h * (D / 32)];
     }
-    const int key = unit * kUnit + 8 * g;
-    const uint8_t* const base = p.cache.at(page_of(key, &x.ok), head);
-    const uint8_t* const c = base + blk.v_code(key & mask, n);
 #pragma unroll
     for (int i = 0; i < D / 16; i += 4) {
-        const vu4 w = *reinterpret_cast<const vu4*>(c + 4 * i);
+        const vu4 w = *reinterpret_cast<const vu4*>(vc + 4 * i);
         x.v[i] = w.x, x.v[i + 1] = w.y, x.v[i + 2] = w.z, x.v[i + 3] = w.w;
     }
-    const vu2 w = *reinterpret_cast<const vu2*>(base + blk.v_scale(key & mask, n * (D / 16) / kKvGroup));
+    const vu2 w = *reinterpret_cast<const vu2*>(vb + (o.vs + in * (D / 32)));
     x.vs[0] = w.x, x.vs[1] = w.y;
 }
 
@@ -230,11 +342,10 @@ struct Rows {
 };
 
 template <typename T, int D, int PARTS>
-__device__ __forceinline__ void load_rows(Rows<D, PARTS>& x, const AttnArgs& p, const Seq& s, int head, int64_t row,
-                                          bool on) {
+__device__ __forceinline__ void load_rows(Rows<D, PARTS>& x, const AttnArgs& p, const Seq& s, int head, int row,
+                                          int token, bool on) {
     const int g = (threadIdx.x & 63) >> 4;
-    const int64_t token = on ? row / p.share : 0;
-    const T* const q = row_ptr<T>(p.q, s.q0 + token, head * p.share + static_cast<int>(on ? row - token * p.share : 0));
+    const T* const q = row_ptr<T>(p.q, s.q0 + token, head * p.share + row - token * p.share);
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
         float f[8];
@@ -264,6 +375,7 @@ struct Shape {
     static constexpr int kParts = sizeof(T) == 4 ? 3 : 1;
     static constexpr int kP = sizeof(T) == 4 ? 2 : 1;
     static constexpr int kRows = 16 * NQ * (SPLIT ? 1 : kWaves);
+    static constexpr int kPad = SPLIT ? 8 : 2;
 };
 
 // Floats of one partial result: rows x (D values, the reference, the sum).
@@ -282,96 +394,58 @@ __device__ __forceinline__ void store_out(T* o, const float (&x)[8]) {
 template <typename T, int D, int NQ, bool SPLIT>
 __global__ __launch_bounds__(kThreads, NQ == 1 ? 2 : 1) void attn_kernel(const AttnArgs p) {
     using S = Shape<T, D, NQ, SPLIT>;
-    constexpr int kRows = S::kRows, kParts = S::kParts, kP = S::kP;
+    constexpr int kRows = S::kRows, kPad = S::kPad, kParts = S::kParts, kP = S::kP;
     constexpr int kJ = D / 16;  // O^T tiles of 16 channel pieces
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
+    const int lane = threadIdx.x & 63, wave = uniform(static_cast<int>(threadIdx.x) >> 6), n = lane & 15, g = lane >> 4;
     // neighbours in the order of the work share keys: let them share an XCD's L2
     const int me = (blockIdx.x & 7) * (p.groups >> 3) + (blockIdx.x >> 3);
 
-    __shared__ int64_t scan[kThreads];
-    __shared__ int64_t found[2];
     __shared__ float stage[SPLIT ? kWaves * 16 * (D + 4) : 1];
     __shared__ float stage_m[SPLIT ? kWaves * 16 : 1], stage_l[SPLIT ? kWaves * 16 : 1];
 
-    // total units, and a workgroup's run of them
-    int64_t mine = 0;
-    for (int b = threadIdx.x; b < p.batch; b += kThreads) mine += head_units<kRows>(p, seq_of(p, b)) * p.cache.heads;
-    scan[threadIdx.x] = mine;
-    __syncthreads();
-    for (int d = kThreads / 2; d > 0; d >>= 1) {
-        if (threadIdx.x < d) scan[threadIdx.x] += scan[threadIdx.x + d];
-        __syncthreads();
-    }
-    const int64_t total = scan[0];
-    int64_t chunk = (total + p.groups - 1) / p.groups;
-    chunk = chunk < kMinUnits ? kMinUnits : chunk;
-    int64_t at = me * chunk;
-    const int64_t end = at + chunk < total ? at + chunk : total;
     if (threadIdx.x == 0) p.joins[me * 4] = -1;
-    if (at >= end) return;
+    Place w;
+    if (!place_of<kRows, kPad>(p, me, &w)) return;
+    const Offsets offs = offsets_of<D>(p);
+    Seq s = seq_at(p, w.b);
 
-    // the sequence of the first unit
-    int64_t before = 0;
-    for (int b0 = 0;; b0 += kThreads) {
-        __syncthreads();
-        const int b = b0 + threadIdx.x;
-        const int64_t own = b < p.batch ? head_units<kRows>(p, seq_of(p, b)) * p.cache.heads : 0;
-        scan[threadIdx.x] = own;
-        __syncthreads();
-        for (int d = 1; d < kThreads; d <<= 1) {
-            const int64_t x = threadIdx.x >= d ? scan[threadIdx.x - d] : 0;
-            __syncthreads();
-            scan[threadIdx.x] += x;
-            __syncthreads();
-        }
-        const int64_t hi = before + scan[threadIdx.x], lo = hi - own;
-        if (at >= lo && at < hi) found[0] = b, found[1] = lo;
-        const int64_t all = before + scan[kThreads - 1];
-        __syncthreads();
-        if (at < all) break;  // total > at, so some round gets here
-        before = all;
-    }
-    int b = static_cast<int>(found[0]);
-    Seq s = seq_of(p, b);
-    int64_t per_head = head_units<kRows>(p, s);
-    int64_t rest = at - found[1];
-    int head = static_cast<int>(rest / per_head);
-    rest -= head * per_head;
-    int64_t tile = 0;
-    int u0, count;
-    for (;; ++tile) {
-        count = units_of<kRows>(p, s, tile, &u0);
-        if (rest < count) break;
-        rest -= count;
-    }
-
-    while (at < end) {
+    while (w.at < w.end) {
         // units [a, z) of this item
-        const int a = static_cast<int>(rest);
-        const int z = count - a < end - at ? count : a + static_cast<int>(end - at);
-        const int64_t rows = s.nq * p.share;
-        const int64_t row0 = tile * kRows + (SPLIT ? 0 : wave * 16 * NQ);
+        int u0;
+        const int count = units_of<kRows>(p, s, w.tile, &u0);
+        const int64_t take = min(w.end - w.at, count + kPad - w.rest);
+        const int a = max(static_cast<int>(w.rest) - kPad, 0), z = static_cast<int>(w.rest + take) - kPad;
+        w.at += take;
+        if (z <= 0) break;  // the next workgroup begins this item
+        const int rows = s.nq * p.share;
+        const int row0 = w.tile * kRows + (SPLIT ? 0 : wave * 16 * NQ);
+        const int head = w.head;
+
+        constexpr int kStep = SPLIT ? kWaves : 1;
+        const int first = a + (SPLIT ? wave : 0);
+        Pages pages = pages_of(p, s, w.b, u0 + first);
+        Keys<D> next;
+        if (first < z) load_keys<D>(next, p, s, pages, offs, head, u0 + first);
+        if (first + kStep < z) pages = pages_of(p, s, w.b, u0 + first + kStep);
 
         Rows<D, kParts> q[NQ];
         int lo[NQ], hi[NQ];                   // keys that row n of each sixteen sees
         int full_lo = 0, full_hi = INT32_MAX; // keys that all of the wave's rows see
+        {
+            const int last = min(row0 + 16 * NQ, rows) - 1;
+            if (last >= row0) {
+                full_lo = seen_lo(p, s, token_of(p, last));
+                full_hi = seen_hi(p, s, token_of(p, row0));
+            }
+        }
 #pragma unroll
         for (int i = 0; i < NQ; ++i) {
-            const int64_t row = row0 + i * 16 + n;
+            const int row = row0 + i * 16 + n;
             const bool on = row < rows;
-            load_rows<T, D, kParts>(q[i], p, s, head, row, on);
-            int64_t l = 0, h = 0;
-            if (on) seen(p, s, row / p.share, &l, &h);
-            lo[i] = static_cast<int>(l);
-            hi[i] = h > 0 ? static_cast<int>(h) : 0;
-            int fl = on ? lo[i] : 0, fh = on ? hi[i] : INT32_MAX;
-#pragma unroll
-            for (int d = 1; d < 16; d <<= 1) {
-                fl = max(fl, __shfl_xor(fl, d, 64));
-                fh = min(fh, __shfl_xor(fh, d, 64));
-            }
-            full_lo = max(full_lo, fl);
-            full_hi = min(full_hi, fh);
+            const int token = token_of(p, on ? row : row0 < rows ? row0 : 0);
+            load_rows<T, D, kParts>(q[i], p, s, head, on ? row : 0, on ? token : 0, on);
+            lo[i] = on ? seen_lo(p, s, token) : 0;
+            hi[i] = on ? seen_hi(p, s, token) : 0;
         }
 
         vf4 o[NQ][kJ];
@@ -383,24 +457,22 @@ __global__ __launch_bounds__(kThreads, NQ == 1 ? 2 : 1) void attn_kernel(const A
             for (int j = 0; j < kJ; ++j) o[i][j] = vf4{0.f, 0.f, 0.f, 0.f};
         }
 
-        constexpr int kStep = SPLIT ? kWaves : 1;
-        const int first = a + (SPLIT ? wave : 0);
-        Keys<D> next;
-        if (first < z) load_keys<D>(next, p, s, b, head, u0 + first);
         for (int u = first; u < z; u += kStep) {
             Keys<D> x = next;
-            if (u + kStep < z) load_keys<D>(next, p, s, b, head, u0 + u + kStep);
+            if (u + kStep < z) load_keys<D>(next, p, s, pages, offs, head, u0 + u + kStep);
+            if (u + 2 * kStep < z) pages = pages_of(p, s, w.b, u0 + u + 2 * kStep);
             const int key0 = (u0 + u) * kUnit;
             // the lane's own eight keys
             const int mine0 = key0 + 8 * g;
-            const bool edge = __any(key0 < full_lo || key0 + kUnit > full_hi || !x.ok);
+            const bool ok = lane & 32 ? x.ok[1] : x.ok[0];
+            const bool edge = key0 < full_lo || key0 + kUnit > full_hi || !x.ok[0] || !x.ok[1];
             uint32_t bad = 0;  // V groups of the lane's keys that read NaN, a bit a key
             uint32_t kbad[2] = {0, 0};
             if (edge) {
                 // V behind the sequence's last key is whatever an earlier owner of the page left
 #pragma unroll
                 for (int t = 0; t < 8; ++t) {
-                    if (x.ok && mine0 + t < s.len) continue;
+                    if (ok && mine0 + t < s.len) continue;
                     if constexpr (D == 128)
                         x.v[t] = 0;
                     else
@@ -457,23 +529,23 @@ __global__ __launch_bounds__(kThreads, NQ == 1 ? 2 : 1) void attn_kernel(const A
             vh8 pf[NQ][kP];
 #pragma unroll
             for (int i = 0; i < NQ; ++i) {
-                float w[8];
+                float x2[8];  // scores in units of log2
 #pragma unroll
-                for (int t = 0; t < 8; ++t) w[t] = sc[i][t >> 2][t & 3] * p.scale_log2;
+                for (int t = 0; t < 8; ++t) x2[t] = sc[i][t >> 2][t & 3] * p.scale_log2;
                 uint32_t see = 0xff;
                 if (nans) {
 #pragma unroll
                     for (int t = 0; t < 8; ++t)
-                        if (kbad[t >> 2] >> (4 * g + (t & 3)) & 1u) w[t] = __builtin_nanf("");
+                        if (kbad[t >> 2] >> (4 * g + (t & 3)) & 1u) x2[t] = __builtin_nanf("");
                 }
                 if (edge) {
 #pragma unroll
                     for (int t = 0; t < 8; ++t)
-                        if (!x.ok || mine0 + t < lo[i] || mine0 + t >= hi[i]) w[t] = kNone, see &= ~(1u << t);
+                        if (!ok || mine0 + t < lo[i] || mine0 + t >= hi[i]) x2[t] = kNone, see &= ~(1u << t);
                 }
                 float top = kNone;
 #pragma unroll
-                for (int t = 0; t < 8; ++t) top = fmaxf(top, w[t]);
+                for (int t = 0; t < 8; ++t) top = fmaxf(top, x2[t]);
                 if (__any(top > m[i] + (kSlack + kLift))) {
                     // the lanes of a row agree on its new reference
                     const float r = fmaxf(across_max(top) - kLift, m[i]);
@@ -486,11 +558,11 @@ __global__ __launch_bounds__(kThreads, NQ == 1 ? 2 : 1) void attn_kernel(const A
                 const float ref = m[i] == kNone ? 0.f : m[i];
 #pragma unroll
                 for (int t = 0; t < 8; ++t) {
-                    w[t] = __builtin_amdgcn_exp2f(w[t] - ref);
-                    sum[i] += w[t];
-                    const _Float16 h = static_cast<_Float16>(w[t]);
+                    x2[t] = __builtin_amdgcn_exp2f(x2[t] - ref);
+                    sum[i] += x2[t];
+                    const _Float16 h = static_cast<_Float16>(x2[t]);
                     pf[i][0][t] = h;
-                    if constexpr (kP == 2) pf[i][1][t] = static_cast<_Float16>(w[t] - static_cast<float>(h));
+                    if constexpr (kP == 2) pf[i][1][t] = static_cast<_Float16>(x2[t] - static_cast<float>(h));
                 }
                 if (nans) {
                     // a NaN of V reaches the rows that see its key, and only those
@@ -559,23 +631,22 @@ __global__ __launch_bounds__(kThreads, NQ == 1 ? 2 : 1) void attn_kernel(const A
         float* const part = p.part + (2 * int64_t(me) + (a == 0)) * part_floats<D>(kRows);
         const auto put = [&](int r, int c, float (&v)[8], float top, float l, bool first_piece) {
             // eight channels from c of row r of the item
-            const int64_t row = tile * kRows + r;
+            const int row = w.tile * kRows + r;
             if (row >= rows) return;
             if (whole) {
-                const int64_t token = row / p.share;
-                const int qh = head * p.share + static_cast<int>(row - token * p.share);
+                const int token = token_of(p, row), qh = head * p.share + row - token * p.share;
                 const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
                 for (int k = 0; k < 8; ++k) v[k] *= inv;
                 store_out<T>(row_ptr<T>(p.out, s.q0 + token, qh) + c, v);
                 if (p.lse && first_piece)
-                    p.lse[(s.q0 + token) * p.q_heads + qh] =
+                    p.lse[int64_t(s.q0 + token) * p.q_heads + qh] =
                         l == 0.f ? kNone : (top + __builtin_amdgcn_logf(l)) * 0.693147180559945309f;
             } else {
-                float* const w = part + int64_t(r) * (D + 2);
+                float* const y = part + int64_t(r) * (D + 2);
 #pragma unroll
-                for (int k = 0; k < 8; k += 2) *reinterpret_cast<float2*>(w + c + k) = float2{v[k], v[k + 1]};
-                if (first_piece) *reinterpret_cast<float2*>(w + D) = float2{top, l};
+                for (int k = 0; k < 8; k += 2) *reinterpret_cast<float2*>(y + c + k) = float2{v[k], v[k + 1]};
+                if (first_piece) *reinterpret_cast<float2*>(y + D) = float2{top, l};
             }
         };
 #pragma unroll
@@ -592,10 +663,10 @@ __global__ __launch_bounds__(kThreads, NQ == 1 ? 2 : 1) void attn_kernel(const A
                 }
             } else {
                 __syncthreads();
-                float* const w = stage + (wave * 16 + n) * (D + 4) + g * (D / 4);
+                float* const y = stage + (wave * 16 + n) * (D + 4) + g * (D / 4);
 #pragma unroll
                 for (int c = 0; c < D / 4; c += 4)
-                    *reinterpret_cast<vf4*>(w + c) = vf4{o[i][c % kJ][c / kJ], o[i][(c + 1) % kJ][(c + 1) / kJ],
+                    *reinterpret_cast<vf4*>(y + c) = vf4{o[i][c % kJ][c / kJ], o[i][(c + 1) % kJ][(c + 1) / kJ],
                                                          o[i][(c + 2) % kJ][(c + 2) / kJ], o[i][(c + 3) % kJ][(c + 3) / kJ]};
                 if (g == 0) stage_m[wave * 16 + n] = m[i], stage_l[wave * 16 + n] = sum[i];
                 __syncthreads();
@@ -620,67 +691,87 @@ __global__ __launch_bounds__(kThreads, NQ == 1 ? 2 : 1) void attn_kernel(const A
             }
         }
         if (threadIdx.x == 0 && a > 0 && z == count) {
-            // units before this item: at - a
             int32_t* const j = p.joins + me * 4;
-            j[1] = b, j[2] = head, j[3] = static_cast<int32_t>(tile);
-            j[0] = static_cast<int32_t>((at - a) / chunk);
+            j[1] = w.b, j[2] = head, j[3] = w.tile;
+            // the workgroup with the item's first unit
+            j[0] = static_cast<int32_t>((w.at - count) / w.chunk);
         }
 
         // on to the next item
-        at += z - a;
-        rest = 0;
-        if (at >= end) break;
-        ++tile;
-        if (tile >= tiles_of<kRows>(p, s)) {
-            tile = 0;
-            if (++head >= p.cache.heads) {
-                head = 0;
-                do s = seq_of(p, ++b);  // at < end <= total: another sequence has units
+        w.rest = 0;
+        if (w.at >= w.end) break;
+        if (++w.tile >= tiles_of<kRows>(p, s)) {
+            w.tile = 0;
+            if (++w.head >= p.cache.heads) {
+                w.head = 0;
+                do s = seq_at(p, ++w.b);  // at < end <= total: another sequence has units
                 while (s.nq == 0);
             }
         }
-        count = units_of<kRows>(p, s, tile, &u0);
     }
 }
 
-// Joins the parts of the items that ended up in several workgroups: block (w, y) the rows
-// 8y .. of the item whose last keys were workgroup w's.
+// Joins the parts of the items that ended up in several workgroups: block (w, y) some rows
+// of the item whose last keys were workgroup w's.
 template <typename T, int D, int ROWS>
 __global__ __launch_bounds__(kThreads) void join_kernel(const AttnArgs p) {
     const int me = blockIdx.x;
-    const int first = p.joins[me * 4];
+    const int first = scalar_load(p.joins + me * 4);
     if (first < 0) return;
-    const int b = p.joins[me * 4 + 1], head = p.joins[me * 4 + 2], tile = p.joins[me * 4 + 3];
-    const Seq s = seq_of(p, b);
-    constexpr int kLanes = D / 4;
-    const int r = blockIdx.y * (kThreads / kLanes) + threadIdx.x / kLanes, c = threadIdx.x % kLanes * 4;
-    const int64_t row = int64_t(tile) * ROWS + r;
-    if (r >= ROWS || row >= s.nq * p.share) return;
-    const auto part = [&](int w) {
-        return p.part + (2 * int64_t(w) + (w == first)) * part_floats<D>(ROWS) + int64_t(r) * (D + 2);
-    };
-    float top = kNone;
-    for (int w = first; w <= me; ++w) top = fmaxf(top, part(w)[D]);
-    float v[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f;
-    for (int w = first; w <= me; ++w) {
-        const float* const x = part(w);
-        const float f = x[D] == kNone ? 0.f : __builtin_amdgcn_exp2f(x[D] - top);
-        l = __builtin_fmaf(x[D + 1], f, l);
-        const float2 a = *reinterpret_cast<const float2*>(x + c), d = *reinterpret_cast<const float2*>(x + c + 2);
-        v[0] = __builtin_fmaf(a.x, f, v[0]);
-        v[1] = __builtin_fmaf(a.y, f, v[1]);
-        v[2] = __builtin_fmaf(d.x, f, v[2]);
-        v[3] = __builtin_fmaf(d.y, f, v[3]);
-    }
-    const int64_t token = row / p.share;
-    const int qh = head * p.share + static_cast<int>(row - token * p.share);
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    T* const o = row_ptr<T>(p.out, s.q0 + token, qh) + c;
+    const int b = scalar_load(p.joins + me * 4 + 1), head = scalar_load(p.joins + me * 4 + 2),
+              tile = scalar_load(p.joins + me * 4 + 3);
+    const Seq s = seq_at(p, b);
+    constexpr int kLanes = D / 4, kAtOnce = kThreads / kLanes;
+    const int rows = min(ROWS, s.nq * p.share - tile * ROWS);
+    const int l0 = threadIdx.x % kLanes, c = 4 * l0, self = threadIdx.x & 63 & ~(kLanes - 1);
+    for (int r0 = blockIdx.y * kAtOnce; r0 < rows; r0 += gridDim.y * kAtOnce) {
+        const int r = min(r0 + static_cast<int>(threadIdx.x) / kLanes, rows - 1);
+        const auto part = [&](int w) {
+            return p.part + (2 * int64_t(w) + (w == first)) * part_floats<D>(ROWS) + int64_t(r) * (D + 2);
+        };
+        // a row's lanes look at a part each
+        float top = kNone;
+        for (int w = first + l0; w <= me; w += kLanes) top = fmaxf(top, part(w)[D]);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) o[k] = static_cast<T>(v[k] * inv);
-    if (p.lse && c == 0)
-        p.lse[(s.q0 + token) * p.q_heads + qh] =
-            l == 0.f ? kNone : (top + __builtin_amdgcn_logf(l)) * 0.693147180559945309f;
+        for (int d = 1; d < kLanes; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
+        float v[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f;
+        for (int w0 = first; w0 <= me; w0 += kLanes) {
+            const int w = w0 + l0;
+            float f = 0.f, lw = 0.f;
+            if (w <= me) {
+                const float2 ml = *reinterpret_cast<const float2*>(part(w) + D);
+                f = ml.x == kNone ? 0.f : __builtin_amdgcn_exp2f(ml.x - top);
+                lw = ml.y;
+            }
+            const int many = min(kLanes, me + 1 - w0);
+            for (int i = 0; i < many; i += 8) {  // eight parts in flight
+                float2 x0[8], x1[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float* const x = part(w0 + min(i + k, many - 1));  // again, for nothing: f is 0
+                    x0[k] = *reinterpret_cast<const float2*>(x + c), x1[k] = *reinterpret_cast<const float2*>(x + c + 2);
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float fi = __shfl(f, self + i + k, 64);
+                    l = __builtin_fmaf(__shfl(lw, self + i + k, 64), fi, l);
+                    v[0] = __builtin_fmaf(x0[k].x, fi, v[0]);
+                    v[1] = __builtin_fmaf(x0[k].y, fi, v[1]);
+                    v[2] = __builtin_fmaf(x1[k].x, fi, v[2]);
+                    v[3] = __builtin_fmaf(x1[k].y, fi, v[3]);
+                }
+            }
+        }
+        if (r0 + static_cast<int>(threadIdx.x) / kLanes >= rows) continue;
+        const int row = tile * ROWS + r, token = token_of(p, row), qh = head * p.share + row - token * p.share;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        T* const o = row_ptr<T>(p.out, s.q0 + token, qh) + c;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[k] = static_cast<T>(v[k] * inv);
+        if (p.lse && c == 0)
+            p.lse[int64_t(s.q0 + token) * p.q_heads + qh] =
+                l == 0.f ? kNone : (top + __builtin_amdgcn_logf(l)) * 0.693147180559945309f;
+    }
 }
 
 struct Plan {
@@ -700,20 +791,21 @@ Plan plan_of(int a_dtype, int head_dim, int64_t rows) {
 }
 
 template <typename T, int D, int NQ, bool SPLIT>
-hipError_t launch(const AttnArgs& p, hipStream_t stream) {
+hipError_t launch(const AttnArgs& p, int64_t max_rows, hipStream_t stream) {
     constexpr int kRows = Shape<T, D, NQ, SPLIT>::kRows, kJoinRows = kThreads / (D / 4);
+    const int join_rows = max_rows < kRows ? static_cast<int>(max_rows) : kRows;
     attn_kernel<T, D, NQ, SPLIT><<<p.groups, kThreads, 0, stream>>>(p);
     if (hipError_t e = hipGetLastError()) return e;
-    join_kernel<T, D, kRows><<<dim3(p.groups, (kRows + kJoinRows - 1) / kJoinRows), kThreads, 0, stream>>>(p);
+    join_kernel<T, D, kRows><<<dim3(p.groups, (join_rows + kJoinRows - 1) / kJoinRows), kThreads, 0, stream>>>(p);
     return hipGetLastError();
 }
 
 template <typename T, int D>
-hipError_t launch_rows(int rows, const AttnArgs& p, hipStream_t stream) {
+hipError_t launch_rows(int rows, const AttnArgs& p, int64_t max_rows, hipStream_t stream) {
     constexpr int kWide = sizeof(T) == 4 ? 2 : 4;
-    if (rows == 16) return launch<T, D, 1, true>(p, stream);
-    if (rows == 32) return launch<T, D, 2, true>(p, stream);
-    return launch<T, D, kWide, false>(p, stream);
+    if (rows == 16) return launch<T, D, 1, true>(p, max_rows, stream);
+    if (rows == 32) return launch<T, D, 2, true>(p, max_rows, stream);
+    return launch<T, D, kWide, false>(p, max_rows, stream);
 }
 
 }  // namespace
@@ -724,11 +816,12 @@ size_t kv4_attention_workspace(int a_dtype, int head_dim, int64_t max_rows) {
 
 hipError_t launch_kv4_attention(int a_dtype, const Kv4Attention& c, void* workspace, hipStream_t stream) {
     const int share = c.q_heads / c.cache.heads;
-    const Plan x = plan_of(a_dtype, c.cache.block.dim, c.max_q * share);
+    const int64_t max_rows = c.max_q * share;
+    const Plan x = plan_of(a_dtype, c.cache.block.dim, max_rows);
     AttnArgs p{};
     p.q = c.q, p.out = c.out, p.cache = c.cache, p.table = c.table, p.width = c.table_width;
-    p.kv_lens = c.kv_lens, p.q_starts = c.q_starts, p.total_q = c.total_q;
-    p.q_each = c.q_starts ? 0 : c.total_q / c.batch;
+    p.kv_lens = c.kv_lens, p.q_starts = c.q_starts, p.total_q = static_cast<int>(c.total_q);
+    p.q_each = c.q_starts ? 0 : static_cast<int>(c.total_q / c.batch);
     p.batch = c.batch, p.q_heads = c.q_heads, p.share = share;
     p.causal = c.causal, p.window = c.window;
     p.scale_log2 = c.scale * 1.44269504088896341f;
@@ -738,8 +831,8 @@ hipError_t launch_kv4_attention(int a_dtype, const Kv4Attention& c, void* worksp
     p.part = reinterpret_cast<float*>(p.joins + 4 * x.groups);
     const bool d64 = c.cache.block.dim == 64;
     if (a_dtype == CF_BF16)
-        return d64 ? launch_rows<__bf16, 64>(x.rows, p, stream) : launch_rows<__bf16, 128>(x.rows, p, stream);
-    return d64 ? launch_rows<float, 64>(x.rows, p, stream) : launch_rows<float, 128>(x.rows, p, stream);
+        return d64 ? launch_rows<__bf16, 64>(x.rows, p, max_rows, stream) : launch_rows<__bf16, 128>(x.rows, p, max_rows, stream);
+    return d64 ? launch_rows<float, 64>(x.rows, p, max_rows, stream) : launch_rows<float, 128>(x.rows, p, max_rows, stream);
 }
 
 }  // namespace cf
