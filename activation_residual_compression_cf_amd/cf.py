@@ -467,24 +467,62 @@ def lowrank_decompress(factor_bits: int, payload, ahat: torch.Tensor, rank: int,
         _stream(stream)))
 
 
-def _rows(name: str, t: torch.Tensor) -> Rows:
-    """The rows of a (tokens, heads, head_dim) tensor, of any strides but the last."""
-    if t.dim() != 3:
-        raise ValueError(f"{name} has {t.dim()} axes; libcf wants (tokens, heads, head_dim)")
-    if not t.is_cuda:
-        raise ValueError("libcf takes device tensors (a host pointer would fault the kernel)")
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name} on {t.device}, but the current device is cuda:{torch.cuda.current_device()} "
+# The calls below are a few microseconds on the device, so their marshalling asks the runtime for
+# the current device and stream once, and for nothing twice.
+
+
+def _here(name: str, t: torch.Tensor, dev: int):
+    """Refuses a tensor that is not on the current device ``dev``."""
+    if t.get_device() != dev:
+        if not t.is_cuda:
+            raise ValueError("libcf takes device tensors (a host pointer would fault the kernel)")
+        raise ValueError(f"{name} on {t.device}, but the current device is cuda:{dev} "
                          "(libcf launches on the current device)")
+
+
+def _rows(name: str, t: torch.Tensor, dev: int) -> Rows:
+    """The rows of a (tokens, heads, head_dim) tensor, of any strides but the last."""
+    _here(name, t, dev)
     st, sh, sd = t.stride()
     if sd != 1 and t.shape[2] > 1:
         raise ValueError(f"{name}: the channels of a row must be consecutive")
     return Rows(t.data_ptr(), st, sh)
 
 
-def _shaped(name: str, t: torch.Tensor | None, *shape):
-    if t is not None and tuple(t.shape) != shape:
+def _flat(name: str, t: torch.Tensor | None, dev: int, dtype: torch.dtype, shape: tuple):
+    """Address of a contiguous tensor of this type and shape, None for None."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{name} is {t.dtype}; libcf wants {dtype}")
+    if t.shape != shape:
         raise ValueError(f"{name} is {tuple(t.shape)}, the call needs {shape}")
+    _here(name, t, dev)
+    if not t.is_contiguous():
+        raise ValueError("libcf needs contiguous tensors")
+    return t.data_ptr()
+
+
+def _shaped(name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple):
+    if t.dtype != dtype:
+        raise TypeError(f"{name} is {t.dtype}; libcf wants {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} is {tuple(t.shape)}, the call needs {tuple(shape)}")
+
+
+def _device(t: torch.Tensor) -> int:
+    """The current device; no tensor's where t is not on one (there may be none)."""
+    return torch._C._cuda_getDevice() if t.is_cuda else -2
+
+
+def _on(stream, dev: int):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+
+
+def _new(like: torch.Tensor, shape, stream, dtype: torch.dtype | None = None) -> torch.Tensor:
+    """A buffer for the launch stream to write."""
+    t = like.new_empty(shape, dtype=dtype)
+    return t if stream is None else _keep_for(t, stream)
 
 
 def qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, norm: int = CF_NORM_RMS,
@@ -502,41 +540,40 @@ def qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, norm: int = CF_
     if a is None or a.dim() != 3:
         raise ValueError("q or k must be a (tokens, heads, head_dim) tensor")
     tokens, _, dim = a.shape
-    dt = _act_dtype(a)
-    sides, outs, rows = (("q", q), ("k", k)), [q_out, k_out], []
-    heads = [0 if t is None else t.shape[1] if t.dim() == 3 else -1 for _, t in sides]
-    for (nm, t), o, h in zip(sides, outs, heads):
+    dt, kind = _act_dtype(a), a.dtype
+    hq = 0 if q is None else q.shape[1] if q.dim() == 3 else -1
+    hk = 0 if k is None else k.shape[1] if k.dim() == 3 else -1
+    for nm, t, o, h in (("q", q, q_out, hq), ("k", k, k_out, hk)):
         if t is not None:
-            _dtype(nm, t, a.dtype)
-            _shaped(nm, t, tokens, h, dim)
-            _dtype(nm + "_out", o, a.dtype)
-            _shaped(nm + "_out", o, tokens, h, dim)
-    for i, (nm, t) in enumerate(sides):
-        if t is None:
-            rows += [None, None]
-            continue
-        if outs[i] is None:
-            outs[i] = _keep_for(torch.empty(t.shape, dtype=t.dtype, device=t.device), stream)
-        rows += [_rows(nm, t), _rows(nm + "_out", outs[i])]
-    for nm, t in (("q_weight", q_weight), ("q_bias", q_bias), ("k_weight", k_weight), ("k_bias", k_bias)):
-        _dtype(nm, t, _F32)
-        _shaped(nm, t, dim)
+            _shaped(nm, t, kind, (tokens, h, dim))
+            if o is not None:
+                _shaped(nm + "_out", o, kind, t.shape)
+    dev = _device(a)
+    rq = rk = rqo = rko = None
+    if q is not None:
+        rq = _rows("q", q, dev)
+        q_out = _new(q, q.shape, stream) if q_out is None else q_out
+        rqo = _rows("q_out", q_out, dev)
+    if k is not None:
+        rk = _rows("k", k, dev)
+        k_out = _new(k, k.shape, stream) if k_out is None else k_out
+        rko = _rows("k_out", k_out, dev)
     n_pos = rot = 0
+    pc = ps = pp = None
     if rope != CF_ROPE_NONE:
         if cos is None or sin is None or cos.dim() != 2:
             raise ValueError("a rotation needs cos and sin, (positions, rot_dim / 2) fp32")
-        n_pos, rot = cos.shape[0], 2 * cos.shape[1]
-        _dtype("cos", cos, _F32)
-        _dtype("sin", sin, _F32)
-        _shaped("sin", sin, *cos.shape)
-        _dtype("positions", positions, torch.int32)
-        _shaped("positions", positions, tokens)
-    else:
-        cos = sin = positions = None
-    _check("cf_qk_norm_rope", lib.cf_qk_norm_rope(
-        dt, tokens, heads[0], heads[1], dim, rows[0], rows[2], rows[1], rows[3], norm, _ptr(q_weight), _ptr(q_bias),
-        _ptr(k_weight), _ptr(k_bias), eps, rope, _ptr(cos), _ptr(sin), n_pos, rot, _ptr(positions), _stream(stream)))
-    return outs[0], outs[1]
+        n_pos, rot = cos.shape
+        pc, ps = _flat("cos", cos, dev, _F32, (n_pos, rot)), _flat("sin", sin, dev, _F32, (n_pos, rot))
+        pp = _flat("positions", positions, dev, torch.int32, (tokens,))
+    row = (dim,)
+    rc = lib.cf_qk_norm_rope(
+        dt, tokens, hq, hk, dim, rq, rk, rqo, rko, norm, _flat("q_weight", q_weight, dev, _F32, row),
+        _flat("q_bias", q_bias, dev, _F32, row), _flat("k_weight", k_weight, dev, _F32, row),
+        _flat("k_bias", k_bias, dev, _F32, row), eps, rope, pc, ps, n_pos, 2 * rot, pp, _on(stream, dev))
+    if rc:
+        raise CFError("cf_qk_norm_rope", rc)
+    return q_out, k_out
 
 
 @dataclass
@@ -555,46 +592,42 @@ class KV4Cache:
         return KV4Cache(torch.zeros((pages, kv_heads, nb // pages // kv_heads), dtype=torch.uint8,
                                     device=device or require_device()), page_size, head_dim)
 
-    def _args(self):
+    def _args(self, dev: int):
         d = self.data
-        _dtype("cache", d, _U8)
         if d.dim() != 3 or d.shape[2] * 16 != self.page_size * self.head_dim * 17:
             raise ValueError(f"cache data is {tuple(d.shape)}: want (pages, kv_heads, page_size * head_dim * 17 / 16)")
-        return _ptr(d), d.shape[0], self.page_size, d.shape[1], self.head_dim
+        return _flat("cache", d, dev, _U8, d.shape), d.shape[0], self.page_size, d.shape[1], self.head_dim
 
 
 def kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, stream=None):
     """Quantize rows k, v (tokens, kv_heads, head_dim) into the cache's slots (tokens,) int64,
     page * page_size + place; a negative slot takes nothing."""
-    want = (k.shape[0] if k.dim() else 0, cache.data.shape[1], cache.head_dim)
-    _shaped("k", k, *want)
-    _shaped("v", v, *want)
-    _dtype("v", v, k.dtype)
-    _dtype("slots", slots, torch.int64)
-    _shaped("slots", slots, want[0])
-    dt = _act_dtype(k)
-    _check("cf_kv4_append", lib.cf_kv4_append(dt, _rows("k", k), _rows("v", v), _ptr(slots), want[0], *cache._args(),
-                                              _stream(stream)))
+    tokens = k.shape[0] if k.dim() == 3 else -1
+    want = (tokens, cache.data.shape[1], cache.head_dim)
+    dt, dev = _act_dtype(k), _device(k)
+    _shaped("k", k, k.dtype, want)
+    _shaped("v", v, k.dtype, want)
+    ps = _flat("slots", slots, dev, torch.int64, (tokens,))
+    rc = lib.cf_kv4_append(dt, _rows("k", k, dev), _rows("v", v, dev), ps, tokens, *cache._args(dev), _on(stream, dev))
+    if rc:
+        raise CFError("cf_kv4_append", rc)
 
 
 def kv4_read(cache: KV4Cache, slots: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
              k: torch.Tensor | None = None, v: torch.Tensor | None = None, stream=None):
     """The rows that the cache holds in slots (tokens,) int64, as (k, v) of (tokens, kv_heads,
     head_dim); zeros for slots that are not in the cache."""
-    if slots.dim() != 1:
-        raise ValueError("slots must be (tokens,)")
-    want = (slots.shape[0], cache.data.shape[1], cache.head_dim)
-    _dtype("slots", slots, torch.int64)
-    if k is None:
-        k = _keep_for(torch.empty(want, dtype=dtype, device=cache.data.device), stream)
-    if v is None:
-        v = _keep_for(torch.empty(want, dtype=k.dtype, device=cache.data.device), stream)
-    _shaped("k", k, *want)
-    _shaped("v", v, *want)
-    _dtype("v", v, k.dtype)
-    dt = _act_dtype(k)
-    _check("cf_kv4_read", lib.cf_kv4_read(dt, *cache._args(), _ptr(slots), want[0], _rows("k", k), _rows("v", v),
-                                          _stream(stream)))
+    tokens = slots.numel()
+    want = (tokens, cache.data.shape[1], cache.head_dim)
+    k = _new(cache.data, want, stream, dtype) if k is None else k
+    v = _new(cache.data, want, stream, k.dtype) if v is None else v
+    dt, dev = _act_dtype(k), _device(k)
+    _shaped("k", k, k.dtype, want)
+    _shaped("v", v, k.dtype, want)
+    ps = _flat("slots", slots, dev, torch.int64, (tokens,))
+    rc = lib.cf_kv4_read(dt, *cache._args(dev), ps, tokens, _rows("k", k, dev), _rows("v", v, dev), _on(stream, dev))
+    if rc:
+        raise CFError("cf_kv4_read", rc)
     return k, v
 
 
@@ -621,30 +654,35 @@ def kv4_attention(q: torch.Tensor, cache: KV4Cache, kv_lens: torch.Tensor, table
     total, heads, dim = q.shape
     if dim != cache.head_dim:
         raise ValueError(f"q has rows of {dim}, the cache of {cache.head_dim}")
-    dt = _act_dtype(q)
-    batch = kv_lens.shape[0] if kv_lens.dim() == 1 else -1
-    for nm, t, shape in (("kv_lens", kv_lens, (batch,)), ("q_starts", q_starts, (batch + 1,))):
-        _dtype(nm, t, torch.int32)
-        _shaped(nm, t, *shape)
+    dt, dev, kv_heads = _act_dtype(q), _device(q), cache.data.shape[1]
+    batch = kv_lens.numel()
+    if kv_lens.dtype != torch.int32:
+        raise TypeError(f"kv_lens is {kv_lens.dtype}; libcf wants torch.int32")
+    pt = None
     if table is not None:
-        _dtype("table", table, torch.int32)
         table_width = table.shape[-1]
-        _shaped("table", table, batch, table_width)
+        pt = _flat("table", table, dev, torch.int32, (batch, table_width))
+    pq = _flat("q_starts", q_starts, dev, torch.int32, (batch + 1,))
+    pe = _flat("lse", lse, dev, _F32, (total, heads))
+    pl = _flat("kv_lens", kv_lens, dev, torch.int32, (batch,))
     if out is None:
-        out = _keep_for(torch.empty((total, heads, dim), dtype=q.dtype, device=q.device), stream)
-    _dtype("out", out, q.dtype)
-    _shaped("out", out, total, heads, dim)
-    _dtype("lse", lse, _F32)
-    _shaped("lse", lse, total, heads)
+        out = _new(q, q.shape, stream)
+    else:
+        _shaped("out", out, q.dtype, q.shape)
     if workspace is None:
         most = max_q or (total if q_starts is not None else total // max(batch, 1))
-        need = lib.cf_kv4_attention_workspace_bytes(dt, most, heads, cache.data.shape[1], dim)
+        need = lib.cf_kv4_attention_workspace_bytes(dt, most, heads, kv_heads, dim)
         if need and total:
             # freed when this call returns, possibly before the launch stream has used it
-            workspace = _keep_for(torch.empty(need, dtype=_U8, device=q.device), stream)
-    _check("cf_kv4_attention", lib.cf_kv4_attention(
-        dt, _rows("q", q), total, heads, *cache._args(), batch, _ptr(table), table_width, _ptr(kv_lens),
-        _ptr(q_starts), max_q, CF_ATTN_CAUSAL if causal else 0, window, dim ** -0.5 if scale is None else scale,
-        _rows("out", out), _ptr(lse), _ptr(workspace),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)))
+            workspace = _new(q, need, stream, _U8)
+    pw, nw = None, 0
+    if workspace is not None:
+        nw = workspace.numel() * workspace.element_size()
+        pw = _flat("workspace", workspace, dev, workspace.dtype, workspace.shape)
+    rc = lib.cf_kv4_attention(
+        dt, _rows("q", q, dev), total, heads, *cache._args(dev), batch, pt, table_width, pl, pq, max_q,
+        CF_ATTN_CAUSAL if causal else 0, window, dim ** -0.5 if scale is None else scale, _rows("out", out, dev), pe,
+        pw, nw, _on(stream, dev))
+    if rc:
+        raise CFError("cf_kv4_attention", rc)
     return out

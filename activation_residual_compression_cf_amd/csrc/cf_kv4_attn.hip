@@ -49,6 +49,10 @@ constexpr int kUnit = 32;  // keys
 // Workgroups of a call: what is resident on 256 compute units, more where a workgroup's
 // registers allow it.
 constexpr int kGroupsSmall = 1024, kGroupsLarge = 256;
+#ifndef KWB
+#define KWB 1
+#endif
+constexpr int kWideBlocks = KWB;
 // A workgroup takes at least so many units, or joining would cost more than it saves.
 constexpr int kMinUnits = 8;
 // p = 2^(x - m + kLift) where m is at most kSlack below the row's largest score so far: the
@@ -122,13 +126,13 @@ __device__ __forceinline__ int token_of(const AttnArgs& p, int row) {
 }
 
 // Units [u0, u0 + n) of an item; at least one, so that rows that see nothing are written too.
-template <int ROWS>
+template <int ROWS, int UNIT>
 __device__ __forceinline__ int units_of(const AttnArgs& p, const Seq& s, int tile, int* u0) {
     const int rows = s.nq * p.share;
     const int lo = seen_lo(p, s, token_of(p, tile * ROWS));
     const int hi = seen_hi(p, s, token_of(p, min(tile * ROWS + ROWS, rows) - 1));
-    *u0 = lo / kUnit;
-    return max((hi + kUnit - 1) / kUnit - *u0, 1);
+    *u0 = lo / UNIT;
+    return max((hi + UNIT - 1) / UNIT - *u0, 1);
 }
 
 template <int ROWS>
@@ -164,7 +168,7 @@ struct Place {
 };
 
 // Every wave works it out by itself: a group of lanes takes a sequence and shares its tiles.
-template <int ROWS, int PAD>
+template <int ROWS, int UNIT, int PAD>
 __device__ __forceinline__ bool place_of(const AttnArgs& p, int me, Place* x) {
     const int lane = threadIdx.x & 63;
     int sub = 64;  // lanes of a sequence
@@ -176,7 +180,7 @@ __device__ __forceinline__ bool place_of(const AttnArgs& p, int me, Place* x) {
             const Seq s = seq_of(p, b);
             const int tiles = tiles_of<ROWS>(p, s);
             int u0;
-            for (int i = lane & (sub - 1); i < tiles; i += sub) n += units_of<ROWS>(p, s, i, &u0) + PAD;
+            for (int i = lane & (sub - 1); i < tiles; i += sub) n += units_of<ROWS, UNIT>(p, s, i, &u0) + PAD;
         }
         for (int d = 1; d < sub; d <<= 1) n += shfl64(n, lane ^ d);
         return n;
@@ -189,7 +193,7 @@ __device__ __forceinline__ bool place_of(const AttnArgs& p, int me, Place* x) {
         total += uniform(shfl64(sum, 63));
     }
     int64_t chunk = (total + p.groups - 1) / p.groups;
-    chunk = max(chunk, int64_t(kMinUnits + PAD));
+    chunk = max(chunk, int64_t(kMinUnits * kUnit / UNIT + PAD));
     x->chunk = chunk;
     x->at = me * chunk;
     x->end = min(x->at + chunk, total);
@@ -218,7 +222,7 @@ __device__ __forceinline__ bool place_of(const AttnArgs& p, int me, Place* x) {
     const int tiles = tiles_of<ROWS>(p, s);
     for (int t0 = 0;; t0 += 64) {
         int u0;
-        const int cost = t0 + lane < tiles ? units_of<ROWS>(p, s, t0 + lane, &u0) + PAD : 0;
+        const int cost = t0 + lane < tiles ? units_of<ROWS, UNIT>(p, s, t0 + lane, &u0) + PAD : 0;
         const int64_t upto = wave_scan(cost);
         const int64_t all = uniform(shfl64(upto, 63));
         if (rest < all) {
@@ -405,14 +409,14 @@ __global__ __launch_bounds__(kThreads, NQ == 1 ? 2 : 1) void attn_kernel(const A
 
     if (threadIdx.x == 0) p.joins[me * 4] = -1;
     Place w;
-    if (!place_of<kRows, kPad>(p, me, &w)) return;
+    if (!place_of<kRows, kUnit, kPad>(p, me, &w)) return;
     const Offsets offs = offsets_of<D>(p);
     Seq s = seq_at(p, w.b);
 
     while (w.at < w.end) {
         // units [a, z) of this item
         int u0;
-        const int count = units_of<kRows>(p, s, w.tile, &u0);
+        const int count = units_of<kRows, kUnit>(p, s, w.tile, &u0);
         const int64_t take = min(w.end - w.at, count + kPad - w.rest);
         const int a = max(static_cast<int>(w.rest) - kPad, 0), z = static_cast<int>(w.rest + take) - kPad;
         w.at += take;
@@ -711,6 +715,398 @@ __global__ __launch_bounds__(kThreads, NQ == 1 ? 2 : 1) void attn_kernel(const A
     }
 }
 
+
+// ---- many rows ------------------------------------------------------------------------
+
+typedef float vf16 __attribute__((ext_vector_type(16)));
+
+// Four waves, each with 32 * QB rows of its own, over tiles of 64 keys that all of them
+// decode once, into shared memory: K as bf16 [key][channel], V as fp16 [channel][key].
+template <typename T, int D, int QB>
+struct Wide {
+    static constexpr int kParts = sizeof(T) == 4 ? 3 : 1;
+    static constexpr int kP = sizeof(T) == 4 ? 2 : 1;
+    static constexpr int kRows = 32 * QB * kWaves;
+    static constexpr int kKeys = 64;
+    static constexpr int kResident = QB == 1 && (sizeof(T) == 2 || D == 64) ? 2 : 1;  // workgroups of a compute unit
+    static constexpr int kPad = 2;
+    // rows of shared memory are 16 bytes longer than they need to be: 32 rows then start on
+    // 32 different groups of banks
+    static constexpr int kKRow = 2 * D + 16, kVRow = 2 * kKeys + 16;
+    static constexpr int kTile = kKeys * kKRow + D * kVRow;
+    static constexpr int kBytes = 2 * kTile;
+};
+
+// A thread's share of a tile: D/4 codes of a key, and four keys of a channel piece.
+template <int D>
+struct Share {
+    uint32_t k[D / 32], v[D / 32];
+    uint32_t ks, vs;  // scale bytes: one, and four
+    bool k_on, v_on;  // the keys have a page
+};
+
+// The pages of a tile's four runs of 16 keys, a lane each.
+__device__ __forceinline__ int64_t tile_page(const AttnArgs& p, const Seq& s, int b, int key) {
+    const int i = min(key, max(s.len - 1, 0)) >> p.cache.shift;
+    const int64_t at = int64_t(b) * p.width + i;
+    return p.table ? p.table[at] : at;
+}
+
+template <int D>
+__device__ __forceinline__ void load_share(Share<D>& x, const AttnArgs& p, const Seq& s, int b, int head, int key0) {
+    const KvBlock blk{p.cache.block.page, D};
+    const int mask = blk.page - 1;
+    const auto block_of = [&](int key, bool* on) {
+        const int64_t at = tile_page(p, s, b, key);
+        *on = s.len > 0 && at >= 0 && at < p.cache.pages;
+        return static_cast<const uint8_t*>(p.cache.at(*on ? at : 0, head));
+    };
+    {
+        const int key = key0 + threadIdx.x / 4, c = threadIdx.x & 3;
+        const uint8_t* const base = block_of(key, &x.k_on);
+        const uint8_t* const w = base + blk.k_code(key & mask) + c * (D / 8);
+#pragma unroll
+        for (int i = 0; i < D / 32; i += 2) {
+            const vu2 y = *reinterpret_cast<const vu2*>(w + 4 * i);
+            x.k[i] = y.x, x.k[i + 1] = y.y;
+        }
+        x.ks = base[blk.k_scale(key & mask, c * (D / 4) / kKvGroup)];
+        x.k_on = x.k_on && key < s.len;
+    }
+    {
+        // half a piece: keys 4 h .. of the eight
+        const int key = key0 + threadIdx.x / 32 * 8 + (threadIdx.x & 1) * 4, n = threadIdx.x / 2 & 15;
+        const uint8_t* const base = block_of(key, &x.v_on);
+        const uint8_t* const w = base + blk.v_code(key & mask, n);
+#pragma unroll
+        for (int i = 0; i < D / 32; i += 2) {
+            const vu2 y = *reinterpret_cast<const vu2*>(w + 4 * i);
+            x.v[i] = y.x, x.v[i + 1] = y.y;
+        }
+        x.vs = *reinterpret_cast<const uint32_t*>(base + blk.v_scale(key & mask, n * (D / 16) / kKvGroup));
+        if (!x.v_on) x.vs = 0x7f7f7f7fu;
+    }
+}
+
+// Decodes a share into a tile; keys behind the last become zeros whatever their bytes.  Returns
+// whether a group reads NaN (and holds zeros in the tile).
+template <int D>
+__device__ __forceinline__ bool store_share(Share<D>& x, uint8_t* tile, int key0, int len) {
+    using W = Wide<__bf16, D, 1>;
+    bool nan = false;
+    {
+        uint32_t ks = x.k_on ? x.ks : 127u;
+        const bool bad = ks >= kKvNanFrom;
+        nan |= bad;
+        const float f = scale_of(bad ? 127u : ks);
+        uint8_t* const w = tile + (threadIdx.x / 4) * W::kKRow + (threadIdx.x & 3) * (D / 2);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+            const uint32_t c = x.k_on && !bad ? x.k[i] : 0u;
+            *reinterpret_cast<vu4*>(w + 16 * i) = vu4{to_bf16<0>(c, f), to_bf16<1>(c, f), to_bf16<2>(c, f), to_bf16<3>(c, f)};
+        }
+    }
+    {
+        const int in = threadIdx.x / 32 * 8 + (threadIdx.x & 1) * 4, n = threadIdx.x / 2 & 15;
+        uint32_t v[4];  // the channels of a key
+        float f[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            uint32_t byte = x.vs >> (8 * t) & 0xffu;
+            const bool on = x.v_on && key0 + in + t < len;
+            const bool bad = on && byte >= kKvNanFrom;
+            nan |= bad;
+            if constexpr (D == 128)
+                v[t] = on && !bad ? x.v[t] : 0u;
+            else
+                v[t] = on && !bad ? x.v[t / 2] >> (16 * (t & 1)) : 0u;
+            f[t] = scale_of(on && !bad ? byte : 127u);
+        }
+        uint8_t* const w = tile + W::kKeys * W::kKRow + (n * (D / 16)) * W::kVRow + in * 2;
+        const auto pair = [&](int j, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+            *reinterpret_cast<vu2*>(w + 2 * j * W::kVRow) =
+                vu2{__builtin_amdgcn_perm(b, a, 0x05040100u), __builtin_amdgcn_perm(d, c, 0x05040100u)};
+            *reinterpret_cast<vu2*>(w + (2 * j + 1) * W::kVRow) =
+                vu2{__builtin_amdgcn_perm(b, a, 0x07060302u), __builtin_amdgcn_perm(d, c, 0x07060302u)};
+        };
+        pair(0, to_f16<0>(v[0], f[0]), to_f16<0>(v[1], f[1]), to_f16<0>(v[2], f[2]), to_f16<0>(v[3], f[3]));
+        pair(1, to_f16<1>(v[0], f[0]), to_f16<1>(v[1], f[1]), to_f16<1>(v[2], f[2]), to_f16<1>(v[3], f[3]));
+        if constexpr (D == 128) {
+            pair(2, to_f16<2>(v[0], f[0]), to_f16<2>(v[1], f[1]), to_f16<2>(v[2], f[2]), to_f16<2>(v[3], f[3]));
+            pair(3, to_f16<3>(v[0], f[0]), to_f16<3>(v[1], f[1]), to_f16<3>(v[2], f[2]), to_f16<3>(v[3], f[3]));
+        }
+    }
+    return nan;
+}
+
+// Scale byte of a key's channel group, read again: for the tiles where some group reads NaN.
+template <int D>
+__device__ __forceinline__ bool reads_nan(const AttnArgs& p, const Seq& s, int b, int head, int key, int group, bool v) {
+    if (key >= s.len) return false;
+    const KvBlock blk{p.cache.block.page, D};
+    const int64_t at = tile_page(p, s, b, key);
+    if (at < 0 || at >= p.cache.pages) return false;
+    const int in = key & (blk.page - 1);
+    return p.cache.at(at, head)[v ? blk.v_scale(in, group) : blk.k_scale(in, group)] >= kKvNanFrom;
+}
+
+// A wave's 16 x 16 matrix products of before are 32 x 32 with 16 terms here: lane = 32 h + n
+// has row n of a block, and of 32 keys 8 h .. 8 h + 7 and 16 + 8 h .. , K's rows being
+// taken in the order that makes it so.
+template <typename T, int D, int QB>
+__global__ __launch_bounds__(kThreads, (Wide<T, D, QB>::kResident)) void wide_kernel(const AttnArgs p) {
+    using W = Wide<T, D, QB>;
+    constexpr int kRows = W::kRows, kPad = W::kPad, kParts = W::kParts, kP = W::kP, kKeys = W::kKeys;
+    constexpr int kDt = D / 32;
+    const int lane = threadIdx.x & 63, wave = uniform(static_cast<int>(threadIdx.x) >> 6), n = lane & 31, h = lane >> 5;
+    const int me = (blockIdx.x & 7) * (p.groups >> 3) + (blockIdx.x >> 3);
+    __shared__ __align__(16) uint8_t lds[W::kBytes];
+    __shared__ uint32_t flag[2][kWaves];
+
+    if (threadIdx.x == 0) p.joins[me * 4] = -1;
+    Place w;
+    if (!place_of<kRows, kKeys, kPad>(p, me, &w)) return;
+    Seq s = seq_at(p, w.b);
+    // key of row n of K's fragments
+    const int k_row = 16 * (n >> 4) + 8 * ((n >> 2) & 1) + 4 * ((n >> 3) & 1) + (n & 3);
+
+    while (w.at < w.end) {
+        int u0;
+        const int count = units_of<kRows, kKeys>(p, s, w.tile, &u0);
+        const int64_t take = min(w.end - w.at, count + kPad - w.rest);
+        const int a = max(static_cast<int>(w.rest) - kPad, 0), z = static_cast<int>(w.rest + take) - kPad;
+        w.at += take;
+        if (z <= 0) break;  // the next workgroup begins this item
+        const int rows = s.nq * p.share;
+        const int row0 = w.tile * kRows + wave * 32 * QB;
+        const int head = w.head;
+
+        Share<D> next;
+        load_share<D>(next, p, s, w.b, head, (u0 + a) * kKeys);
+
+        vb8 q[QB][kParts][D / 16];
+        int lo[QB], hi[QB];
+        int full_lo = 0, full_hi = INT32_MAX;
+        {
+            const int last = min(row0 + 32 * QB, rows) - 1;
+            if (last >= row0) {
+                full_lo = seen_lo(p, s, token_of(p, last));
+                full_hi = seen_hi(p, s, token_of(p, row0));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < QB; ++i) {
+            const int row = row0 + i * 32 + n;
+            const bool on = row < rows;
+            const int token = on ? token_of(p, row) : 0;
+            const T* const src = row_ptr<T>(p.q, s.q0 + token, head * p.share + (on ? row : 0) - token * p.share);
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+                float f[8];
+                if (on) {
+                    Row8<T> r;
+                    r.load(src + 16 * c + 8 * h);
+                    r.get(f);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    float rest = on ? f[j] : 0.f;
+#pragma unroll
+                    for (int k = 0; k < kParts; ++k) {
+                        const __bf16 y = static_cast<__bf16>(rest);
+                        q[i][k][c][j] = y;
+                        rest -= static_cast<float>(y);
+                    }
+                }
+            }
+            lo[i] = on ? seen_lo(p, s, token) : 0;
+            hi[i] = on ? seen_hi(p, s, token) : 0;
+        }
+
+        vf16 o[QB][kDt];
+        float m[QB], sum[QB];
+#pragma unroll
+        for (int i = 0; i < QB; ++i) {
+            m[i] = kNone, sum[i] = 0.f;
+#pragma unroll
+            for (int j = 0; j < kDt; ++j)
+#pragma unroll
+                for (int k = 0; k < 16; ++k) o[i][j][k] = 0.f;
+        }
+
+        __syncthreads();  // the last item's tiles have been read
+        {
+            const bool nan = store_share<D>(next, lds, (u0 + a) * kKeys, s.len);
+            const bool any = __any(nan);
+            if (lane == 0) flag[0][wave] = any;
+        }
+        if (a + 1 < z) load_share<D>(next, p, s, w.b, head, (u0 + a + 1) * kKeys);
+        __syncthreads();
+
+        for (int u = a; u < z; ++u) {
+            const int buf = (u - a) & 1;
+            const uint8_t* const kt = lds + buf * W::kTile;
+            const uint8_t* const vt = kt + kKeys * W::kKRow;
+            const int key0 = (u0 + u) * kKeys;
+            uint32_t pages_on = 15;  // runs of 16 keys that have a page
+            if (p.table || s.len == 0) {
+                const int64_t at = tile_page(p, s, w.b, key0 + 16 * (lane & 3));
+                pages_on = static_cast<uint32_t>(__ballot(s.len > 0 && at >= 0 && at < p.cache.pages)) & 15u;
+            }
+            const bool edge = key0 < full_lo || key0 + kKeys > full_hi || pages_on != 15;
+            const bool nans = (flag[buf][0] | flag[buf][1] | flag[buf][2] | flag[buf][3]) != 0;
+
+            vf16 sc[2][QB];
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+#pragma unroll
+                for (int i = 0; i < QB; ++i)
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) sc[g][i][k] = 0.f;
+#pragma unroll
+                for (int k = kParts - 1; k >= 0; --k)
+#pragma unroll
+                    for (int c = 0; c < D / 16; ++c) {
+                        const vb8 kf = *reinterpret_cast<const vb8*>(kt + (32 * g + k_row) * W::kKRow + 32 * c + 16 * h);
+#pragma unroll
+                        for (int i = 0; i < QB; ++i)
+                            sc[g][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, q[i][k][c], sc[g][i], 0, 0, 0);
+                    }
+            }
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                vh8 pf[QB][kP][2];
+#pragma unroll
+                for (int i = 0; i < QB; ++i) {
+                    // score r is of key mine0 + 16 * (r / 8) + r % 8
+                    const int mine0 = key0 + 32 * g + 8 * h;
+                    if (nans) {
+                        for (int r = 0; r < 16; ++r)
+                            for (int c = 0; c < D / kKvGroup; ++c)
+                                if (reads_nan<D>(p, s, w.b, head, mine0 + 16 * (r / 8) + r % 8, c, false)) {
+#pragma unroll
+                                    for (int k = 0; k < 16; ++k)
+                                        if (k == r) sc[g][i][k] = __builtin_nanf("");
+                                }
+                    }
+                    if (edge) {
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) {
+                            const int key = mine0 + 16 * (r / 8) + r % 8;
+                            if (!(pages_on >> (2 * g + r / 8) & 1u) || key < lo[i] || key >= hi[i]) sc[g][i][r] = kNone;
+                        }
+                    }
+                    float top = kNone;
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) top = fmaxf(top, sc[g][i][r]);
+                    top *= p.scale_log2;
+                    if (__any(top > m[i] + (kSlack + kLift))) {
+                        const float r = fmaxf(fmaxf(top, __shfl_xor(top, 32, 64)) - kLift, m[i]);
+                        const float f = m[i] == r ? 1.f : __builtin_amdgcn_exp2f(m[i] - r);
+                        m[i] = r;
+                        sum[i] *= f;
+#pragma unroll
+                        for (int j = 0; j < kDt; ++j) o[i][j] *= f;
+                    }
+                    const float ref = m[i] == kNone ? 0.f : -m[i];
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[g][i][r], p.scale_log2, ref));
+                        sum[i] += e;
+                        const _Float16 y = static_cast<_Float16>(e);
+                        pf[i][0][r / 8][r % 8] = y;
+                        if constexpr (kP == 2) pf[i][1][r / 8][r % 8] = static_cast<_Float16>(e - static_cast<float>(y));
+                    }
+                    if (nans) {
+                        // a NaN of V reaches the rows that see its key, and only those
+                        for (int t = 0; t < 32; ++t) {
+                            const int key = key0 + 32 * g + t;
+                            if (key < lo[i] || key >= hi[i]) continue;
+#pragma unroll
+                            for (int j = 0; j < kDt; ++j)
+                                if (reads_nan<D>(p, s, w.b, head, key, j, true))
+#pragma unroll
+                                    for (int k = 0; k < 16; ++k) o[i][j][k] = __builtin_nanf("");
+                        }
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < kDt; ++j)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const vh8 vf = *reinterpret_cast<const vh8*>(vt + (32 * j + n) * W::kVRow + 2 * (32 * g + 16 * t + 8 * h));
+#pragma unroll
+                        for (int i = 0; i < QB; ++i)
+#pragma unroll
+                            for (int k = kP - 1; k >= 0; --k)
+                                o[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, pf[i][k][t], o[i][j], 0, 0, 0);
+                    }
+            }
+            if (u + 1 < z) {
+                const bool nan = store_share<D>(next, lds + (buf ^ 1) * W::kTile, key0 + kKeys, s.len);
+                const bool any = __any(nan);
+                if (lane == 0) flag[buf ^ 1][wave] = any;
+                if (u + 2 < z) load_share<D>(next, p, s, w.b, head, key0 + 2 * kKeys);
+                __syncthreads();
+            }
+        }
+
+        const bool whole = a == 0 && z == count;
+        float* const part = p.part + (2 * int64_t(me) + (a == 0)) * part_floats<D>(kRows);
+#pragma unroll
+        for (int i = 0; i < QB; ++i) {
+            const float l = sum[i] + __shfl_xor(sum[i], 32, 64);
+            const int r = wave * 32 * QB + i * 32 + n, row = w.tile * kRows + r;
+            if (row >= rows) continue;
+            const int token = token_of(p, row), qh = head * p.share + row - token * p.share;
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            T* const dst = row_ptr<T>(p.out, s.q0 + token, qh);
+            float* const y = part + int64_t(r) * (D + 2);
+            // registers 4 k .. are channels 8 k + 4 h ..
+#pragma unroll
+            for (int j = 0; j < kDt; ++j)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int c = 32 * j + 8 * k + 4 * h;
+                    if (whole) {
+                        if constexpr (sizeof(T) == 2) {
+                            *reinterpret_cast<vb2*>(dst + c) = vb2{static_cast<__bf16>(o[i][j][4 * k] * inv), static_cast<__bf16>(o[i][j][4 * k + 1] * inv)};
+                            *reinterpret_cast<vb2*>(dst + c + 2) = vb2{static_cast<__bf16>(o[i][j][4 * k + 2] * inv), static_cast<__bf16>(o[i][j][4 * k + 3] * inv)};
+                        } else {
+                            *reinterpret_cast<vf4*>(dst + c) = vf4{o[i][j][4 * k], o[i][j][4 * k + 1], o[i][j][4 * k + 2], o[i][j][4 * k + 3]} * inv;
+                        }
+                    } else {
+                        *reinterpret_cast<float2*>(y + c) = float2{o[i][j][4 * k], o[i][j][4 * k + 1]};
+                        *reinterpret_cast<float2*>(y + c + 2) = float2{o[i][j][4 * k + 2], o[i][j][4 * k + 3]};
+                    }
+                }
+            if (h == 0) {
+                if (!whole)
+                    *reinterpret_cast<float2*>(y + D) = float2{m[i], l};
+                else if (p.lse)
+                    p.lse[int64_t(s.q0 + token) * p.q_heads + qh] =
+                        l == 0.f ? kNone : (m[i] + __builtin_amdgcn_logf(l)) * 0.693147180559945309f;
+            }
+        }
+        if (threadIdx.x == 0 && a > 0 && z == count) {
+            int32_t* const j = p.joins + me * 4;
+            j[1] = w.b, j[2] = head, j[3] = w.tile;
+            j[0] = static_cast<int32_t>((w.at - count) / w.chunk);
+        }
+
+        w.rest = 0;
+        if (w.at >= w.end) break;
+        if (++w.tile >= tiles_of<kRows>(p, s)) {
+            w.tile = 0;
+            if (++w.head >= p.cache.heads) {
+                w.head = 0;
+                do s = seq_at(p, ++w.b);  // at < end <= total: another sequence has units
+                while (s.nq == 0);
+            }
+        }
+    }
+}
+
 // Joins the parts of the items that ended up in several workgroups: block (w, y) some rows
 // of the item whose last keys were workgroup w's.
 template <typename T, int D, int ROWS>
@@ -779,12 +1175,15 @@ struct Plan {
     size_t bytes;
 };
 
+constexpr int wide_blocks(int esz, int dim) { return esz == 4 ? 1 : kWideBlocks; }
+constexpr int wide_rows(int a_dtype, int dim) { return 128 * wide_blocks(a_dtype == CF_F32 ? 4 : 2, dim); }
+
 // The kernel for a call: rows is the number of rows that the longest sequence has.
 Plan plan_of(int a_dtype, int head_dim, int64_t rows) {
-    const int large = a_dtype == CF_F32 ? 128 : 256;
+    const int large = wide_rows(a_dtype, head_dim);
     Plan x;
     x.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : large;
-    x.groups = x.rows == 16 ? kGroupsSmall : x.rows == 32 ? kGroupsSmall / 2 : kGroupsLarge;
+    x.groups = x.rows == 16 ? kGroupsSmall : x.rows == 32 ? kGroupsSmall / 2 : (large == 128 && (a_dtype == CF_BF16 || head_dim == 64) ? 2 : 1) * kGroupsLarge;
     const int64_t floats = head_dim == 64 ? part_floats<64>(x.rows) : part_floats<128>(x.rows);
     x.bytes = size_t(x.groups) * (2 * floats * 4 + 16);
     return x;
@@ -802,10 +1201,14 @@ hipError_t launch(const AttnArgs& p, int64_t max_rows, hipStream_t stream) {
 
 template <typename T, int D>
 hipError_t launch_rows(int rows, const AttnArgs& p, int64_t max_rows, hipStream_t stream) {
-    constexpr int kWide = sizeof(T) == 4 ? 2 : 4;
+    constexpr int kQB = wide_blocks(sizeof(T), D);
     if (rows == 16) return launch<T, D, 1, true>(p, max_rows, stream);
     if (rows == 32) return launch<T, D, 2, true>(p, max_rows, stream);
-    return launch<T, D, kWide, false>(p, max_rows, stream);
+    constexpr int kRows = Wide<T, D, kQB>::kRows, kJoinRows = kThreads / (D / 4);
+    wide_kernel<T, D, kQB><<<p.groups, kThreads, 0, stream>>>(p);
+    if (hipError_t e = hipGetLastError()) return e;
+    join_kernel<T, D, kRows><<<dim3(p.groups, kRows / kJoinRows), kThreads, 0, stream>>>(p);
+    return hipGetLastError();
 }
 
 }  // namespace

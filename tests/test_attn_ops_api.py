@@ -213,9 +213,9 @@ def test_binding_refuses(cf):
     with pytest.raises(ValueError, match="v is"):
         cf.kv4_append(cache, x, x[:, :1], slots)
     with pytest.raises(ValueError, match="cache data"):
-        cf.KV4Cache(cache.data, 32, 64)._args()
+        cf.KV4Cache(cache.data, 32, 64)._args(-2)
     with pytest.raises(TypeError, match="cache"):
-        cf.KV4Cache(cache.data.to(torch.int8), 16, 64)._args()
+        cf.KV4Cache(cache.data.to(torch.int8), 16, 64)._args(-2)
     lens = torch.zeros(1, dtype=torch.int32)
     with pytest.raises(TypeError, match="kv_lens"):
         cf.kv4_attention(x, cache, lens.long())
