@@ -495,7 +495,7 @@ int cf_qk_norm_rope(int a_dtype, int64_t tokens, int q_heads, int k_heads, int h
 }
 
 int64_t cf_kv4_cache_bytes(int64_t pages, int page_size, int kv_heads, int head_dim) {
-    if (!kv4_dims(page_size, kv_heads, head_dim) || pages < 1) return CF_E_SHAPE;
+    if (!kv4_dims(page_size, kv_heads, head_dim) || pages < 1 || pages > INT32_MAX) return CF_E_SHAPE;
     const wide bytes = wide(pages) * kv_heads * page_size * head_dim * 17 / 16;
     return bytes <= kMaxExtent ? static_cast<int64_t>(bytes) : CF_E_SHAPE;
 }

@@ -257,6 +257,10 @@ __device__ __forceinline__ uint32_t to_f16(uint32_t c, float s) {
 
 __device__ __forceinline__ float scale_of(uint32_t byte) { return __uint_as_float(byte << 23); }
 
+__device__ __forceinline__ bool page_on(const AttnArgs& p, const Seq& s, int page) {
+    return s.len > 0 && static_cast<uint32_t>(page) < static_cast<uint32_t>(p.cache.pages);
+}
+
 // One wave's share of 32 keys, as loaded.
 template <int D>
 struct Keys {
@@ -269,7 +273,7 @@ struct Keys {
 
 // The two pages of a unit's first and last 16 keys (one page, where it has 32 tokens or more).
 struct Pages {
-    int64_t at[2];
+    int at[2];
 };
 
 __device__ __forceinline__ Pages pages_of(const AttnArgs& p, const Seq& s, int b, int unit) {
@@ -279,7 +283,7 @@ __device__ __forceinline__ Pages pages_of(const AttnArgs& p, const Seq& s, int b
         // keys behind the last are read from its page (and masked later): always inside the cache
         const int i = min(unit * kUnit + 16 * h, max(s.len - 1, 0)) >> p.cache.shift;
         const int64_t at = int64_t(b) * p.width + i;
-        x.at[h] = p.table ? scalar_load(p.table + at) : at;
+        x.at[h] = p.table ? scalar_load(p.table + at) : static_cast<int>(at);
     }
     return x;
 }
@@ -312,7 +316,7 @@ __device__ __forceinline__ void load_keys(Keys<D>& x, const AttnArgs& p, const S
     const uint8_t* base[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        x.ok[h] = s.len > 0 && pages.at[h] >= 0 && pages.at[h] < p.cache.pages;
+        x.ok[h] = page_on(p, s, pages.at[h]);
         base[h] = p.cache.at(x.ok[h] ? pages.at[h] : 0, head);
     }
     const uint8_t* const kb = lane & 8 ? base[1] : base[0];
@@ -737,92 +741,99 @@ struct Wide {
     static constexpr int kBytes = 2 * kTile;
 };
 
-// A thread's share of a tile: D/4 codes of a key, and four keys of a channel piece.
+// A thread's share of a tile: D/4 codes of a key, and four keys of a channel piece.  Its wave's
+// threads share 16 keys, and so one page.
 template <int D>
 struct Share {
     uint32_t k[D / 32], v[D / 32];
     uint32_t ks, vs;  // scale bytes: one, and four
-    bool k_on, v_on;  // the keys have a page
+    bool on;          // the keys have a page
 };
 
-// The pages of a tile's four runs of 16 keys, a lane each.
-__device__ __forceinline__ int64_t tile_page(const AttnArgs& p, const Seq& s, int b, int key) {
-    const int i = min(key, max(s.len - 1, 0)) >> p.cache.shift;
-    const int64_t at = int64_t(b) * p.width + i;
-    return p.table ? p.table[at] : at;
+// The page of a key (the last key's behind it: always inside the cache, and masked later).
+__device__ __forceinline__ int page_at(const AttnArgs& p, const Seq& s, int b, int key) {
+    const int64_t at = int64_t(b) * p.width + (min(key, max(s.len - 1, 0)) >> p.cache.shift);
+    return p.table ? scalar_load(p.table + at) : static_cast<int>(at);  // at < pages < 2^31 without a table
 }
 
+// Where a thread's share lies in a page's block, from its wave's first key on.
 template <int D>
-__device__ __forceinline__ void load_share(Share<D>& x, const AttnArgs& p, const Seq& s, int b, int head, int key0) {
+__device__ __forceinline__ Offsets share_offsets(const AttnArgs& p) {
+    const int lane = threadIdx.x & 63;
     const KvBlock blk{p.cache.block.page, D};
-    const int mask = blk.page - 1;
-    const auto block_of = [&](int key, bool* on) {
-        const int64_t at = tile_page(p, s, b, key);
-        *on = s.len > 0 && at >= 0 && at < p.cache.pages;
-        return static_cast<const uint8_t*>(p.cache.at(*on ? at : 0, head));
-    };
-    {
-        const int key = key0 + threadIdx.x / 4, c = threadIdx.x & 3;
-        const uint8_t* const base = block_of(key, &x.k_on);
-        const uint8_t* const w = base + blk.k_code(key & mask) + c * (D / 8);
-#pragma unroll
-        for (int i = 0; i < D / 32; i += 2) {
-            const vu2 y = *reinterpret_cast<const vu2*>(w + 4 * i);
-            x.k[i] = y.x, x.k[i + 1] = y.y;
-        }
-        x.ks = base[blk.k_scale(key & mask, c * (D / 4) / kKvGroup)];
-        x.k_on = x.k_on && key < s.len;
-    }
-    {
-        // half a piece: keys 4 h .. of the eight
-        const int key = key0 + threadIdx.x / 32 * 8 + (threadIdx.x & 1) * 4, n = threadIdx.x / 2 & 15;
-        const uint8_t* const base = block_of(key, &x.v_on);
-        const uint8_t* const w = base + blk.v_code(key & mask, n);
-#pragma unroll
-        for (int i = 0; i < D / 32; i += 2) {
-            const vu2 y = *reinterpret_cast<const vu2*>(w + 4 * i);
-            x.v[i] = y.x, x.v[i + 1] = y.y;
-        }
-        x.vs = *reinterpret_cast<const uint32_t*>(base + blk.v_scale(key & mask, n * (D / 16) / kKvGroup));
-        if (!x.v_on) x.vs = 0x7f7f7f7fu;
-    }
+    Offsets o;
+    o.k = blk.k_code(lane / 4) + (lane & 3) * (D / 8);
+    o.ks = blk.k_scale(lane / 4, (lane & 3) * (D / 4) / kKvGroup);
+    // half a piece: keys 4 h .. of the eight
+    const int key = lane / 32 * 8 + (lane & 1) * 4, n = lane / 2 & 15;
+    o.v = blk.v_code(key, n);
+    o.vs = blk.v_scale(key, n * (D / 16) / kKvGroup);
+    return o;
 }
 
-// Decodes a share into a tile; keys behind the last become zeros whatever their bytes.  Returns
-// whether a group reads NaN (and holds zeros in the tile).
+// key: the wave's first.
 template <int D>
-__device__ __forceinline__ bool store_share(Share<D>& x, uint8_t* tile, int key0, int len) {
+__device__ __forceinline__ void load_share(Share<D>& x, const AttnArgs& p, const Seq& s, int page, const Offsets& o,
+                                           int head, int key) {
+    x.on = page_on(p, s, page);
+    const uint8_t* const base = p.cache.at(x.on ? page : 0, head);
+    const int in = key & (p.cache.block.page - 1);
+    const uint8_t* const kc = base + in * (D / 2) + o.k;
+    const uint8_t* const vc = base + in * (D / 2) + o.v;
+#pragma unroll
+    for (int i = 0; i < D / 32; i += 2) {
+        const vu2 y = *reinterpret_cast<const vu2*>(kc + 4 * i), z = *reinterpret_cast<const vu2*>(vc + 4 * i);
+        x.k[i] = y.x, x.k[i + 1] = y.y;
+        x.v[i] = z.x, x.v[i + 1] = z.y;
+    }
+    x.ks = base[in * (D / 32) + o.ks];
+    x.vs = *reinterpret_cast<const uint32_t*>(base + in * (D / 32) + o.vs);
+}
+
+// Decodes a share into a tile, of whose keys the sequence has the first `left`.  Keys behind them
+// become zeros whatever their bytes, and so do groups that read NaN; returns whether the
+// wave has any of those.
+template <int D>
+__device__ __forceinline__ bool store_share(Share<D>& x, uint8_t* tile, int left) {
     using W = Wide<__bf16, D, 1>;
+    const int kin = threadIdx.x / 4, vin = threadIdx.x / 32 * 8 + (threadIdx.x & 1) * 4, n = threadIdx.x / 2 & 15;
+    uint32_t v[4];  // the channels of a key
+#pragma unroll
+    for (int t = 0; t < 4; ++t) v[t] = D == 128 ? x.v[t] : x.v[t / 2] >> (16 * (t & 1));
     bool nan = false;
+    if (!x.on || left < W::kKeys || __any(x.ks >= kKvNanFrom || (x.vs & x.vs << 1 & 0x80808080u) != 0)) {
+        const bool on = x.on && kin < left;
+        nan = on && x.ks >= kKvNanFrom;
+        if (!on || nan) {
+            x.ks = 127u;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) x.k[i] = 0;
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const bool on = x.on && vin + t < left;
+            const bool bad = on && (x.vs >> (8 * t) & 0xffu) >= kKvNanFrom;
+            nan |= bad;
+            if (on && !bad) continue;
+            x.vs = (x.vs & ~(0xffu << (8 * t))) | 127u << (8 * t);
+            v[t] = 0;
+        }
+        nan = __any(nan);
+    }
     {
-        uint32_t ks = x.k_on ? x.ks : 127u;
-        const bool bad = ks >= kKvNanFrom;
-        nan |= bad;
-        const float f = scale_of(bad ? 127u : ks);
-        uint8_t* const w = tile + (threadIdx.x / 4) * W::kKRow + (threadIdx.x & 3) * (D / 2);
+        const float f = scale_of(x.ks);
+        uint8_t* const w = tile + kin * W::kKRow + (threadIdx.x & 3) * (D / 2);
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
-            const uint32_t c = x.k_on && !bad ? x.k[i] : 0u;
+            const uint32_t c = x.k[i];
             *reinterpret_cast<vu4*>(w + 16 * i) = vu4{to_bf16<0>(c, f), to_bf16<1>(c, f), to_bf16<2>(c, f), to_bf16<3>(c, f)};
         }
     }
     {
-        const int in = threadIdx.x / 32 * 8 + (threadIdx.x & 1) * 4, n = threadIdx.x / 2 & 15;
-        uint32_t v[4];  // the channels of a key
         float f[4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            uint32_t byte = x.vs >> (8 * t) & 0xffu;
-            const bool on = x.v_on && key0 + in + t < len;
-            const bool bad = on && byte >= kKvNanFrom;
-            nan |= bad;
-            if constexpr (D == 128)
-                v[t] = on && !bad ? x.v[t] : 0u;
-            else
-                v[t] = on && !bad ? x.v[t / 2] >> (16 * (t & 1)) : 0u;
-            f[t] = scale_of(on && !bad ? byte : 127u);
-        }
-        uint8_t* const w = tile + W::kKeys * W::kKRow + (n * (D / 16)) * W::kVRow + in * 2;
+        for (int t = 0; t < 4; ++t) f[t] = scale_of(x.vs >> (8 * t) & 0xffu);
+        uint8_t* const w = tile + W::kKeys * W::kKRow + (n * (D / 16)) * W::kVRow + vin * 2;
         const auto pair = [&](int j, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
             *reinterpret_cast<vu2*>(w + 2 * j * W::kVRow) =
                 vu2{__builtin_amdgcn_perm(b, a, 0x05040100u), __builtin_amdgcn_perm(d, c, 0x05040100u)};
@@ -844,8 +855,9 @@ template <int D>
 __device__ __forceinline__ bool reads_nan(const AttnArgs& p, const Seq& s, int b, int head, int key, int group, bool v) {
     if (key >= s.len) return false;
     const KvBlock blk{p.cache.block.page, D};
-    const int64_t at = tile_page(p, s, b, key);
-    if (at < 0 || at >= p.cache.pages) return false;
+    const int64_t i = int64_t(b) * p.width + (key >> p.cache.shift);
+    const int at = p.table ? p.table[i] : static_cast<int>(i);
+    if (!page_on(p, s, at)) return false;
     const int in = key & (blk.page - 1);
     return p.cache.at(at, head)[v ? blk.v_scale(in, group) : blk.k_scale(in, group)] >= kKvNanFrom;
 }
@@ -867,6 +879,7 @@ __global__ __launch_bounds__(kThreads, (Wide<T, D, QB>::kResident)) void wide_ke
     Place w;
     if (!place_of<kRows, kKeys, kPad>(p, me, &w)) return;
     Seq s = seq_at(p, w.b);
+    const Offsets offs = share_offsets<D>(p);
     // key of row n of K's fragments
     const int k_row = 16 * (n >> 4) + 8 * ((n >> 2) & 1) + 4 * ((n >> 3) & 1) + (n & 3);
 
@@ -881,8 +894,10 @@ __global__ __launch_bounds__(kThreads, (Wide<T, D, QB>::kResident)) void wide_ke
         const int row0 = w.tile * kRows + wave * 32 * QB;
         const int head = w.head;
 
+        const int wave_key = 16 * wave;
         Share<D> next;
-        load_share<D>(next, p, s, w.b, head, (u0 + a) * kKeys);
+        load_share<D>(next, p, s, page_at(p, s, w.b, (u0 + a) * kKeys + wave_key), offs, head, (u0 + a) * kKeys + wave_key);
+        int page = page_at(p, s, w.b, (u0 + a + 1) * kKeys + wave_key);  // of the tile to load next
 
         vb8 q[QB][kParts][D / 16];
         int lo[QB], hi[QB];
@@ -936,11 +951,11 @@ __global__ __launch_bounds__(kThreads, (Wide<T, D, QB>::kResident)) void wide_ke
 
         __syncthreads();  // the last item's tiles have been read
         {
-            const bool nan = store_share<D>(next, lds, (u0 + a) * kKeys, s.len);
-            const bool any = __any(nan);
-            if (lane == 0) flag[0][wave] = any;
+            const uint32_t nan = store_share<D>(next, lds, s.len - (u0 + a) * kKeys);
+            if (lane == 0) flag[0][wave] = nan | (next.on ? 0u : 2u);
         }
-        if (a + 1 < z) load_share<D>(next, p, s, w.b, head, (u0 + a + 1) * kKeys);
+        if (a + 1 < z) load_share<D>(next, p, s, page, offs, head, (u0 + a + 1) * kKeys + wave_key);
+        page = page_at(p, s, w.b, (u0 + a + 2) * kKeys + wave_key);
         __syncthreads();
 
         for (int u = a; u < z; ++u) {
@@ -948,13 +963,11 @@ __global__ __launch_bounds__(kThreads, (Wide<T, D, QB>::kResident)) void wide_ke
             const uint8_t* const kt = lds + buf * W::kTile;
             const uint8_t* const vt = kt + kKeys * W::kKRow;
             const int key0 = (u0 + u) * kKeys;
-            uint32_t pages_on = 15;  // runs of 16 keys that have a page
-            if (p.table || s.len == 0) {
-                const int64_t at = tile_page(p, s, w.b, key0 + 16 * (lane & 3));
-                pages_on = static_cast<uint32_t>(__ballot(s.len > 0 && at >= 0 && at < p.cache.pages)) & 15u;
-            }
-            const bool edge = key0 < full_lo || key0 + kKeys > full_hi || pages_on != 15;
-            const bool nans = (flag[buf][0] | flag[buf][1] | flag[buf][2] | flag[buf][3]) != 0;
+            // what the tile's writers saw in their 16 keys: 1 a group that reads NaN, 2 no page
+            const uint32_t f4[4] = {flag[buf][0], flag[buf][1], flag[buf][2], flag[buf][3]};
+            const uint32_t seen_by = uniform(static_cast<int>(f4[0] | f4[1] << 2 | f4[2] << 4 | f4[3] << 6));
+            const bool edge = key0 < full_lo || key0 + kKeys > full_hi || (seen_by & 0xaa) != 0;
+            const bool nans = (seen_by & 0x55) != 0;
 
             vf16 sc[2][QB];
 #pragma unroll
@@ -973,63 +986,77 @@ __global__ __launch_bounds__(kThreads, (Wide<T, D, QB>::kResident)) void wide_ke
                             sc[g][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, q[i][k][c], sc[g][i], 0, 0, 0);
                     }
             }
+            // score r of half g is of key mine0 + 32 g + 16 * (r / 8) + r % 8
+            const int mine0 = key0 + 8 * h;
+            if (nans) {
+                for (int r = 0; r < 32; ++r) {
+                    bool bad = false;
+                    for (int c = 0; c < D / kKvGroup; ++c)
+                        bad |= reads_nan<D>(p, s, w.b, head, mine0 + 16 * (r / 8) + r % 8, c, false);
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                vh8 pf[QB][kP][2];
+                    for (int i = 0; i < QB; ++i)
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (bad && k == r) sc[k / 16][i][k % 16] = __builtin_nanf("");
+                }
+                // a NaN of V reaches the rows that see its key, and only those
+                for (int t = 0; t < kKeys; ++t)
+#pragma unroll
+                    for (int j = 0; j < kDt; ++j)
+                        if (reads_nan<D>(p, s, w.b, head, key0 + t, j, true))
+#pragma unroll
+                            for (int i = 0; i < QB; ++i)
+                                if (key0 + t >= lo[i] && key0 + t < hi[i])
+#pragma unroll
+                                    for (int k = 0; k < 16; ++k) o[i][j][k] = __builtin_nanf("");
+            }
+            if (edge) {
+#pragma unroll
+                for (int i = 0; i < QB; ++i)
+#pragma unroll
+                    for (int r = 0; r < 32; ++r) {
+                        const int key = mine0 + 16 * (r / 8) + r % 8;
+                        if ((seen_by >> (2 * (r / 8)) & 2u) || key < lo[i] || key >= hi[i]) sc[r / 16][i][r % 16] = kNone;
+                    }
+            }
+            float top[QB];
+            bool move = false;
+#pragma unroll
+            for (int i = 0; i < QB; ++i) {
+                top[i] = kNone;
+#pragma unroll
+                for (int r = 0; r < 32; ++r) top[i] = fmaxf(top[i], sc[r / 16][i][r % 16]);
+                top[i] *= p.scale_log2;
+                move |= top[i] > m[i] + (kSlack + kLift);
+            }
+            if (__any(move)) {
 #pragma unroll
                 for (int i = 0; i < QB; ++i) {
-                    // score r is of key mine0 + 16 * (r / 8) + r % 8
-                    const int mine0 = key0 + 32 * g + 8 * h;
-                    if (nans) {
-                        for (int r = 0; r < 16; ++r)
-                            for (int c = 0; c < D / kKvGroup; ++c)
-                                if (reads_nan<D>(p, s, w.b, head, mine0 + 16 * (r / 8) + r % 8, c, false)) {
+                    const float r = fmaxf(fmaxf(top[i], __shfl_xor(top[i], 32, 64)) - kLift, m[i]);
+                    const float f = m[i] == r ? 1.f : __builtin_amdgcn_exp2f(m[i] - r);
+                    m[i] = r;
+                    sum[i] *= f;
 #pragma unroll
-                                    for (int k = 0; k < 16; ++k)
-                                        if (k == r) sc[g][i][k] = __builtin_nanf("");
-                                }
-                    }
-                    if (edge) {
+                    for (int j = 0; j < kDt; ++j) o[i][j] *= f;
+                }
+            }
+            vh8 pf[2][QB][kP][2];
 #pragma unroll
-                        for (int r = 0; r < 16; ++r) {
-                            const int key = mine0 + 16 * (r / 8) + r % 8;
-                            if (!(pages_on >> (2 * g + r / 8) & 1u) || key < lo[i] || key >= hi[i]) sc[g][i][r] = kNone;
-                        }
-                    }
-                    float top = kNone;
+            for (int g = 0; g < 2; ++g)
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) top = fmaxf(top, sc[g][i][r]);
-                    top *= p.scale_log2;
-                    if (__any(top > m[i] + (kSlack + kLift))) {
-                        const float r = fmaxf(fmaxf(top, __shfl_xor(top, 32, 64)) - kLift, m[i]);
-                        const float f = m[i] == r ? 1.f : __builtin_amdgcn_exp2f(m[i] - r);
-                        m[i] = r;
-                        sum[i] *= f;
-#pragma unroll
-                        for (int j = 0; j < kDt; ++j) o[i][j] *= f;
-                    }
+                for (int i = 0; i < QB; ++i) {
                     const float ref = m[i] == kNone ? 0.f : -m[i];
 #pragma unroll
                     for (int r = 0; r < 16; ++r) {
                         const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[g][i][r], p.scale_log2, ref));
                         sum[i] += e;
                         const _Float16 y = static_cast<_Float16>(e);
-                        pf[i][0][r / 8][r % 8] = y;
-                        if constexpr (kP == 2) pf[i][1][r / 8][r % 8] = static_cast<_Float16>(e - static_cast<float>(y));
-                    }
-                    if (nans) {
-                        // a NaN of V reaches the rows that see its key, and only those
-                        for (int t = 0; t < 32; ++t) {
-                            const int key = key0 + 32 * g + t;
-                            if (key < lo[i] || key >= hi[i]) continue;
-#pragma unroll
-                            for (int j = 0; j < kDt; ++j)
-                                if (reads_nan<D>(p, s, w.b, head, key, j, true))
-#pragma unroll
-                                    for (int k = 0; k < 16; ++k) o[i][j][k] = __builtin_nanf("");
-                        }
+                        pf[g][i][0][r / 8][r % 8] = y;
+                        if constexpr (kP == 2) pf[g][i][1][r / 8][r % 8] = static_cast<_Float16>(e - static_cast<float>(y));
                     }
                 }
+#pragma unroll
+            for (int g = 0; g < 2; ++g)
 #pragma unroll
                 for (int j = 0; j < kDt; ++j)
 #pragma unroll
@@ -1039,14 +1066,13 @@ __global__ __launch_bounds__(kThreads, (Wide<T, D, QB>::kResident)) void wide_ke
                         for (int i = 0; i < QB; ++i)
 #pragma unroll
                             for (int k = kP - 1; k >= 0; --k)
-                                o[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, pf[i][k][t], o[i][j], 0, 0, 0);
+                                o[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, pf[g][i][k][t], o[i][j], 0, 0, 0);
                     }
-            }
             if (u + 1 < z) {
-                const bool nan = store_share<D>(next, lds + (buf ^ 1) * W::kTile, key0 + kKeys, s.len);
-                const bool any = __any(nan);
-                if (lane == 0) flag[buf ^ 1][wave] = any;
-                if (u + 2 < z) load_share<D>(next, p, s, w.b, head, key0 + 2 * kKeys);
+                const uint32_t nan = store_share<D>(next, lds + (buf ^ 1) * W::kTile, s.len - key0 - kKeys);
+                if (lane == 0) flag[buf ^ 1][wave] = nan | (next.on ? 0u : 2u);
+                if (u + 2 < z) load_share<D>(next, p, s, page, offs, head, key0 + 2 * kKeys + wave_key);
+                page = page_at(p, s, w.b, key0 + 3 * kKeys + wave_key);
                 __syncthreads();
             }
         }

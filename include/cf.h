@@ -298,7 +298,7 @@ int cf_qk_norm_rope(int a_dtype, int64_t tokens, int q_heads, int k_heads, int h
 
 /*
  * The 4-bit K/V cache: `pages` pages of `page_size` tokens for each of kv_heads heads, in one
- * buffer of cf_kv4_cache_bytes bytes.  head_dim D is 64 or 128; page_size P is 16, 32, 64, 128
+ * buffer of cf_kv4_cache_bytes bytes.  There are fewer than 2^31 pages.  head_dim D is 64 or 128; page_size P is 16, 32, 64, 128
  * or 256.  The block of page p and head h starts at (p * kv_heads + h) * P * D * 17/16 and
  * holds, in this order:
  *   K codes   [P][D/2]                   low nibble first

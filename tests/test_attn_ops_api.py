@@ -93,7 +93,7 @@ def test_cache_bytes(cf):
     assert f(1, 16, 1, 64) == 16 * 64 * 17 // 16
     assert f(100, 256, 8, 128) == 100 * 8 * 256 * 136
     for bad in ((0, 16, 1, 64), (-1, 16, 1, 64), (1, 8, 1, 64), (1, 24, 1, 64), (1, 512, 1, 64), (1, 16, 0, 64),
-                (1, 16, 65536, 64), (1, 16, 1, 96), (1, 16, 1, 256), (1 << 50, 16, 8, 128)):
+                (1, 16, 65536, 64), (1, 16, 1, 96), (1, 16, 1, 256), (1 << 50, 16, 8, 128), (1 << 31, 16, 1, 64)):
         assert f(*bad) == CF_E_SHAPE, bad
 
 
