@@ -732,7 +732,10 @@ struct Wide {
     static constexpr int kP = sizeof(T) == 4 ? 2 : 1;
     static constexpr int kRows = 32 * QB * kWaves;
     static constexpr int kKeys = 64;
-    static constexpr int kResident = QB == 1 && (sizeof(T) == 2 || D == 64) ? 2 : 1;  // workgroups of a compute unit
+#ifndef KR64
+#define KR64 3
+#endif
+    static constexpr int kResident = sizeof(T) == 4 ? 128 / D : D == 64 ? KR64 : 2;  // workgroups of a compute unit
     static constexpr int kPad = 2;
     // rows of shared memory are 16 bytes longer than they need to be: 32 rows then start on
     // 32 different groups of banks
@@ -791,10 +794,10 @@ __device__ __forceinline__ void load_share(Share<D>& x, const AttnArgs& p, const
 }
 
 // Decodes a share into a tile, of whose keys the sequence has the first `left`.  Keys behind them
-// become zeros whatever their bytes, and so do groups that read NaN; returns whether the
-// wave has any of those.
+// become zeros whatever their bytes, and so do groups that read NaN: returns whether the
+// wave has any of those, and then k_nan and v_nan, [key][group], say which of its keys' do.
 template <int D>
-__device__ __forceinline__ bool store_share(Share<D>& x, uint8_t* tile, int left) {
+__device__ __forceinline__ bool store_share(Share<D>& x, uint8_t* tile, uint8_t* k_nan, uint8_t* v_nan, int left) {
     using W = Wide<__bf16, D, 1>;
     const int kin = threadIdx.x / 4, vin = threadIdx.x / 32 * 8 + (threadIdx.x & 1) * 4, n = threadIdx.x / 2 & 15;
     uint32_t v[4];  // the channels of a key
@@ -802,9 +805,10 @@ __device__ __forceinline__ bool store_share(Share<D>& x, uint8_t* tile, int left
     for (int t = 0; t < 4; ++t) v[t] = D == 128 ? x.v[t] : x.v[t / 2] >> (16 * (t & 1));
     bool nan = false;
     if (!x.on || left < W::kKeys || __any(x.ks >= kKvNanFrom || (x.vs & x.vs << 1 & 0x80808080u) != 0)) {
-        const bool on = x.on && kin < left;
-        nan = on && x.ks >= kKvNanFrom;
-        if (!on || nan) {
+        const bool on = x.on && kin < left, k_bad = x.ks >= kKvNanFrom;
+        uint32_t v_bad = 0;
+        nan = on && k_bad;
+        if (!on || k_bad) {
             x.ks = 127u;
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) x.k[i] = 0;
@@ -814,11 +818,18 @@ __device__ __forceinline__ bool store_share(Share<D>& x, uint8_t* tile, int left
             const bool on = x.on && vin + t < left;
             const bool bad = on && (x.vs >> (8 * t) & 0xffu) >= kKvNanFrom;
             nan |= bad;
+            v_bad |= static_cast<uint32_t>(bad) << t;
             if (on && !bad) continue;
             x.vs = (x.vs & ~(0xffu << (8 * t))) | 127u << (8 * t);
             v[t] = 0;
         }
         nan = __any(nan);
+        if (nan) {
+            constexpr int kGroups = D / kKvGroup;
+            k_nan[kin * 4 + (threadIdx.x & 3)] = on && k_bad;
+#pragma unroll
+            for (int t = 0; t < 4; ++t) v_nan[(vin + t) * kGroups + n / (16 / kGroups)] = v_bad >> t & 1;
+        }
     }
     {
         const float f = scale_of(x.ks);
@@ -850,18 +861,6 @@ __device__ __forceinline__ bool store_share(Share<D>& x, uint8_t* tile, int left
     return nan;
 }
 
-// Scale byte of a key's channel group, read again: for the tiles where some group reads NaN.
-template <int D>
-__device__ __forceinline__ bool reads_nan(const AttnArgs& p, const Seq& s, int b, int head, int key, int group, bool v) {
-    if (key >= s.len) return false;
-    const KvBlock blk{p.cache.block.page, D};
-    const int64_t i = int64_t(b) * p.width + (key >> p.cache.shift);
-    const int at = p.table ? p.table[i] : static_cast<int>(i);
-    if (!page_on(p, s, at)) return false;
-    const int in = key & (blk.page - 1);
-    return p.cache.at(at, head)[v ? blk.v_scale(in, group) : blk.k_scale(in, group)] >= kKvNanFrom;
-}
-
 // A wave's 16 x 16 matrix products of before are 32 x 32 with 16 terms here: lane = 32 h + n
 // has row n of a block, and of 32 keys 8 h .. 8 h + 7 and 16 + 8 h .. , K's rows being
 // taken in the order that makes it so.
@@ -874,6 +873,7 @@ __global__ __launch_bounds__(kThreads, (Wide<T, D, QB>::kResident)) void wide_ke
     const int me = (blockIdx.x & 7) * (p.groups >> 3) + (blockIdx.x >> 3);
     __shared__ __align__(16) uint8_t lds[W::kBytes];
     __shared__ uint32_t flag[2][kWaves];
+    __shared__ uint8_t k_nan[2][kKeys * 4], v_nan[2][kKeys * kDt];
 
     if (threadIdx.x == 0) p.joins[me * 4] = -1;
     Place w;
@@ -951,7 +951,7 @@ __global__ __launch_bounds__(kThreads, (Wide<T, D, QB>::kResident)) void wide_ke
 
         __syncthreads();  // the last item's tiles have been read
         {
-            const uint32_t nan = store_share<D>(next, lds, s.len - (u0 + a) * kKeys);
+            const uint32_t nan = store_share<D>(next, lds, k_nan[0], v_nan[0], s.len - (u0 + a) * kKeys);
             if (lane == 0) flag[0][wave] = nan | (next.on ? 0u : 2u);
         }
         if (a + 1 < z) load_share<D>(next, p, s, page, offs, head, (u0 + a + 1) * kKeys + wave_key);
@@ -989,26 +989,32 @@ __global__ __launch_bounds__(kThreads, (Wide<T, D, QB>::kResident)) void wide_ke
             // score r of half g is of key mine0 + 32 g + 16 * (r / 8) + r % 8
             const int mine0 = key0 + 8 * h;
             if (nans) {
-                for (int r = 0; r < 32; ++r) {
-                    bool bad = false;
-                    for (int c = 0; c < D / kKvGroup; ++c)
-                        bad |= reads_nan<D>(p, s, w.b, head, mine0 + 16 * (r / 8) + r % 8, c, false);
-#pragma unroll
-                    for (int i = 0; i < QB; ++i)
-#pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            if (bad && k == r) sc[k / 16][i][k % 16] = __builtin_nanf("");
-                }
-                // a NaN of V reaches the rows that see its key, and only those
+                // a NaN reaches the rows that see its key, and only those
+                uint32_t k_bad = 0, v_bad[QB][kDt] = {};
+                for (int r = 0; r < 32; ++r)
+                    if (seen_by >> (2 * (r / 8)) & 1u) {
+                        const uint8_t* const y = k_nan[buf] + 4 * (8 * h + 16 * (r / 8) + r % 8);
+                        k_bad |= static_cast<uint32_t>((y[0] | y[1] | y[2] | y[3]) != 0) << r;
+                    }
                 for (int t = 0; t < kKeys; ++t)
+                    if (seen_by >> (2 * (t / 16)) & 1u) {
+#pragma unroll
+                        for (int i = 0; i < QB; ++i)
+#pragma unroll
+                            for (int j = 0; j < kDt; ++j)
+                                v_bad[i][j] |= key0 + t >= lo[i] && key0 + t < hi[i] ? v_nan[buf][t * kDt + j] : 0u;
+                    }
+#pragma unroll
+                for (int i = 0; i < QB; ++i) {
+#pragma unroll
+                    for (int r = 0; r < 32; ++r)
+                        if (k_bad >> r & 1u) sc[r / 16][i][r % 16] = __builtin_nanf("");
 #pragma unroll
                     for (int j = 0; j < kDt; ++j)
-                        if (reads_nan<D>(p, s, w.b, head, key0 + t, j, true))
+                        if (v_bad[i][j])
 #pragma unroll
-                            for (int i = 0; i < QB; ++i)
-                                if (key0 + t >= lo[i] && key0 + t < hi[i])
-#pragma unroll
-                                    for (int k = 0; k < 16; ++k) o[i][j][k] = __builtin_nanf("");
+                            for (int k = 0; k < 16; ++k) o[i][j][k] = __builtin_nanf("");
+                }
             }
             if (edge) {
 #pragma unroll
@@ -1069,7 +1075,8 @@ __global__ __launch_bounds__(kThreads, (Wide<T, D, QB>::kResident)) void wide_ke
                                 o[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, pf[g][i][k][t], o[i][j], 0, 0, 0);
                     }
             if (u + 1 < z) {
-                const uint32_t nan = store_share<D>(next, lds + (buf ^ 1) * W::kTile, s.len - key0 - kKeys);
+                const uint32_t nan =
+                    store_share<D>(next, lds + (buf ^ 1) * W::kTile, k_nan[buf ^ 1], v_nan[buf ^ 1], s.len - key0 - kKeys);
                 if (lane == 0) flag[buf ^ 1][wave] = nan | (next.on ? 0u : 2u);
                 if (u + 2 < z) load_share<D>(next, p, s, page, offs, head, key0 + 2 * kKeys + wave_key);
                 page = page_at(p, s, w.b, key0 + 3 * kKeys + wave_key);
@@ -1209,7 +1216,7 @@ Plan plan_of(int a_dtype, int head_dim, int64_t rows) {
     const int large = wide_rows(a_dtype, head_dim);
     Plan x;
     x.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : large;
-    x.groups = x.rows == 16 ? kGroupsSmall : x.rows == 32 ? kGroupsSmall / 2 : (large == 128 && (a_dtype == CF_BF16 || head_dim == 64) ? 2 : 1) * kGroupsLarge;
+    x.groups = x.rows == 16 ? kGroupsSmall : x.rows == 32 ? kGroupsSmall / 2 : (a_dtype == CF_F32 ? 128 / head_dim : head_dim == 64 ? KR64 : 2) * kGroupsLarge;
     const int64_t floats = head_dim == 64 ? part_floats<64>(x.rows) : part_floats<128>(x.rows);
     x.bytes = size_t(x.groups) * (2 * floats * 4 + 16);
     return x;
