@@ -737,10 +737,18 @@ struct Wide {
 #endif
     static constexpr int kResident = sizeof(T) == 4 ? 128 / D : D == 64 ? KR64 : 2;  // workgroups of a compute unit
     static constexpr int kPad = 2;
-    // rows of shared memory are 16 bytes longer than they need to be: 32 rows then start on
-    // 32 different groups of banks
-    static constexpr int kKRow = 2 * D + 16, kVRow = 2 * kKeys + 16;
-    static constexpr int kTile = kKeys * kKRow + D * kVRow;
+    // K's rows are 16 bytes longer than they need to be: 16 rows then start on different banks
+    static constexpr int kKRow = 2 * D + 16;
+    static constexpr int kTile = kKeys * kKRow + D * 2 * kKeys;
+    // V's rows (a channel's 64 keys) lie two together in 256 bytes, as 16 runs of 8 keys: run q of
+    // channel c is number (8 (c & 1) + q) ^ v_turn(c / 2).  Both the 16 consecutive channels that
+    // a product reads and the 16 channel pieces that the decoding threads write then lie on
+    // different banks.  The turn of c / 2 + x is that of c / 2, ^ x, for x below 4 (2 at 64
+    // channels) and c a piece's first.
+    __host__ __device__ static constexpr int v_turn(int pair) {
+        return D == 128 ? (pair & 7) ^ (pair >> 3 & 3) ^ (pair >> 5 & 1) << 3
+                        : (pair & 7) ^ (pair >> 3 & 1) ^ (pair >> 4 & 1) << 3;
+    }
     static constexpr int kBytes = 2 * kTile;
 };
 
@@ -844,11 +852,12 @@ __device__ __forceinline__ bool store_share(Share<D>& x, uint8_t* tile, uint8_t*
         float f[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) f[t] = scale_of(x.vs >> (8 * t) & 0xffu);
-        uint8_t* const w = tile + W::kKeys * W::kKRow + (n * (D / 16)) * W::kVRow + vin * 2;
+        const int first = n * (D / 32), turn = W::v_turn(first) ^ vin / 8;  // pair of channels
+        uint8_t* const w = tile + W::kKeys * W::kKRow + first * 256 + (vin & 4) * 2;
         const auto pair = [&](int j, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-            *reinterpret_cast<vu2*>(w + 2 * j * W::kVRow) =
+            *reinterpret_cast<vu2*>(w + 256 * j + 16 * (turn ^ j)) =
                 vu2{__builtin_amdgcn_perm(b, a, 0x05040100u), __builtin_amdgcn_perm(d, c, 0x05040100u)};
-            *reinterpret_cast<vu2*>(w + (2 * j + 1) * W::kVRow) =
+            *reinterpret_cast<vu2*>(w + 256 * j + 16 * (turn ^ j ^ 8)) =
                 vu2{__builtin_amdgcn_perm(b, a, 0x07060302u), __builtin_amdgcn_perm(d, c, 0x07060302u)};
         };
         pair(0, to_f16<0>(v[0], f[0]), to_f16<0>(v[1], f[1]), to_f16<0>(v[2], f[2]), to_f16<0>(v[3], f[3]));
@@ -880,6 +889,7 @@ __global__ __launch_bounds__(kThreads, (Wide<T, D, QB>::kResident)) void wide_ke
     if (!place_of<kRows, kKeys, kPad>(p, me, &w)) return;
     Seq s = seq_at(p, w.b);
     const Offsets offs = share_offsets<D>(p);
+    const int v_lane = 8 * (n & 1) ^ h ^ W::v_turn(n / 2);  // v_turn(16 j + x) = v_turn(16 j) ^ v_turn(x)
     // key of row n of K's fragments
     const int k_row = 16 * (n >> 4) + 8 * ((n >> 2) & 1) + 4 * ((n >> 3) & 1) + (n & 3);
 
@@ -1067,7 +1077,8 @@ __global__ __launch_bounds__(kThreads, (Wide<T, D, QB>::kResident)) void wide_ke
                 for (int j = 0; j < kDt; ++j)
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
-                        const vh8 vf = *reinterpret_cast<const vh8*>(vt + (32 * j + n) * W::kVRow + 2 * (32 * g + 16 * t + 8 * h));
+                        const vh8 vf = *reinterpret_cast<const vh8*>(
+                            vt + (16 * j + n / 2) * 256 + 16 * (v_lane ^ (4 * g + 2 * t) ^ W::v_turn(16 * j)));
 #pragma unroll
                         for (int i = 0; i < QB; ++i)
 #pragma unroll
