@@ -732,6 +732,8 @@ struct Wide {
     static constexpr int kP = sizeof(T) == 4 ? 2 : 1;
     static constexpr int kRows = 32 * QB * kWaves;
     static constexpr int kKeys = 64;
+    // with two waves a SIMD the order of reads and products is fixed; three hide it, and lack registers
+    static constexpr bool kAhead = D == 128;
 #ifndef KR64
 #define KR64 3
 #endif
@@ -762,9 +764,12 @@ struct Share {
 };
 
 // The page of a key (the last key's behind it: always inside the cache, and masked later).
-__device__ __forceinline__ int page_at(const AttnArgs& p, const Seq& s, int b, int key) {
+// Lanes ask for a tile's four runs of 16 keys, and a wave takes its own: a scalar load, which
+// shares its counter with shared memory, would be waited for at the next barrier.
+__device__ __forceinline__ int page_at(const AttnArgs& p, const Seq& s, int b, int key0) {
+    const int key = key0 + 16 * static_cast<int>(threadIdx.x & 3);
     const int64_t at = int64_t(b) * p.width + (min(key, max(s.len - 1, 0)) >> p.cache.shift);
-    return p.table ? scalar_load(p.table + at) : static_cast<int>(at);  // at < pages < 2^31 without a table
+    return p.table ? p.table[at] : static_cast<int>(at);  // at < pages < 2^31 without a table
 }
 
 // Where a thread's share lies in a page's block, from its wave's first key on.
@@ -870,6 +875,13 @@ __device__ __forceinline__ bool store_share(Share<D>& x, uint8_t* tile, uint8_t*
     return nan;
 }
 
+// Nothing moves across: what is read before is in flight while what stands before is worked on.
+// Left alone, the compiler reads shared memory one product ahead of nothing, and each waits.
+template <bool ON>
+__device__ __forceinline__ void stay() {
+    if constexpr (ON) __builtin_amdgcn_sched_barrier(0);
+}
+
 // A wave's 16 x 16 matrix products of before are 32 x 32 with 16 terms here: lane = 32 h + n
 // has row n of a block, and of 32 keys 8 h .. 8 h + 7 and 16 + 8 h .. , K's rows being
 // taken in the order that makes it so.
@@ -906,8 +918,9 @@ __global__ __launch_bounds__(kThreads, (Wide<T, D, QB>::kResident)) void wide_ke
 
         const int wave_key = 16 * wave;
         Share<D> next;
-        load_share<D>(next, p, s, page_at(p, s, w.b, (u0 + a) * kKeys + wave_key), offs, head, (u0 + a) * kKeys + wave_key);
-        int page = page_at(p, s, w.b, (u0 + a + 1) * kKeys + wave_key);  // of the tile to load next
+        int pages = page_at(p, s, w.b, (u0 + a) * kKeys);  // of the tile to load next
+        load_share<D>(next, p, s, __builtin_amdgcn_readlane(pages, wave), offs, head, (u0 + a) * kKeys + wave_key);
+        pages = page_at(p, s, w.b, (u0 + a + 1) * kKeys);
 
         vb8 q[QB][kParts][D / 16];
         int lo[QB], hi[QB];
@@ -964,8 +977,12 @@ __global__ __launch_bounds__(kThreads, (Wide<T, D, QB>::kResident)) void wide_ke
             const uint32_t nan = store_share<D>(next, lds, k_nan[0], v_nan[0], s.len - (u0 + a) * kKeys);
             if (lane == 0) flag[0][wave] = nan | (next.on ? 0u : 2u);
         }
-        if (a + 1 < z) load_share<D>(next, p, s, page, offs, head, (u0 + a + 1) * kKeys + wave_key);
-        page = page_at(p, s, w.b, (u0 + a + 2) * kKeys + wave_key);
+        const auto load_next = [&](int u) {
+            const int page = __builtin_amdgcn_readlane(pages, wave);
+            pages = page_at(p, s, w.b, (u0 + u + 1) * kKeys);
+            load_share<D>(next, p, s, page, offs, head, (u0 + u) * kKeys + wave_key);
+        };
+        if (a + 1 < z) load_next(a + 1);
         __syncthreads();
 
         for (int u = a; u < z; ++u) {
@@ -979,33 +996,47 @@ __global__ __launch_bounds__(kThreads, (Wide<T, D, QB>::kResident)) void wide_ke
             const bool edge = key0 < full_lo || key0 + kKeys > full_hi || (seen_by & 0xaa) != 0;
             const bool nans = (seen_by & 0x55) != 0;
 
+            // K's fragments, four ahead of the products: number f is terms 16 (f % (D/16)) of half f / (D/16)
+            constexpr int kFrags = 2 * D / 16;
+            const uint8_t* const kn = kt + k_row * W::kKRow + 16 * h;
             vf16 sc[2][QB];
+            vb8 kf[2][4];
+            const auto read_k = [&](int f0) {
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
+                for (int f = f0; f < f0 + 4; ++f)
+                    kf[f / 4 & 1][f & 3] = *reinterpret_cast<const vb8*>(kn + f / (D / 16) * 32 * W::kKRow + f % (D / 16) * 32);
+            };
+            read_k(0);
 #pragma unroll
-                for (int i = 0; i < QB; ++i)
+            for (int f0 = 0; f0 < kFrags; f0 += 4) {
+                if (f0 + 4 < kFrags) read_k(f0 + 4);
+                stay<W::kAhead>();
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) sc[g][i][k] = 0.f;
+                for (int f = f0; f < f0 + 4; ++f)
 #pragma unroll
-                for (int k = kParts - 1; k >= 0; --k)
+                    for (int i = 0; i < QB; ++i)
 #pragma unroll
-                    for (int c = 0; c < D / 16; ++c) {
-                        const vb8 kf = *reinterpret_cast<const vb8*>(kt + (32 * g + k_row) * W::kKRow + 32 * c + 16 * h);
+                        for (int k = kParts - 1; k >= 0; --k) {
+                            vf16& x = sc[f / (D / 16)][i];
+                            if (f % (D / 16) == 0 && k == kParts - 1)
 #pragma unroll
-                        for (int i = 0; i < QB; ++i)
-                            sc[g][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, q[i][k][c], sc[g][i], 0, 0, 0);
-                    }
+                                for (int r = 0; r < 16; ++r) x[r] = 0.f;
+                            x = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[f / 4 & 1][f & 3], q[i][k][f % (D / 16)], x, 0, 0, 0);
+                        }
+                stay<W::kAhead>();
             }
             // score r of half g is of key mine0 + 32 g + 16 * (r / 8) + r % 8
             const int mine0 = key0 + 8 * h;
             if (nans) {
                 // a NaN reaches the rows that see its key, and only those
                 uint32_t k_bad = 0, v_bad[QB][kDt] = {};
+#pragma unroll 1
                 for (int r = 0; r < 32; ++r)
                     if (seen_by >> (2 * (r / 8)) & 1u) {
                         const uint8_t* const y = k_nan[buf] + 4 * (8 * h + 16 * (r / 8) + r % 8);
                         k_bad |= static_cast<uint32_t>((y[0] | y[1] | y[2] | y[3]) != 0) << r;
                     }
+#pragma unroll 1
                 for (int t = 0; t < kKeys; ++t)
                     if (seen_by >> (2 * (t / 16)) & 1u) {
 #pragma unroll
@@ -1056,41 +1087,60 @@ __global__ __launch_bounds__(kThreads, (Wide<T, D, QB>::kResident)) void wide_ke
                     for (int j = 0; j < kDt; ++j) o[i][j] *= f;
                 }
             }
+            float ref[QB];
+#pragma unroll
+            for (int i = 0; i < QB; ++i) ref[i] = m[i] == kNone ? 0.f : -m[i];
             vh8 pf[2][QB][kP][2];
+            // probabilities r0 .. r0 + N - 1 of half g
+            const auto exps = [&](int g, int r0, int many) {
 #pragma unroll
-            for (int g = 0; g < 2; ++g)
+                for (int i = 0; i < QB; ++i)
 #pragma unroll
-                for (int i = 0; i < QB; ++i) {
-                    const float ref = m[i] == kNone ? 0.f : -m[i];
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[g][i][r], p.scale_log2, ref));
+                    for (int r = r0; r < r0 + many; ++r) {
+                        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[g][i][r], p.scale_log2, ref[i]));
                         sum[i] += e;
                         const _Float16 y = static_cast<_Float16>(e);
                         pf[g][i][0][r / 8][r % 8] = y;
                         if constexpr (kP == 2) pf[g][i][1][r / 8][r % 8] = static_cast<_Float16>(e - static_cast<float>(y));
                     }
+            };
+            // V's fragments, likewise: number f is of half f / (2 kDt), terms 16 (f % 2), channels 32 (f / 2 % kDt)
+            constexpr int kVFrags = 4 * kDt;
+            const uint8_t* const vn = vt + n / 2 * 256;
+            vh8 vf[2][4];
+            const auto read_v = [&](int f0) {
+#pragma unroll
+                for (int f = f0; f < f0 + 4; ++f) {
+                    const int g = f / (2 * kDt), j = f / 2 % kDt, t = f & 1;
+                    vf[f / 4 & 1][f & 3] = *reinterpret_cast<const vh8*>(
+                        vn + j * 4096 + 16 * (v_lane ^ (4 * g + 2 * t) ^ W::v_turn(16 * j)));
                 }
+            };
+            read_v(0);
+            stay<W::kAhead>();
+            exps(0, 0, 16);
 #pragma unroll
-            for (int g = 0; g < 2; ++g)
+            for (int f0 = 0; f0 < kVFrags; f0 += 4) {
+                if (f0 + 4 < kVFrags) read_v(f0 + 4);
+                stay<W::kAhead>();
 #pragma unroll
-                for (int j = 0; j < kDt; ++j)
+                for (int f = f0; f < f0 + 4; ++f)
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        const vh8 vf = *reinterpret_cast<const vh8*>(
-                            vt + (16 * j + n / 2) * 256 + 16 * (v_lane ^ (4 * g + 2 * t) ^ W::v_turn(16 * j)));
+                    for (int i = 0; i < QB; ++i)
 #pragma unroll
-                        for (int i = 0; i < QB; ++i)
-#pragma unroll
-                            for (int k = kP - 1; k >= 0; --k)
-                                o[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, pf[g][i][k][t], o[i][j], 0, 0, 0);
-                    }
+                        for (int k = kP - 1; k >= 0; --k) {
+                            vf16& x = o[i][f / 2 % kDt];
+                            x = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf[f / 4 & 1][f & 3], pf[f / (2 * kDt)][i][k][f & 1], x, 0, 0, 0);
+                        }
+                // the other half's probabilities beside this half's products
+                if (f0 < kVFrags / 2) exps(1, f0 * 32 / kVFrags, 4 * 32 / kVFrags);
+                stay<W::kAhead>();
+            }
             if (u + 1 < z) {
                 const uint32_t nan =
                     store_share<D>(next, lds + (buf ^ 1) * W::kTile, k_nan[buf ^ 1], v_nan[buf ^ 1], s.len - key0 - kKeys);
                 if (lane == 0) flag[buf ^ 1][wave] = nan | (next.on ? 0u : 2u);
-                if (u + 2 < z) load_share<D>(next, p, s, page, offs, head, key0 + 2 * kKeys + wave_key);
-                page = page_at(p, s, w.b, key0 + 3 * kKeys + wave_key);
+                if (u + 2 < z) load_next(u + 2);
                 __syncthreads();
             }
         }
@@ -1219,7 +1269,7 @@ struct Plan {
     size_t bytes;
 };
 
-constexpr int wide_blocks(int esz, int dim) { return esz == 4 ? 1 : kWideBlocks; }
+constexpr int wide_blocks(int esz, int dim) { return esz == 4 || dim == 128 ? 1 : kWideBlocks; }
 constexpr int wide_rows(int a_dtype, int dim) { return 128 * wide_blocks(a_dtype == CF_F32 ? 4 : 2, dim); }
 
 // The kernel for a call: rows is the number of rows that the longest sequence has.
