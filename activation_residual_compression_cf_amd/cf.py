@@ -519,6 +519,11 @@ def _on(stream, dev: int):
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
+def _like(t: torch.Tensor, stream) -> torch.Tensor:
+    o = torch.empty_like(t)
+    return o if stream is None else _keep_for(o, stream)
+
+
 def _new(like: torch.Tensor, shape, stream, dtype: torch.dtype | None = None) -> torch.Tensor:
     """A buffer for the launch stream to write."""
     t = like.new_empty(shape, dtype=dtype)
@@ -552,11 +557,11 @@ def qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, norm: int = CF_
     rq = rk = rqo = rko = None
     if q is not None:
         rq = _rows("q", q, dev)
-        q_out = _new(q, q.shape, stream) if q_out is None else q_out
+        q_out = _like(q, stream) if q_out is None else q_out
         rqo = _rows("q_out", q_out, dev)
     if k is not None:
         rk = _rows("k", k, dev)
-        k_out = _new(k, k.shape, stream) if k_out is None else k_out
+        k_out = _like(k, stream) if k_out is None else k_out
         rko = _rows("k_out", k_out, dev)
     n_pos = rot = 0
     pc = ps = pp = None
@@ -666,7 +671,7 @@ def kv4_attention(q: torch.Tensor, cache: KV4Cache, kv_lens: torch.Tensor, table
     pe = _flat("lse", lse, dev, _F32, (total, heads))
     pl = _flat("kv_lens", kv_lens, dev, torch.int32, (batch,))
     if out is None:
-        out = _new(q, q.shape, stream)
+        out = _like(q, stream)
     else:
         _shaped("out", out, q.dtype, q.shape)
     if workspace is None:

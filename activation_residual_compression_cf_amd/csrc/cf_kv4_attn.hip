@@ -162,6 +162,7 @@ __device__ __forceinline__ int64_t wave_scan(int64_t v) {
 // Where a workgroup's run of the work begins, and its length.  An item costs its units and PAD
 // more: what starting and finishing one takes, in units.
 struct Place {
+    int me;  // which run
     int64_t at, end, chunk;
     int b, head, tile;
     int64_t rest;  // of at, from the item's start
@@ -169,7 +170,7 @@ struct Place {
 
 // Every wave works it out by itself: a group of lanes takes a sequence and shares its tiles.
 template <int ROWS, int UNIT, int PAD>
-__device__ __forceinline__ bool place_of(const AttnArgs& p, int me, Place* x) {
+__device__ __forceinline__ bool place_of(const AttnArgs& p, Place* x) {
     const int lane = threadIdx.x & 63;
     int sub = 64;  // lanes of a sequence
     while (sub > 1 && 64 / sub < p.batch) sub >>= 1;
@@ -195,7 +196,12 @@ __device__ __forceinline__ bool place_of(const AttnArgs& p, int me, Place* x) {
     int64_t chunk = (total + p.groups - 1) / p.groups;
     chunk = max(chunk, int64_t(kMinUnits * kUnit / UNIT + PAD));
     x->chunk = chunk;
-    x->at = me * chunk;
+    // Workgroups are dealt to the eight XCDs in turn.  Neighbours in the order of the work share keys:
+    // each XCD takes an eighth of the runs there are, side by side, and so one part of L2's keys.
+    const int each_xcd = static_cast<int>((total + chunk - 1) / chunk + 7) / 8;
+    const int bid = blockIdx.x;
+    x->me = bid < 8 * each_xcd ? (bid & 7) * each_xcd + (bid >> 3) : bid;
+    x->at = x->me * chunk;
     x->end = min(x->at + chunk, total);
     if (x->at >= x->end) return false;
     int64_t before = 0;
@@ -405,15 +411,15 @@ __global__ __launch_bounds__(kThreads, NQ == 1 ? 2 : 1) void attn_kernel(const A
     constexpr int kRows = S::kRows, kPad = S::kPad, kParts = S::kParts, kP = S::kP;
     constexpr int kJ = D / 16;  // O^T tiles of 16 channel pieces
     const int lane = threadIdx.x & 63, wave = uniform(static_cast<int>(threadIdx.x) >> 6), n = lane & 15, g = lane >> 4;
-    // neighbours in the order of the work share keys: let them share an XCD's L2
-    const int me = (blockIdx.x & 7) * (p.groups >> 3) + (blockIdx.x >> 3);
 
     __shared__ float stage[SPLIT ? kWaves * 16 * (D + 4) : 1];
     __shared__ float stage_m[SPLIT ? kWaves * 16 : 1], stage_l[SPLIT ? kWaves * 16 : 1];
 
-    if (threadIdx.x == 0) p.joins[me * 4] = -1;
     Place w;
-    if (!place_of<kRows, kUnit, kPad>(p, me, &w)) return;
+    const bool work = place_of<kRows, kUnit, kPad>(p, &w);
+    const int me = w.me;
+    if (threadIdx.x == 0) p.joins[me * 4] = -1;
+    if (!work) return;
     const Offsets offs = offsets_of<D>(p);
     Seq s = seq_at(p, w.b);
 
@@ -891,14 +897,15 @@ __global__ __launch_bounds__(kThreads, (Wide<T, D, QB>::kResident)) void wide_ke
     constexpr int kRows = W::kRows, kPad = W::kPad, kParts = W::kParts, kP = W::kP, kKeys = W::kKeys;
     constexpr int kDt = D / 32;
     const int lane = threadIdx.x & 63, wave = uniform(static_cast<int>(threadIdx.x) >> 6), n = lane & 31, h = lane >> 5;
-    const int me = (blockIdx.x & 7) * (p.groups >> 3) + (blockIdx.x >> 3);
     __shared__ __align__(16) uint8_t lds[W::kBytes];
     __shared__ uint32_t flag[2][kWaves];
     __shared__ uint8_t k_nan[2][kKeys * 4], v_nan[2][kKeys * kDt];
 
-    if (threadIdx.x == 0) p.joins[me * 4] = -1;
     Place w;
-    if (!place_of<kRows, kKeys, kPad>(p, me, &w)) return;
+    const bool work = place_of<kRows, kKeys, kPad>(p, &w);
+    const int me = w.me;
+    if (threadIdx.x == 0) p.joins[me * 4] = -1;
+    if (!work) return;
     Seq s = seq_at(p, w.b);
     const Offsets offs = share_offsets<D>(p);
     const int v_lane = 8 * (n & 1) ^ h ^ W::v_turn(n / 2);  // v_turn(16 j + x) = v_turn(16 j) ^ v_turn(x)
