@@ -143,6 +143,8 @@ struct RowsOf {
     Range range() const { return range_of(r.data, none() ? 0 : static_cast<int64_t>(extent() * esz)); }
 };
 
+// Rows of one call: a row takes at least 8 work-items, of which a dispatch counts 2^32 - 1.
+constexpr int64_t kMaxRows = int64_t(1) << 28;
 constexpr wide kMaxExtent = wide(1) << 46;  // bytes: beyond any device's memory
 
 // NULL, strides, alignment of one operand's rows, in this order.
@@ -231,9 +233,10 @@ const char* cf_strerror(int status) {
     switch (status) {
         case CF_OK: return "ok";
         case CF_E_NULL: return "required pointer is NULL";
-        case CF_E_SHAPE: return "size out of range (numel must be a positive multiple of 128, at most 2^33)";
+        case CF_E_SHAPE: return "size, stride or head count out of range (numel of the 1/2-bit and top-k calls: a positive "
+                                "multiple of 128, at most 2^33)";
         case CF_E_ALIGN: return "pointer misaligned (16 bytes; scales 4 bytes)";
-        case CF_E_ARG: return "unsupported bits, k, dtype or mode";
+        case CF_E_ARG: return "unsupported bits, k, dtype, mode, flag or scale";
         case CF_E_ALIAS: return "output range overlaps another operand";
         case CF_E_WORKSPACE: return "workspace missing or too small";
         case CF_E_DEVICE: return "current device is not gfx950";
@@ -457,7 +460,7 @@ int cf_qk_norm_rope(int a_dtype, int64_t tokens, int q_heads, int k_heads, int h
         head_dim % 8 || head_dim > 256)
         return CF_E_SHAPE;
     const int64_t heads = int64_t(q_heads) + k_heads;
-    if (heads == 0 || tokens > kMaxNumel / head_dim / heads) return CF_E_SHAPE;
+    if (heads == 0 || tokens > kMaxNumel / head_dim / heads || tokens > kMaxRows / heads) return CF_E_SHAPE;
     const bool turn = rope != CF_ROPE_NONE;
     if (turn && (rot_dim <= 0 || rot_dim % 16 || rot_dim > head_dim || n_pos <= 0 || n_pos > kMaxNumel / rot_dim ||
                  (!positions && tokens > n_pos)))
@@ -524,7 +527,7 @@ int cf_kv4_attention(int a_dtype, const cf_rows* q, int64_t total_q, int q_heads
                      void* stream) {
     if (a_dtype != CF_BF16 && a_dtype != CF_F32) return CF_E_ARG;
     if ((flags & ~CF_ATTN_CAUSAL) || window < 0 || (window && !(flags & CF_ATTN_CAUSAL))) return CF_E_ARG;
-    if (!(scale > 0.f) || scale > 3.4e38f) return CF_E_ARG;
+    if (!(scale > 0.f) || scale > 1e38f) return CF_E_ARG;
     const int64_t cache_bytes = cf_kv4_cache_bytes(pages, page_size, kv_heads, head_dim);
     if (cache_bytes < 0) return CF_E_SHAPE;
     if (q_heads < 1 || q_heads > 65535 || q_heads % kv_heads || total_q < 0 || total_q > INT32_MAX / q_heads ||

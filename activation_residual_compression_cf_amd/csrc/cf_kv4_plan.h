@@ -83,7 +83,7 @@ __device__ __forceinline__ Seq seq_at(const AttnArgs& p, int b) {
 
 // Keys [lo, hi) that a query token sees; hi may be below lo.
 __device__ __forceinline__ int seen_lo(const AttnArgs& p, const Seq& s, int token) {
-    return p.window ? max(s.len - s.nq + token - p.window + 1, 0) : 0;
+    return p.window ? static_cast<int>(max(int64_t(s.len) - s.nq + token - p.window + 1, int64_t(0))) : 0;
 }
 __device__ __forceinline__ int seen_hi(const AttnArgs& p, const Seq& s, int token) {
     return p.causal ? min(s.len - s.nq + token + 1, s.len) : s.len;

@@ -284,7 +284,8 @@ enum { CF_ROPE_NONE = 0, CF_ROPE_INTERLEAVED = 1, CF_ROPE_HALF = 2 };
  *     token with a negative position is padding: its rows in q_out and k_out stay as they
  *     are.  A position of n_pos or more gives rows of NaN.
  *   cos, sin: n_pos x rot_dim/2 fp32.
- * head_dim a multiple of 8, at most 256; rot_dim a multiple of 16, at most head_dim; eps
+ * tokens * heads at most 2^28 rows, times head_dim at most 2^33.  head_dim a multiple of 8, at
+ * most 256; rot_dim a multiple of 16, at most head_dim; eps
  * finite and not negative.  q_heads or k_heads may be 0 (that side's pointers are then not
  * used).  In place (q_out the same rows as q, k_out as k) is allowed; any other overlap of an
  * output with another operand is not.
@@ -350,7 +351,7 @@ int cf_kv4_read(int a_dtype, const uint8_t* cache, int64_t pages, int page_size,
  *     It chooses the kernel and the workspace; the results are right for any lengths.
  *   workspace: cf_kv4_attention_workspace_bytes, 256-byte aligned; nothing in it has to be
  *     set before a call, and nothing is kept in it for the next.
- * scale > 0; window >= 0, and 0 unless causal; q_heads a multiple of kv_heads, at most 65535;
+ * 0 < scale <= 1e38; window >= 0, and 0 unless causal; q_heads a multiple of kv_heads, at most 65535;
  * total_q * q_heads < 2^31, table_width * page_size < 2^31 - 256.
  * K and V enter the products exactly.  bf16: queries exactly, probabilities rounded to fp16;
  * fp32: queries exactly, probabilities to 22 bits.  Scores, sums and results are fp32 up to

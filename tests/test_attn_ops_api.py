@@ -46,7 +46,7 @@ def test_norm_rope_refusals(cf, L):
         assert norm(cf, eps=eps) == CF_E_ARG
     assert norm(cf, eps=0.0) == CF_E_DEVICE
     for bad in (dict(tokens=-1), dict(hq=-1), dict(hq=0, hk=0), dict(dim=0), dict(dim=12), dict(dim=264), dict(hq=65536),
-                dict(tokens=1 << 40), dict(rot=0), dict(rot=8), dict(rot=24), dict(rot=80), dict(n_pos=0),
+                dict(tokens=1 << 40), dict(tokens=(1 << 28) + 1, hq=1, hk=0, dim=8, rope=0), dict(rot=0), dict(rot=8), dict(rot=24), dict(rot=80), dict(n_pos=0),
                 dict(pos=0, n_pos=9)):
         assert norm(cf, **bad) == CF_E_SHAPE, bad
     assert norm(cf, rope=0, rot=0, n_pos=0, cos=0, sin=0, pos=0) == CF_E_DEVICE
@@ -143,7 +143,7 @@ def test_attention_refusals(cf, L):
     assert attn(cf) == CF_E_DEVICE
     assert attn(cf, flags=1, window=7) == CF_E_DEVICE
     for bad in (dict(dt=2), dict(flags=2), dict(window=-1, flags=1), dict(window=5), dict(scale=0.0), dict(scale=-1.0),
-                dict(scale=float("nan")), dict(scale=float("inf"))):
+                dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=2e38)):
         assert attn(cf, **bad) == CF_E_ARG, bad
     for bad in (dict(pages=0), dict(page=17), dict(hk=3), dict(hq=0), dict(hq=9), dict(dim=80), dict(total=-1),
                 dict(total=1 << 30), dict(max_q=13), dict(max_q=-1), dict(batch=0), dict(width=0), dict(width=1 << 27),

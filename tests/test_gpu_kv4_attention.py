@@ -296,6 +296,41 @@ def test_many_sequences(cf, dev):
     c.check(*c.run(cf, max_q=2, causal=True), causal=True)
 
 
+@pytest.mark.parametrize("batch", [33, 64, 65, 130])
+def test_many_sequences_of_many_rows(cf, dev, batch):
+    say(f"kv4 attention {batch} sequences of up to 45 queries")
+    rng = np.random.default_rng(batch)
+    kv = [int(x) for x in rng.integers(0, 90, batch)]
+    nq = [int(x) for x in rng.integers(0, 46, batch)]
+    nq[3] = 45
+    c = Case(cf, dev, kv, nq, 2, 1, 64, "bf16", seed=3)
+    c.check(*c.run(cf, max_q=45, causal=True), causal=True)
+
+
+def test_largest_window(cf, dev):
+    say("kv4 attention with a window past every length")
+    for nq in (3, 90):
+        c = Case(cf, dev, [70, 5], [nq, nq], 2, 2, 64, "bf16")
+        want = c.run(cf, causal=True)
+        got = c.run(cf, causal=True, window=2 ** 31 - 1)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_rows_do_not_depend_on_the_tile_they_are_in(cf, dev):
+    """The same query at several places of a batch: results agree to the bound, whatever kernel and
+    split they meet."""
+    say("kv4 attention, one query in many places")
+    c = Case(cf, dev, [2000] * 3, [1, 20, 200], 4, 1, 128, "f32", seed=7)
+    c.q[:] = c.q[0]
+    for i in (1, 2):  # three times the same keys
+        c.table[i] = c.table[0]
+        c.k[i], c.v[i] = c.k[0], c.v[0]
+    out, lse = c.run(cf)
+    c.check(out, lse)
+    for m in (1, 8, 0):
+        c.check(*c.run(cf, max_q=m))
+
+
 def test_workspace_needs_nothing_and_is_not_overrun(cf, dev):
     say("kv4 attention workspace")
     for nq, dtype in ((1, "bf16"), (10, "f32"), (130, "bf16")):

@@ -181,3 +181,27 @@ def test_strides_stream_and_graph(cf, dev):
     ks, vs = cf.kv4_read(cache, slots, stream=side)
     side.synchronize()
     assert torch.equal(ks, vs)
+
+
+def test_offsets_past_32_bits(cf, dev):
+    """A cache of more than 2^32 bytes: its last page is as good as its first."""
+    say("kv4 cache of 4.5 GB")
+    page, heads, dim = 256, 8, 128
+    block = page * dim * 17 // 16 * heads
+    pages = (9 << 29) // block
+    cache = cf.KV4Cache(torch.empty((pages, heads, block // heads), dtype=torch.uint8, device=dev), page, dim)
+    assert cache.data.numel() > 1 << 32
+    x = torch.randn(40, heads, dim, device=dev, dtype=torch.bfloat16)
+    slots = torch.arange(40, device=dev) * 7 + (pages - 2) * page
+    cf.kv4_append(cache, x, -x, slots)
+    k, v = cf.kv4_read(cache, slots)
+    assert torch.equal(k, -v) and np.array_equal(host(k.float()), ref.quantize(host(x.float())))
+    # attention over the last page only
+    q = torch.randn(1, heads, dim, device=dev, dtype=torch.bfloat16)
+    s = torch.arange(40, device=dev) + (pages - 1) * page
+    cf.kv4_append(cache, x, -x, s)
+    table = torch.tensor([[pages - 1]], dtype=torch.int32, device=dev)
+    out = cf.kv4_attention(q, cache, torch.tensor([40], dtype=torch.int32, device=dev), table=table)
+    kk = ref.quantize(host(x.float()))
+    o, _, bo, _ = ref.attention(host(q.double()), kk, -kk, 1, dim ** -0.5, False, 0)
+    assert (np.abs(host(out.double()) - o) <= ref.out_bound(o, bo, 40, -kk, "bf16", heads)).all()
