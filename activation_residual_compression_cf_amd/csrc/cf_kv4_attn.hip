@@ -42,13 +42,11 @@ namespace {
 template <typename T, int D, int ROWS>
 __global__ __launch_bounds__(kThreads) void join_kernel(const AttnArgs p) {
     const int me = blockIdx.x;
-    const int first = scalar_load(p.joins + me * 4);
-    if (first < 0) return;
-    const int b = scalar_load(p.joins + me * 4 + 1), head = scalar_load(p.joins + me * 4 + 2),
-              tile = scalar_load(p.joins + me * 4 + 3);
-    const Seq s = seq_at(p, b);
+    const int32_t* const left = p.joins + me * kJoin;
+    const int first = scalar_load(left), head = scalar_load(left + 1), q0 = scalar_load(left + 2),
+              row0 = scalar_load(left + 3), rows = scalar_load(left + 4);
+    if (first < 0) return;  // and the rest says nothing
     constexpr int kLanes = D / 4, kAtOnce = kThreads / kLanes;
-    const int rows = min(ROWS, s.nq * p.share - tile * ROWS);
     const int l0 = threadIdx.x % kLanes, c = 4 * l0, self = threadIdx.x & 63 & ~(kLanes - 1);
     for (int r0 = blockIdx.y * kAtOnce; r0 < rows; r0 += gridDim.y * kAtOnce) {
         const int r = min(r0 + static_cast<int>(threadIdx.x) / kLanes, rows - 1);
@@ -89,13 +87,13 @@ __global__ __launch_bounds__(kThreads) void join_kernel(const AttnArgs p) {
             }
         }
         if (r0 + static_cast<int>(threadIdx.x) / kLanes >= rows) continue;
-        const int row = tile * ROWS + r, token = token_of(p, row), qh = head * p.share + row - token * p.share;
+        const int row = row0 + r, token = token_of(p, row), qh = head * p.share + row - token * p.share;
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        T* const o = row_ptr<T>(p.out, s.q0 + token, qh) + c;
+        T* const o = row_ptr<T>(p.out, q0 + token, qh) + c;
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[k] = static_cast<T>(v[k] * inv);
         if (p.lse && c == 0)
-            p.lse[int64_t(s.q0 + token) * p.q_heads + qh] =
+            p.lse[int64_t(q0 + token) * p.q_heads + qh] =
                 lse_of(top, l);
     }
 }
@@ -104,7 +102,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(const AttnArgs p) {
 struct Plan {
     int rows, groups, dim;
     size_t bytes() const {
-        return size_t(groups) * (2 * (dim == 64 ? part_floats<64>(rows) : part_floats<128>(rows)) * 4 + 16);
+        return size_t(groups) * (2 * (dim == 64 ? part_floats<64>(rows) : part_floats<128>(rows)) * 4 + 4 * kJoin);
     }
 };
 
@@ -149,7 +147,7 @@ hipError_t launch_kv4_attention(int a_dtype, const Kv4Attention& c, void* worksp
         using S = decltype(shape);
         p.groups = plan_of<S>(c.cache.block.dim).groups;
         p.joins = static_cast<int32_t*>(workspace);
-        p.part = reinterpret_cast<float*>(p.joins + 4 * p.groups);
+        p.part = reinterpret_cast<float*>(p.joins + kJoin * p.groups);
         kernel<<<p.groups, kThreads, 0, stream>>>(p);
         if (hipError_t e = hipGetLastError()) return e;
         const int at_once = kThreads / (S::kDim / 4), rows = max_rows < S::kRows ? static_cast<int>(max_rows) : S::kRows;

@@ -159,7 +159,7 @@ __global__ __launch_bounds__(kThreads, (Few<T, D, NQ>::kResident)) void few_kern
     Place w;
     const bool work = place_of<kRows, kUnit, kPad>(p, &w);
     const int me = w.me;
-    if (threadIdx.x == 0) p.joins[me * 4] = -1;
+    if (threadIdx.x == 0) p.joins[me * kJoin] = -1;
     if (!work) return;
     const Offsets offs = offsets_of<D>(p);
     Seq s = seq_at(p, w.b);
@@ -435,8 +435,8 @@ __global__ __launch_bounds__(kThreads, (Few<T, D, NQ>::kResident)) void few_kern
             }
         }
         if (threadIdx.x == 0 && a > 0 && z == count) {
-            int32_t* const j = p.joins + me * 4;
-            j[1] = w.b, j[2] = w.head, j[3] = w.tile;
+            int32_t* const j = p.joins + me * kJoin;
+            j[1] = w.head, j[2] = s.q0, j[3] = w.tile * kRows, j[4] = min(kRows, rows - w.tile * kRows);
             // the workgroup with the item's first unit
             j[0] = static_cast<int32_t>((w.at - count) / w.chunk);
         }

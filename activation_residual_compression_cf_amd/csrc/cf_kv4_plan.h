@@ -43,9 +43,14 @@ struct AttnArgs {
     float scale_log2;
     float* lse;
     float* part;    // partial O, m and sum
-    int32_t* joins; // what each workgroup leaves to be joined
+    int32_t* joins; // what each workgroup leaves to be joined, kJoin numbers each
     int groups;
 };
+
+// What a workgroup with an item's last units, but not its first, leaves for the second kernel: the workgroup
+// with its first (-1 where there is nothing to join), the K/V head, the sequence's first query
+// token, the item's first row and its rows.
+constexpr int kJoin = 8;
 
 // One sequence's rows and keys.
 struct Seq {
@@ -117,10 +122,22 @@ __device__ __forceinline__ int64_t shfl64(int64_t v, int lane) {
     return static_cast<int64_t>(static_cast<uint64_t>(static_cast<uint32_t>(hi)) << 32 | static_cast<uint32_t>(lo));
 }
 
-// Inclusive sums over the wave's lanes.
+// Sum of v over the lanes up to this one, in 32 bits: within rows of 16 lanes, and then from row to row.
+__device__ __forceinline__ uint32_t wave_scan32(uint32_t v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);  // one lane up
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // row 0's last to row 1, 2's to 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // row 1's last to rows 2 and 3
+    return v;
+}
+
+// Inclusive sums over the wave's lanes, of values that are not negative.
 __device__ __forceinline__ int64_t wave_scan(int64_t v) {
+    if (__all(v < int64_t(1) << 25)) return wave_scan32(static_cast<uint32_t>(v));
     const int lane = threadIdx.x & 63;
-#pragma unroll
+#pragma unroll 1
     for (int d = 1; d < 64; d <<= 1) {
         const int64_t x = shfl64(v, lane - d);
         if (lane >= d) v += x;
@@ -146,12 +163,14 @@ __device__ __forceinline__ bool place_of(const AttnArgs& p, Place* x) {
     const int each = 64 / sub;
     const auto head_cost = [&](int b) -> int64_t {
         int64_t n = 0;
+        int tiles = 0;
         if (b < p.batch) {
             const Seq s = seq_of(p, b);
-            const int tiles = tiles_of<ROWS>(p, s);
+            tiles = tiles_of<ROWS>(p, s);
             int u0;
             for (int i = lane & (sub - 1); i < tiles; i += sub) n += units_of<ROWS, UNIT>(p, s, i, &u0) + PAD;
         }
+        if (__all(tiles <= 1)) return shfl64(n, lane & ~(sub - 1));
         for (int d = 1; d < sub; d <<= 1) n += shfl64(n, lane ^ d);
         return n;
     };
@@ -195,6 +214,11 @@ __device__ __forceinline__ bool place_of(const AttnArgs& p, Place* x) {
     rest -= x->head * per_head;
     const Seq s = seq_at(p, x->b);
     const int tiles = tiles_of<ROWS>(p, s);
+    if (tiles == 1) {
+        x->tile = 0;
+        x->rest = rest;
+        return true;
+    }
     for (int t0 = 0;; t0 += 64) {
         int u0;
         const int cost = t0 + lane < tiles ? units_of<ROWS, UNIT>(p, s, t0 + lane, &u0) + PAD : 0;
