@@ -121,6 +121,26 @@ __device__ __forceinline__ void load_rows(Rows<D, PARTS>& x, const AttnArgs& p, 
 }
 
 // The kernel for few rows: its four waves share the item's 16 * NQ rows and take its units in turn.
+//
+// What a wave does with 32 keys and 16 rows (matrix products of 16 x 16 with 32 terms; lane =
+// 16 g + n):
+//   S^T = K Q^T   K rows are keys; lane (g, n) holds a quarter of key row n's channels, which
+//                 is one load of codes, and the codes become bf16 by the hardware's
+//                 conversion with the group's scale.  Rows are keys in such an order that
+//                 lane (g, n) ends up with the scores of keys 8g .. 8g+7 for row n.
+//   O^T = V^T P^T the terms are keys: lane (g, n) needs keys 8g .. 8g+7 of its rows, which it
+//                 has, and of channel piece n, which is how the cache lays V out: one load.
+//                 Conversions give pairs of channels of one key; a byte permutation makes
+//                 pairs of keys of them.
+// So nothing passes through shared memory, and m, the sum and the rescaling of O are a
+// lane's own.  The next unit's codes are loaded, and the page numbers of the one after it, while
+// one is worked on (with the numbers loaded beside the codes: 235 us for 64 conversations of 0
+// to 32768 keys, 233 MB, where it now takes 59).  Three contexts of 65537 keys, 642 MB, take
+// 131 us, 4.9 TB/s.
+//
+// Workgroups are as many as are resident: with 1024 where 768 fit, the last 256 ran by themselves
+// (76 against 66 us), and with two or three rounds of resident ones starts and joins cost more than
+// the balance gains (72, 75 us).
 template <typename T, int D, int NQ>
 struct Few {
     using Type = T;
@@ -204,7 +224,7 @@ __global__ __launch_bounds__(kThreads, (Few<T, D, NQ>::kResident)) void few_kern
         }
 
         vf4 o[NQ][kJ];
-        float m[NQ], sum[NQ];  // m: reference in units of log2, raised by kLift
+        float m[NQ], sum[NQ];  // m: reference in units of log2, lowered by kLift
 #pragma unroll
         for (int i = 0; i < NQ; ++i) {
             m[i] = kNone, sum[i] = 0.f;

@@ -10,6 +10,10 @@ typedef float vf16 __attribute__((ext_vector_type(16)));
 
 // Four waves, each with 32 rows of its own, over tiles of 64 keys that all of them
 // decode once, into shared memory: K as bf16 [key][channel], V as fp16 [channel][key].
+// Decoding in registers, as the kernel for few rows does, took a third of the vector units'
+// time at 64 rows a wave (165 us for 1024 queries over 4608 keys in 24 heads of 128, where the
+// tiles take 86).  64 rows a wave here leave one wave a SIMD, which nothing overlaps: 229 us.
+// 4096 queries over 16384 keys run at 955 TFLOP/s at 128 channels and 775 at 64.
 template <typename T, int D>
 struct Wide {
     using Type = T;
@@ -18,9 +22,13 @@ struct Wide {
     static constexpr int kP = sizeof(T) == 4 ? 2 : 1;
     static constexpr int kRows = 32 * kWaves;
     static constexpr int kKeys = 64;
-    // with two waves a SIMD the order of reads and products is fixed; three hide it, and lack registers
+    // Whether the order of reads and products is fixed, four reads ahead: with two waves a SIMD each
+    // product would wait for its read (97 against 99 us for the 1024 queries).  Three waves hide
+    // that, and lack the registers (534 against 600 us for 2925 queries over 17550 keys of 64).
     static constexpr bool kAhead = D == 128;
-    static constexpr int kResident = sizeof(T) == 4 ? 128 / D : D == 64 ? 3 : 2;  // workgroups of a compute unit
+    // workgroups of a compute unit, by their registers; at 64 channels 2 take 597 us and 4, which spill,
+    // 591 where 3 take 543
+    static constexpr int kResident = sizeof(T) == 4 ? 128 / D : D == 64 ? 3 : 2;
     static constexpr int kPad = 2;
     // K's rows are 16 bytes longer than they need to be: 16 rows then start on different banks
     static constexpr int kKRow = 2 * D + 16;
@@ -28,7 +36,8 @@ struct Wide {
     // V's rows (a channel's 64 keys) lie two together in 256 bytes, as 16 runs of 8 keys: run q of
     // channel c is number (8 (c & 1) + q) ^ v_turn(c / 2).  Both the 16 consecutive channels that
     // a product reads and the 16 channel pieces that the decoding threads write then lie on
-    // different banks.  The turn of c / 2 + x is that of c / 2, ^ x, for x below 4 (2 at 64
+    // different banks (without: half of the LDS cycles were conflicts, 108 against 99 us for the 1024
+    // queries).  The turn of c / 2 + x is that of c / 2, ^ x, for x below 4 (2 at 64
     // channels) and c a piece's first.
     __host__ __device__ static constexpr int v_turn(int pair) {
         return D == 128 ? (pair & 7) ^ (pair >> 3 & 3) ^ (pair >> 5 & 1) << 3
