@@ -29,10 +29,11 @@ struct Wide {
     // workgroups of a compute unit, by their registers; at 64 channels 2 take 597 us and 4, which spill,
     // 591 where 3 take 543
     static constexpr int kResident = sizeof(T) == 4 ? 128 / D : D == 64 ? 3 : 2;
-    static constexpr int kPad = 2;
+    static constexpr int kPad = 5;  // 2 takes 231 us for the five prompts in chunks, 3 219, 5 216
     // K's rows are 16 bytes longer than they need to be: 16 rows then start on different banks
     static constexpr int kKRow = 2 * D + 16;
     static constexpr int kTile = kKeys * kKRow + D * 2 * kKeys;
+    static_assert(kKeys * kKRow % 256 == 0 && kTile % 256 == 0, "V's rows start on 256 bytes");
     // V's rows (a channel's 64 keys) lie two together in 256 bytes, as 16 runs of 8 keys: run q of
     // channel c is number (8 (c & 1) + q) ^ v_turn(c / 2).  Both the 16 consecutive channels that
     // a product reads and the 16 channel pieces that the decoding threads write then lie on
@@ -98,11 +99,11 @@ __device__ __forceinline__ void load_share(Share<D>& x, const AttnArgs& p, const
     x.vs = *reinterpret_cast<const uint32_t*>(base + in * (D / 32) + o.vs);
 }
 
-// Decodes a share into a tile, of whose keys the sequence has the first `left`.  Keys behind them
+// Decodes a share into the tile at lds + tile_at, of whose keys the sequence has the first `left`.  Keys behind them
 // become zeros whatever their bytes, and so do groups that read NaN: returns whether the
 // wave has any of those, and then k_nan and v_nan, [key][group], say which of its keys' do.
 template <int D>
-__device__ __forceinline__ bool store_share(Share<D>& x, uint8_t* tile, uint8_t* k_nan, uint8_t* v_nan, int left) {
+__device__ __forceinline__ bool store_share(Share<D>& x, uint8_t* lds, uint32_t tile_at, uint8_t* k_nan, uint8_t* v_nan, int left) {
     using W = Wide<__bf16, D>;
     const int kin = threadIdx.x / 4, vin = threadIdx.x / 32 * 8 + (threadIdx.x & 1) * 4, n = threadIdx.x / 2 & 15;
     uint32_t v[4];  // the channels of a key
@@ -138,7 +139,7 @@ __device__ __forceinline__ bool store_share(Share<D>& x, uint8_t* tile, uint8_t*
     }
     {
         const float f = scale_of(x.ks);
-        uint8_t* const w = tile + kin * W::kKRow + (threadIdx.x & 3) * (D / 2);
+        uint8_t* const w = lds + (tile_at + kin * W::kKRow + (threadIdx.x & 3) * (D / 2));
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
             const uint32_t c = x.k[i];
@@ -150,11 +151,12 @@ __device__ __forceinline__ bool store_share(Share<D>& x, uint8_t* tile, uint8_t*
 #pragma unroll
         for (int t = 0; t < 4; ++t) f[t] = scale_of(x.vs >> (8 * t) & 0xffu);
         const int first = n * (D / 32), turn = W::v_turn(first) ^ vin / 8;  // pair of channels
-        uint8_t* const w = tile + W::kKeys * W::kKRow + first * 256 + (vin & 4) * 2;
+        // a turn of the address: tiles start on 256 bytes
+        const uint32_t w = static_cast<uint32_t>(W::kKeys * W::kKRow + first * 256 + (vin & 4) * 2 + 16 * turn) + tile_at;
         const auto pair = [&](int j, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-            *reinterpret_cast<vu2*>(w + 256 * j + 16 * (turn ^ j)) =
+            *reinterpret_cast<vu2*>(lds + ((w ^ 16 * j) + 256 * j)) =
                 vu2{__builtin_amdgcn_perm(b, a, 0x05040100u), __builtin_amdgcn_perm(d, c, 0x05040100u)};
-            *reinterpret_cast<vu2*>(w + 256 * j + 16 * (turn ^ j ^ 8)) =
+            *reinterpret_cast<vu2*>(lds + ((w ^ 16 * (j ^ 8)) + 256 * j)) =
                 vu2{__builtin_amdgcn_perm(b, a, 0x07060302u), __builtin_amdgcn_perm(d, c, 0x07060302u)};
         };
         pair(0, to_f16<0>(v[0], f[0]), to_f16<0>(v[1], f[1]), to_f16<0>(v[2], f[2]), to_f16<0>(v[3], f[3]));
@@ -183,7 +185,7 @@ __global__ __launch_bounds__(kThreads, (Wide<T, D>::kResident)) void wide_kernel
     constexpr int kRows = W::kRows, kPad = W::kPad, kParts = W::kParts, kP = W::kP, kKeys = W::kKeys;
     constexpr int kDt = D / 32;
     const int lane = threadIdx.x & 63, wave = uniform(static_cast<int>(threadIdx.x) >> 6), n = lane & 31, h = lane >> 5;
-    __shared__ __align__(16) uint8_t lds[W::kBytes];
+    __shared__ __align__(256) uint8_t lds[W::kBytes];
     __shared__ uint32_t flag[2][kWaves];
     __shared__ uint8_t k_nan[2][kKeys * 4], v_nan[2][kKeys * kDt];
 
@@ -254,7 +256,7 @@ __global__ __launch_bounds__(kThreads, (Wide<T, D>::kResident)) void wide_kernel
             for (int k = 0; k < 16; ++k) o[j][k] = 0.f;
 
         const auto store_next = [&](int buf, int key0) {
-            const bool nan = store_share<D>(next, lds + buf * W::kTile, k_nan[buf], v_nan[buf], s.len - key0);
+            const bool nan = store_share<D>(next, lds, buf * W::kTile, k_nan[buf], v_nan[buf], s.len - key0);
             if (lane == 0) flag[buf][wave] = (nan ? 1u : 0u) | (next.on ? 0u : 2u);
         };
         __syncthreads();  // the last item's tiles have been read
@@ -265,7 +267,6 @@ __global__ __launch_bounds__(kThreads, (Wide<T, D>::kResident)) void wide_kernel
         for (int u = a; u < z; ++u) {
             const int buf = (u - a) & 1;
             const uint8_t* const kt = lds + buf * W::kTile;
-            const uint8_t* const vt = kt + kKeys * W::kKRow;
             const int key0 = (u0 + u) * kKeys;
             // what the tile's writers saw in their 16 keys: 1 a group that reads NaN, 2 no page
             const uint32_t f4[4] = {flag[buf][0], flag[buf][1], flag[buf][2], flag[buf][3]};
@@ -284,6 +285,8 @@ __global__ __launch_bounds__(kThreads, (Wide<T, D>::kResident)) void wide_kernel
                     kf[f / 4 & 1][f & 3] = *reinterpret_cast<const vb8*>(kn + f / (D / 16) * 32 * W::kKRow + f % (D / 16) * 32);
             };
             read_k(0);
+            // products go before the other waves' probabilities: 2% of the 2925 queries' time
+            __builtin_amdgcn_s_setprio(1);
 #pragma unroll
             for (int f0 = 0; f0 < kFrags; f0 += 4) {
                 if (f0 + 4 < kFrags) read_k(f0 + 4);
@@ -300,6 +303,7 @@ __global__ __launch_bounds__(kThreads, (Wide<T, D>::kResident)) void wide_kernel
                     }
                 stay<W::kAhead>();
             }
+            __builtin_amdgcn_s_setprio(0);
             // score r is of key mine0 + 16 * (r / 8) + r % 8, r in [0, 32)
             const int mine0 = key0 + 8 * h;
             if (nans) {
@@ -361,19 +365,20 @@ __global__ __launch_bounds__(kThreads, (Wide<T, D>::kResident)) void wide_kernel
             };
             // V's fragments: number f is of half f / (2 kDt), terms 16 (f % 2), channels 32 (f / 2 % kDt)
             constexpr int kVFrags = 4 * kDt;
-            const uint8_t* const vn = vt + n / 2 * 256;
+            const uint32_t vn = buf * W::kTile + kKeys * W::kKRow + n / 2 * 256 + 16 * v_lane;
             vh8 vf[2][4];
             const auto read_v = [&](int f0) {
 #pragma unroll
                 for (int f = f0; f < f0 + 4; ++f) {
                     const int g = f / (2 * kDt), j = f / 2 % kDt, t = f & 1;
-                    vf[f / 4 & 1][f & 3] = *reinterpret_cast<const vh8*>(
-                        vn + j * 4096 + 16 * (v_lane ^ (4 * g + 2 * t) ^ W::v_turn(16 * j)));
+                    vf[f / 4 & 1][f & 3] =
+                        *reinterpret_cast<const vh8*>(lds + ((vn ^ 16 * (4 * g + 2 * t ^ W::v_turn(16 * j))) + j * 4096));
                 }
             };
             read_v(0);
             stay<W::kAhead>();
             exps(0, 0, 16);
+            __builtin_amdgcn_s_setprio(1);
 #pragma unroll
             for (int f0 = 0; f0 < kVFrags; f0 += 4) {
                 if (f0 + 4 < kVFrags) read_v(f0 + 4);
@@ -389,6 +394,7 @@ __global__ __launch_bounds__(kThreads, (Wide<T, D>::kResident)) void wide_kernel
                 if (f0 < kVFrags / 2) exps(1, f0 * 32 / kVFrags, 4 * 32 / kVFrags);
                 stay<W::kAhead>();
             }
+            __builtin_amdgcn_s_setprio(0);
             if (u + 1 < z) {
                 store_next(buf ^ 1, key0 + kKeys);
                 if (u + 2 < z) load_next(u + 2);
