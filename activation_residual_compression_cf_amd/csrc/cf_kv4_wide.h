@@ -186,7 +186,7 @@ __global__ __launch_bounds__(kThreads, (Wide<T, D>::kResident)) void wide_kernel
     constexpr int kDt = D / 32;
     const int lane = threadIdx.x & 63, wave = uniform(static_cast<int>(threadIdx.x) >> 6), n = lane & 31, h = lane >> 5;
     __shared__ __align__(256) uint8_t lds[W::kBytes];
-    __shared__ uint32_t flag[2][kWaves];
+    __shared__ uint32_t flag[2];  // of a tile's 16 keys, a byte for each wave: 1 a group that reads NaN, 2 no page
     __shared__ uint8_t k_nan[2][kKeys * 4], v_nan[2][kKeys * kDt];
 
     Place w;
@@ -257,7 +257,7 @@ __global__ __launch_bounds__(kThreads, (Wide<T, D>::kResident)) void wide_kernel
 
         const auto store_next = [&](int buf, int key0) {
             const bool nan = store_share<D>(next, lds, buf * W::kTile, k_nan[buf], v_nan[buf], s.len - key0);
-            if (lane == 0) flag[buf][wave] = (nan ? 1u : 0u) | (next.on ? 0u : 2u);
+            if (lane == 0) reinterpret_cast<uint8_t*>(&flag[buf])[wave] = (nan ? 1 : 0) | (next.on ? 0 : 2);
         };
         __syncthreads();  // the last item's tiles have been read
         store_next(0, (u0 + a) * kKeys);
@@ -268,11 +268,9 @@ __global__ __launch_bounds__(kThreads, (Wide<T, D>::kResident)) void wide_kernel
             const int buf = (u - a) & 1;
             const uint8_t* const kt = lds + buf * W::kTile;
             const int key0 = (u0 + u) * kKeys;
-            // what the tile's writers saw in their 16 keys: 1 a group that reads NaN, 2 no page
-            const uint32_t f4[4] = {flag[buf][0], flag[buf][1], flag[buf][2], flag[buf][3]};
-            const uint32_t seen_by = uniform(static_cast<int>(f4[0] | f4[1] << 2 | f4[2] << 4 | f4[3] << 6));
-            const bool edge = key0 < full_lo || key0 + kKeys > full_hi || (seen_by & 0xaa) != 0;
-            const bool nans = (seen_by & 0x55) != 0;
+            const uint32_t seen_by = uniform(static_cast<int>(flag[buf]));
+            const bool edge = key0 < full_lo || key0 + kKeys > full_hi || (seen_by & 0x02020202u) != 0;
+            const bool nans = (seen_by & 0x01010101u) != 0;
 
             // K's fragments: number f is terms 16 (f % (D/16)) of half f / (D/16) of the keys
             constexpr int kFrags = 2 * D / 16;
@@ -311,13 +309,13 @@ __global__ __launch_bounds__(kThreads, (Wide<T, D>::kResident)) void wide_kernel
                 uint32_t k_bad = 0, v_bad[kDt] = {};
 #pragma unroll 1
                 for (int r = 0; r < 32; ++r)
-                    if (seen_by >> (2 * (r / 8)) & 1u) {
+                    if (seen_by >> (8 * (r / 8)) & 1u) {
                         const uint8_t* const y = k_nan[buf] + 4 * (8 * h + 16 * (r / 8) + r % 8);
                         k_bad |= static_cast<uint32_t>((y[0] | y[1] | y[2] | y[3]) != 0) << r;
                     }
 #pragma unroll 1
                 for (int t = 0; t < kKeys; ++t)
-                    if (seen_by >> (2 * (t / 16)) & 1u) {
+                    if (seen_by >> (8 * (t / 16)) & 1u) {
 #pragma unroll
                         for (int j = 0; j < kDt; ++j)
                             v_bad[j] |= key0 + t >= lo && key0 + t < hi ? v_nan[buf][t * kDt + j] : 0u;
@@ -335,7 +333,7 @@ __global__ __launch_bounds__(kThreads, (Wide<T, D>::kResident)) void wide_kernel
 #pragma unroll
                 for (int r = 0; r < 32; ++r) {
                     const int key = mine0 + 16 * (r / 8) + r % 8;
-                    if ((seen_by >> (2 * (r / 8)) & 2u) || key < lo || key >= hi) sc[r / 16][r % 16] = kNone;
+                    if ((seen_by >> (8 * (r / 8)) & 2u) || key < lo || key >= hi) sc[r / 16][r % 16] = kNone;
                 }
             }
             float top = kNone;
