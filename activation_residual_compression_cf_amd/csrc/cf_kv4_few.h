@@ -135,8 +135,8 @@ __device__ __forceinline__ void load_rows(Rows<D, PARTS>& x, const AttnArgs& p, 
 // So nothing passes through shared memory, and m, the sum and the rescaling of O are a
 // lane's own.  The next unit's codes are loaded, and the page numbers of the one after it, while
 // one is worked on (with the numbers loaded beside the codes: 235 us for 64 conversations of 0
-// to 32768 keys, 233 MB, where it now takes 59).  Three contexts of 65537 keys, 642 MB, take
-// 131 us, 4.9 TB/s.
+// to 32768 keys, 233 MB, where call and join now take 56).  Three contexts of 65537 keys, 642 MB,
+// take 129 us, 5.0 TB/s.
 //
 // Workgroups are as many as are resident: with 1024 where 768 fit, the last 256 ran by themselves
 // (76 against 66 us), and with two or three rounds of resident ones starts and joins cost more than

@@ -14,7 +14,6 @@
 namespace cf {
 namespace {
 
-typedef _Float16 vh2 __attribute__((ext_vector_type(2)));
 typedef _Float16 vh8 __attribute__((ext_vector_type(8)));
 typedef uint32_t vu4 __attribute__((ext_vector_type(4)));
 

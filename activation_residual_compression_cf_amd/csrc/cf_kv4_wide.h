@@ -12,7 +12,7 @@ typedef float vf16 __attribute__((ext_vector_type(16)));
 // decode once, into shared memory: K as bf16 [key][channel], V as fp16 [channel][key].
 // Decoding in registers, as the kernel for few rows does, took a third of the vector units'
 // time at 64 rows a wave (165 us for 1024 queries over 4608 keys in 24 heads of 128, where the
-// tiles take 86).  64 rows a wave here leave one wave a SIMD, which nothing overlaps: 229 us.
+// tiles take 88).  64 rows a wave here leave one wave a SIMD, which nothing overlaps: 229 us.
 // 4096 queries over 16384 keys run at 955 TFLOP/s at 128 channels and 775 at 64.
 template <typename T, int D>
 struct Wide {
