@@ -122,8 +122,17 @@ Plan plan_of(int head_dim) {
 
 }  // namespace
 
+// The largest of what the kernels for up to so many rows use: a kernel for more rows may take less (it has
+// fewer workgroups resident), and a workspace has to serve every call with fewer rows too.
 size_t kv4_attention_workspace(int a_dtype, int head_dim, int64_t max_rows) {
-    return with_kernel(a_dtype, head_dim, max_rows, [&](auto shape, auto) { return plan_of<decltype(shape)>(head_dim).bytes(); });
+    size_t most = 0;
+    for (const int64_t rows : {1, 17, 33}) {  // the fewest of each kernel
+        if (rows > max_rows) break;
+        const size_t n = with_kernel(a_dtype, head_dim, rows,
+                                     [&](auto shape, auto) { return plan_of<decltype(shape)>(head_dim).bytes(); });
+        most = n > most ? n : most;
+    }
+    return most;
 }
 
 hipError_t launch_kv4_attention(int a_dtype, const Kv4Attention& c, void* workspace, hipStream_t stream) {

@@ -347,7 +347,8 @@ int cf_kv4_read(int a_dtype, const uint8_t* cache, int64_t pages, int page_size,
  *   kv_lens: batch int32; lengths are cut to [0, table_width * page_size];
  *   q_starts: batch + 1 int32, or NULL: total_q / batch queries each, without a rest.  Rows of
  *     out and lse that belong to no sequence stay as they are.
- *   max_q: the most query tokens of a sequence, a bound that the caller knows (0: total_q).
+ *   max_q: the most query tokens of a sequence, a bound that the caller knows (0: total_q, or
+ *     total_q / batch where q_starts is NULL).
  *     It chooses the kernel and the workspace; the results are right for any lengths.
  *   workspace: cf_kv4_attention_workspace_bytes, 256-byte aligned; nothing in it has to be
  *     set before a call, and nothing is kept in it for the next.
@@ -366,8 +367,9 @@ int cf_kv4_attention(int a_dtype, const cf_rows* q, int64_t total_q, int q_heads
                      int window, float scale, const cf_rows* out, float* lse, void* workspace, size_t ws_bytes,
                      void* stream);
 
-/* Workspace bytes of cf_kv4_attention (0 for arguments outside the limits): max_q as there, or
- * total_q where that is 0. */
+/* Workspace bytes of cf_kv4_attention (0 for arguments outside the limits): max_q as there; where
+ * that is 0, total_q with q_starts and total_q / batch without.  Never less for a larger max_q: a
+ * workspace of one call's bytes serves every call with fewer queries. */
 size_t cf_kv4_attention_workspace_bytes(int a_dtype, int64_t max_q, int q_heads, int kv_heads, int head_dim);
 
 /* Workspace bytes cf_lowrank_compress needs (0 for arguments outside the limits). */
