@@ -653,7 +653,7 @@ def kv4_attention(q: torch.Tensor, cache: KV4Cache, kv_lens: torch.Tensor, table
     sequence b has pages b * table_width and on, without q_starts every sequence has
     total_q / batch queries.  lse (total_q, q_heads) fp32 is written where it is given.  Rows
     that belong to no sequence stay as they are.  max_q: the most queries of a sequence, if
-    known; scale: head_dim ** -0.5 if None."""
+    known (a bound above total_q is as good as total_q); scale: head_dim ** -0.5 if None."""
     if q.dim() != 3:
         raise ValueError("q must be (total_q, q_heads, head_dim)")
     total, heads, dim = q.shape
@@ -661,6 +661,8 @@ def kv4_attention(q: torch.Tensor, cache: KV4Cache, kv_lens: torch.Tensor, table
         raise ValueError(f"q has rows of {dim}, the cache of {cache.head_dim}")
     dt, dev, kv_heads = _act_dtype(q), _device(q), cache.data.shape[1]
     batch = kv_lens.numel()
+    if max_q > total:
+        max_q = total
     if kv_lens.dtype != torch.int32:
         raise TypeError(f"kv_lens is {kv_lens.dtype}; libcf wants torch.int32")
     pt = None

@@ -531,9 +531,10 @@ int cf_kv4_attention(int a_dtype, const cf_rows* q, int64_t total_q, int q_heads
     const int64_t cache_bytes = cf_kv4_cache_bytes(pages, page_size, kv_heads, head_dim);
     if (cache_bytes < 0) return CF_E_SHAPE;
     if (q_heads < 1 || q_heads > 65535 || q_heads % kv_heads || total_q < 0 || total_q > INT32_MAX / q_heads ||
-        max_q < 0 || max_q > total_q)
+        max_q < 0)
         return CF_E_SHAPE;
     if (total_q == 0) return CF_OK;
+    if (max_q > total_q) return CF_E_SHAPE;
     if (batch < 1 || table_width < 1 || int64_t(table_width) * page_size > INT32_MAX - 256 ||
         (!table && int64_t(batch) * table_width > pages) || (!q_starts && total_q % batch))
         return CF_E_SHAPE;

@@ -347,9 +347,10 @@ int cf_kv4_read(int a_dtype, const uint8_t* cache, int64_t pages, int page_size,
  *   kv_lens: batch int32; lengths are cut to [0, table_width * page_size];
  *   q_starts: batch + 1 int32, or NULL: total_q / batch queries each, without a rest.  Rows of
  *     out and lse that belong to no sequence stay as they are.
- *   max_q: the most query tokens of a sequence, a bound that the caller knows (0: total_q, or
- *     total_q / batch where q_starts is NULL).
- *     It chooses the kernel and the workspace; the results are right for any lengths.
+ *   max_q: the most query tokens of a sequence, a bound that the caller knows, at most total_q
+ *     (0: total_q, or total_q / batch where q_starts is NULL).  It chooses the kernel and the
+ *     workspace; the results are right for any lengths.  total_q = 0 is a valid call that does
+ *     nothing, whatever the bound.
  *   workspace: cf_kv4_attention_workspace_bytes, 256-byte aligned; nothing in it has to be
  *     set before a call, and nothing is kept in it for the next.
  * 0 < scale <= 1e38; window >= 0, and 0 unless causal; q_heads a multiple of kv_heads, at most 65535;
