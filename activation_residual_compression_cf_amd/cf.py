@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 
 import torch
@@ -510,6 +511,15 @@ def _shaped(name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple):
         raise ValueError(f"{name} is {tuple(t.shape)}, the call needs {tuple(shape)}")
 
 
+def _fit(fn: str, status: int, form: str, *numbers):
+    """Refuses numbers that the C ABI's int (i) and int64_t (q) cannot hold: ctypes would hand on their
+    lowest bits."""
+    try:
+        struct.pack(form, *numbers)
+    except struct.error:
+        raise CFError(fn, status) from None
+
+
 def _device(t: torch.Tensor) -> int:
     """The current device; no tensor's where t is not on one (there may be none)."""
     return torch._C._cuda_getDevice() if t.is_cuda else -2
@@ -553,6 +563,7 @@ def qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, norm: int = CF_
             _shaped(nm, t, kind, (tokens, h, dim))
             if o is not None:
                 _shaped(nm + "_out", o, kind, t.shape)
+    _fit("cf_qk_norm_rope", -4, "iiii", norm, rope, hq, hk)
     dev = _device(a)
     rq = rk = rqo = rko = None
     if q is not None:
@@ -569,6 +580,7 @@ def qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, norm: int = CF_
         if cos is None or sin is None or cos.dim() != 2:
             raise ValueError("a rotation needs cos and sin, (positions, rot_dim / 2) fp32")
         n_pos, rot = cos.shape
+        _fit("cf_qk_norm_rope", -2, "i", 2 * rot)
         pc, ps = _flat("cos", cos, dev, _F32, (n_pos, rot)), _flat("sin", sin, dev, _F32, (n_pos, rot))
         pp = _flat("positions", positions, dev, torch.int32, (tokens,))
     row = (dim,)
@@ -591,6 +603,7 @@ class KV4Cache:
 
     @staticmethod
     def create(pages: int, page_size: int, kv_heads: int, head_dim: int, device=None) -> "KV4Cache":
+        _fit("cf_kv4_cache_bytes", -2, "qiii", pages, page_size, kv_heads, head_dim)
         nb = lib.cf_kv4_cache_bytes(pages, page_size, kv_heads, head_dim)
         if nb < 0:
             raise CFError("cf_kv4_cache_bytes", nb)
@@ -601,6 +614,7 @@ class KV4Cache:
         d = self.data
         if d.dim() != 3 or d.shape[2] * 16 != self.page_size * self.head_dim * 17:
             raise ValueError(f"cache data is {tuple(d.shape)}: want (pages, kv_heads, page_size * head_dim * 17 / 16)")
+        _fit("KV4Cache", -2, "iii", self.page_size, d.shape[1], self.head_dim)
         return _flat("cache", d, dev, _U8, d.shape), d.shape[0], self.page_size, d.shape[1], self.head_dim
 
 
@@ -638,6 +652,7 @@ def kv4_read(cache: KV4Cache, slots: torch.Tensor, dtype: torch.dtype = torch.bf
 
 def kv4_attention_workspace_bytes(dtype: torch.dtype, max_q: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
     dt = CF_BF16 if dtype == torch.bfloat16 else CF_F32 if dtype == torch.float32 else -1
+    _fit("cf_kv4_attention_workspace_bytes", -2, "qiii", max_q, q_heads, kv_heads, head_dim)
     nb = lib.cf_kv4_attention_workspace_bytes(dt, max_q, q_heads, kv_heads, head_dim)
     if nb == 0:
         raise CFError("cf_kv4_attention_workspace_bytes", -2)
@@ -669,6 +684,7 @@ def kv4_attention(q: torch.Tensor, cache: KV4Cache, kv_lens: torch.Tensor, table
     if table is not None:
         table_width = table.shape[-1]
         pt = _flat("table", table, dev, torch.int32, (batch, table_width))
+    _fit("cf_kv4_attention", -2, "qiiiii", max_q, window, batch, table_width, heads, kv_heads)
     pq = _flat("q_starts", q_starts, dev, torch.int32, (batch + 1,))
     pe = _flat("lse", lse, dev, _F32, (total, heads))
     pl = _flat("kv_lens", kv_lens, dev, torch.int32, (batch,))

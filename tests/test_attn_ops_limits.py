@@ -67,3 +67,82 @@ def test_binding_cuts_the_bound_to_the_queries(cf, monkeypatch):
     seen.clear()
     cf.kv4_attention(q[:0], cache, lens, q_starts=starts, table_width=1, max_q=4)
     assert seen[-1][1][14] in (0, 4)
+
+
+def _on_host(cf, monkeypatch):
+    """The binding without a device: calls are noted, and report success."""
+    seen = []
+    strerror = cf.lib.cf_strerror
+
+    class Lib:
+        cf_strerror = staticmethod(strerror)
+
+        def __getattr__(self, name):
+            return lambda *a: seen.append((name, a)) or (1 << 20 if name.endswith("_bytes") else 0)
+
+    monkeypatch.setattr(cf, "lib", Lib())
+    monkeypatch.setattr(cf, "_here", lambda *a: None)
+    monkeypatch.setattr(cf, "_on", lambda *a: None)
+    return seen
+
+
+TOO_BIG = [1 << 31, (1 << 32) + 5, -(1 << 32) + 5, 1 << 70]
+
+
+@pytest.mark.parametrize("n", TOO_BIG)
+def test_binding_refuses_numbers_past_32_bits(cf, monkeypatch, n):
+    """An int of the C ABI takes the lowest 32 bits of what it is given: a window of 2^32 + 5 would be one of 5."""
+    import torch
+
+    lib = cf.lib
+    with pytest.raises(cf.CFError):
+        cf.KV4Cache.create(1, 16 + n, 1, 64, device="cpu")
+    with pytest.raises(cf.CFError):
+        cf.KV4Cache.create(1, 16, 1 + n, 64, device="cpu")
+    with pytest.raises(cf.CFError):
+        cf.KV4Cache.create(1, 16, 1, 64 + n, device="cpu")
+    with pytest.raises(cf.CFError):
+        cf.kv4_attention_workspace_bytes(torch.bfloat16, 1, 8 + n, 2, 64)
+    with pytest.raises(cf.CFError):
+        cf.kv4_attention_workspace_bytes(torch.bfloat16, 1, 8, 2 + n, 64)
+    with pytest.raises(cf.CFError):
+        cf.kv4_attention_workspace_bytes(torch.bfloat16, 1, 8, 2, 64 + n)
+    seen = _on_host(cf, monkeypatch)
+    q = torch.zeros(3, 2, 64, dtype=torch.bfloat16)
+    cache = cf.KV4Cache(torch.zeros(2, 2, 16 * 68, dtype=torch.uint8), 16, 64)
+    lens, starts = torch.zeros(2, dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
+    good = dict(q_starts=starts, table_width=1)
+    cf.kv4_attention(q, cache, lens, **good, causal=True, window=(1 << 31) - 1)
+    assert seen[-1][1][16] == (1 << 31) - 1
+    for bad in (dict(good, causal=True, window=n), dict(good, table_width=n), dict(good, table_width=n, max_q=1)):
+        seen.clear()
+        with pytest.raises(cf.CFError):
+            cf.kv4_attention(q, cache, lens, **bad)
+        assert not [x for x in seen if x[0] == "cf_kv4_attention"]
+    row = torch.zeros(2, 2, 64)
+    for bad in (dict(norm=cf.CF_NORM_RMS + n), dict(rope=cf.CF_ROPE_HALF + n, cos=torch.zeros(4, 32), sin=torch.zeros(4, 32))):
+        seen.clear()
+        with pytest.raises(cf.CFError):
+            cf.qk_norm_rope(row, row, **bad)
+        assert not seen
+    for bad in (cf.KV4Cache(cache.data, 16, 64 + n), cf.KV4Cache(cache.data, 16 + n, 64)):
+        with pytest.raises((ValueError, cf.CFError)):
+            cf.kv4_append(bad, q, q, torch.zeros(3, dtype=torch.int64))
+    assert lib.cf_kv4_cache_bytes(1, 16, 1, 64) > 0
+
+
+@pytest.mark.parametrize("n", [1 << 63, -(1 << 63) - 1])
+def test_binding_refuses_numbers_past_64_bits(cf, monkeypatch, n):
+    """cf_kv4_cache_bytes(2^64 + 1, ...) would be that of one page."""
+    import torch
+
+    with pytest.raises(cf.CFError):
+        cf.KV4Cache.create(1 + 2 * n, 16, 1, 64, device="cpu")
+    with pytest.raises(cf.CFError):
+        cf.kv4_attention_workspace_bytes(torch.bfloat16, 1 + 2 * n, 8, 2, 64)
+    seen = _on_host(cf, monkeypatch)
+    q = torch.zeros(3, 2, 64, dtype=torch.bfloat16)
+    cache = cf.KV4Cache(torch.zeros(2, 2, 16 * 68, dtype=torch.uint8), 16, 64)
+    with pytest.raises(cf.CFError):
+        cf.kv4_attention(q, cache, torch.zeros(3, dtype=torch.int32), table_width=1, max_q=-2 * (1 << 63) + 1)
+    assert not [x for x in seen if x[0] == "cf_kv4_attention"]
