@@ -146,6 +146,8 @@ struct RowsOf {
 // Rows of one call: a row takes at least 8 work-items, of which a dispatch counts 2^32 - 1.
 constexpr int64_t kMaxRows = int64_t(1) << 28;
 constexpr wide kMaxExtent = wide(1) << 46;  // bytes: beyond any device's memory
+// Sequences of one attention call: every workgroup counts through them, 64 at a time and in 32 bits.
+constexpr int kMaxSequences = 1 << 24;
 
 // NULL, strides, alignment of one operand's rows, in this order.
 int check_rows(const cf_rows* r, int64_t tokens, int64_t heads, int64_t dim, int64_t esz, bool written, RowsOf* x) {
@@ -535,7 +537,7 @@ int cf_kv4_attention(int a_dtype, const cf_rows* q, int64_t total_q, int q_heads
         return CF_E_SHAPE;
     if (total_q == 0) return CF_OK;
     if (max_q > total_q) return CF_E_SHAPE;
-    if (batch < 1 || table_width < 1 || int64_t(table_width) * page_size > INT32_MAX - 256 ||
+    if (batch < 1 || batch > kMaxSequences || table_width < 1 || int64_t(table_width) * page_size > INT32_MAX - 256 ||
         (!table && int64_t(batch) * table_width > pages) || (!q_starts && total_q % batch))
         return CF_E_SHAPE;
     if (!cache || !kv_lens || !workspace) return CF_E_NULL;

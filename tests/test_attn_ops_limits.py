@@ -146,3 +146,13 @@ def test_binding_refuses_numbers_past_64_bits(cf, monkeypatch, n):
     with pytest.raises(cf.CFError):
         cf.kv4_attention(q, cache, torch.zeros(3, dtype=torch.int32), table_width=1, max_q=-2 * (1 << 63) + 1)
     assert not [x for x in seen if x[0] == "cf_kv4_attention"]
+
+
+def test_number_of_sequences(cf, L):
+    """The plan counts through the sequences in 64s and in 32 bits: 2^31 - 1 of them would never end."""
+    most = 1 << 24
+    many = dict(total=12, width=1, lens=4 * G, table=9 * G)
+    assert attn(cf, batch=most, **many) == CF_E_DEVICE
+    for batch in (most + 1, (1 << 31) - 64, (1 << 31) - 1):
+        assert attn(cf, batch=batch, **many) == CF_E_SHAPE, batch
+        assert attn(cf, batch=batch, **{**many, "total": 0}) == CF_OK
