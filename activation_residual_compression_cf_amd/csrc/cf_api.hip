@@ -148,6 +148,8 @@ constexpr int64_t kMaxRows = int64_t(1) << 28;
 constexpr wide kMaxExtent = wide(1) << 46;  // bytes: beyond any device's memory
 // Sequences of one attention call: every workgroup counts through them, 64 at a time and in 32 bits.
 constexpr int kMaxSequences = 1 << 24;
+// Query tokens times query heads of one: a tile of up to 128 rows behind the last still counts in 32 bits.
+constexpr int64_t kMaxAttnRows = (int64_t(1) << 31) - 256;
 
 // NULL, strides, alignment of one operand's rows, in this order.
 int check_rows(const cf_rows* r, int64_t tokens, int64_t heads, int64_t dim, int64_t esz, bool written, RowsOf* x) {
@@ -517,7 +519,7 @@ int cf_kv4_read(int a_dtype, const uint8_t* cache, int64_t pages, int page_size,
 
 size_t cf_kv4_attention_workspace_bytes(int a_dtype, int64_t max_q, int q_heads, int kv_heads, int head_dim) {
     if ((a_dtype != CF_BF16 && a_dtype != CF_F32) || !kv4_dims(16, kv_heads, head_dim) || q_heads < 1 ||
-        q_heads > 65535 || q_heads % kv_heads || max_q < 1 || max_q > INT32_MAX / q_heads)
+        q_heads > 65535 || q_heads % kv_heads || max_q < 1 || max_q > kMaxAttnRows / q_heads)
         return 0;
     return cf::kv4_attention_workspace(a_dtype, head_dim, max_q * (q_heads / kv_heads));
 }
@@ -532,7 +534,7 @@ int cf_kv4_attention(int a_dtype, const cf_rows* q, int64_t total_q, int q_heads
     if (!(scale > 0.f) || scale > 1e38f) return CF_E_ARG;
     const int64_t cache_bytes = cf_kv4_cache_bytes(pages, page_size, kv_heads, head_dim);
     if (cache_bytes < 0) return CF_E_SHAPE;
-    if (q_heads < 1 || q_heads > 65535 || q_heads % kv_heads || total_q < 0 || total_q > INT32_MAX / q_heads ||
+    if (q_heads < 1 || q_heads > 65535 || q_heads % kv_heads || total_q < 0 || total_q > kMaxAttnRows / q_heads ||
         max_q < 0)
         return CF_E_SHAPE;
     if (total_q == 0) return CF_OK;

@@ -156,3 +156,16 @@ def test_number_of_sequences(cf, L):
     for batch in (most + 1, (1 << 31) - 64, (1 << 31) - 1):
         assert attn(cf, batch=batch, **many) == CF_E_SHAPE, batch
         assert attn(cf, batch=batch, **{**many, "total": 0}) == CF_OK
+
+
+def test_number_of_rows(cf, L):
+    """Rows are counted in tiles of up to 128 and in 32 bits: the end of the last tile has to fit."""
+    f = cf.lib.cf_kv4_attention_workspace_bytes
+    most = (1 << 31) - 256
+    big = dict(hq=1, hk=1, pages=50, q=(G, 0, 0), out=(1 << 45, 64, 64), lse=0, max_q=0)
+    assert attn(cf, total=most, **big) == CF_E_DEVICE
+    assert f(0, most, 1, 1, 64) > 0 and f(0, most // 8, 8, 2, 64) > 0
+    for total in (most + 1, (1 << 31) - 1):
+        assert attn(cf, total=total, **big) == CF_E_SHAPE, total
+        assert f(0, total, 1, 1, 64) == 0
+    assert attn(cf, total=most // 8 + 1, q=(G, 0, 0), out=(1 << 45, 512, 64), lse=0, max_q=0) == CF_E_SHAPE
