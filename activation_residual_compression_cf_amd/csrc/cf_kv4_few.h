@@ -111,11 +111,7 @@ __device__ __forceinline__ void load_rows(Rows<D, PARTS>& x, const AttnArgs& p, 
         for (int j = 0; j < 8; ++j) {
             float rest = on ? f[j] : 0.f;
 #pragma unroll
-            for (int k = 0; k < PARTS; ++k) {
-                const __bf16 h = static_cast<__bf16>(rest);
-                x.q[k][i][j] = h;
-                rest -= static_cast<float>(h);
-            }
+            for (int k = 0; k < PARTS; ++k) x.q[k][i][j] = take_bf16(&rest);
         }
     }
 }

@@ -243,6 +243,14 @@ __device__ __forceinline__ float across_sum(float v) {
     return v + __shfl_xor(v, 32, 64);
 }
 
+// The leading eight bits of an fp32 number, which it loses: three in turn are all of it.  Cut off, not
+// rounded: rounded, numbers from 3.396e38 on would become infinite.
+__device__ __forceinline__ __bf16 take_bf16(float* rest) {
+    const uint32_t top = __float_as_uint(*rest) & 0xffff0000u;
+    *rest -= __uint_as_float(top);
+    return __builtin_bit_cast(__bf16, static_cast<uint16_t>(top >> 16));
+}
+
 // bf16 pair of byte B of codes c.
 template <int B>
 __device__ __forceinline__ uint32_t to_bf16(uint32_t c, float s) {

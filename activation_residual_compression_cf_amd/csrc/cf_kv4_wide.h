@@ -236,11 +236,7 @@ __global__ __launch_bounds__(kThreads, (Wide<T, D>::kResident)) void wide_kernel
             for (int j = 0; j < 8; ++j) {
                 float rest = on ? f[j] : 0.f;
 #pragma unroll
-                for (int k = 0; k < kParts; ++k) {
-                    const __bf16 y = static_cast<__bf16>(rest);
-                    q[k][c][j] = y;
-                    rest -= static_cast<float>(y);
-                }
+                for (int k = 0; k < kParts; ++k) q[k][c][j] = take_bf16(&rest);
             }
         }
         const int lo = on ? seen_lo(p, s, token) : 0, hi = on ? seen_hi(p, s, token) : 0;  // keys that the row sees
