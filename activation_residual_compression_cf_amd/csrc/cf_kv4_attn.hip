@@ -5,9 +5,9 @@
 // and sum.  A row is one (query token, query head); the rows of the query heads that share a
 // K/V head are worked on together.
 //
-// Precision.  K is exact in bf16 and V in fp16 (the cache's exponents see to that), and so are
-// bf16 queries; fp32 queries are split into three bf16 parts that add up to them.  P is
-// rounded to fp16 (half a step is 2^-11 of it), from fp32 queries to a sum of two fp16.  Sums,
+// Precision.  K is exact in bf16 and V in fp16 (the cache's exponents see to that) and in bf16, and so are
+// bf16 queries; fp32 queries are split into three bf16 parts that add up to them, and so are their
+// probabilities.  With bf16 queries P is rounded to fp16 (half a step is 2^-11 of it).  Sums,
 // references and O are fp32, and the sum is of unrounded probabilities.
 //
 // Work.  It is cut into units of 32 (few rows) or 64 keys of one item, an item being up to kRows

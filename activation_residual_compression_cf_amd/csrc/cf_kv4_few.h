@@ -132,7 +132,7 @@ __device__ __forceinline__ void load_rows(Rows<D, PARTS>& x, const AttnArgs& p, 
 // lane's own.  The next unit's codes are loaded, and the page numbers of the one after it, while
 // one is worked on (with the numbers loaded beside the codes: 235 us for 64 conversations of 0
 // to 32768 keys, 233 MB, where call and join now take 56).  Three contexts of 65537 keys, 642 MB,
-// take 129 us, 5.0 TB/s.
+// take 140 us with fp32 queries, 4.6 TB/s (129 with two parts of P in place of three).
 //
 // Workgroups are as many as are resident: with 1024 where 768 fit, the last 256 ran by themselves
 // (76 against 66 us), and with two or three rounds of resident ones starts and joins cost more than
@@ -142,7 +142,7 @@ struct Few {
     using Type = T;
     static constexpr int kDim = D;
     static constexpr int kParts = sizeof(T) == 4 ? 3 : 1;  // bf16 parts of a query
-    static constexpr int kP = sizeof(T) == 4 ? 2 : 1;      // fp16 parts of a probability
+    static constexpr int kP = Prob<T>::kParts;             // parts of a probability
     static constexpr int kRows = 16 * NQ;
     static constexpr int kKeys = kUnit;
     static constexpr int kPad = 12;  // 8 takes 66 us for the 64 conversations, 12 and 14 59
@@ -297,7 +297,7 @@ __global__ __launch_bounds__(kThreads, (Few<T, D, NQ>::kResident)) void few_kern
                 }
             }
 
-            vh8 pf[NQ][kP];
+            typename Prob<T>::Frag pf[NQ][kP];
 #pragma unroll
             for (int i = 0; i < NQ; ++i) {
                 float x2[8];  // scores in units of log2
@@ -331,9 +331,7 @@ __global__ __launch_bounds__(kThreads, (Few<T, D, NQ>::kResident)) void few_kern
                 for (int t = 0; t < 8; ++t) {
                     x2[t] = __builtin_amdgcn_exp2f(x2[t] - ref);
                     sum[i] += x2[t];
-                    const _Float16 h = static_cast<_Float16>(x2[t]);
-                    pf[i][0][t] = h;
-                    if constexpr (kP == 2) pf[i][1][t] = static_cast<_Float16>(x2[t] - static_cast<float>(h));
+                    Prob<T>::set(pf[i], t, x2[t]);
                 }
                 if (nans) {
                     // a NaN of V reaches the rows that see its key, and only those
@@ -364,35 +362,34 @@ __global__ __launch_bounds__(kThreads, (Few<T, D, NQ>::kResident)) void few_kern
                 for (int i = 0; i < NQ; ++i)
 #pragma unroll
                     for (int k = kP - 1; k >= 0; --k) {
-                        o[i][2 * j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(vh8, even), pf[i][k],
-                                                                            o[i][2 * j], 0, 0, 0);
-                        o[i][2 * j + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(vh8, odd_),
-                                                                                pf[i][k], o[i][2 * j + 1], 0, 0, 0);
+                        using Frag = typename Prob<T>::Frag;
+                        o[i][2 * j] = Prob<T>::mul16(__builtin_bit_cast(Frag, even), pf[i][k], o[i][2 * j]);
+                        o[i][2 * j + 1] = Prob<T>::mul16(__builtin_bit_cast(Frag, odd_), pf[i][k], o[i][2 * j + 1]);
                     }
             };
             if constexpr (D == 128) {
                 uint32_t c[8];
 #pragma unroll
-                for (int t = 0; t < 8; ++t) c[t] = to_f16<0>(x.v[t], vs[t]);
+                for (int t = 0; t < 8; ++t) c[t] = Prob<T>::template decode<0>(x.v[t], vs[t]);
                 pv(0, c);
 #pragma unroll
-                for (int t = 0; t < 8; ++t) c[t] = to_f16<1>(x.v[t], vs[t]);
+                for (int t = 0; t < 8; ++t) c[t] = Prob<T>::template decode<1>(x.v[t], vs[t]);
                 pv(1, c);
 #pragma unroll
-                for (int t = 0; t < 8; ++t) c[t] = to_f16<2>(x.v[t], vs[t]);
+                for (int t = 0; t < 8; ++t) c[t] = Prob<T>::template decode<2>(x.v[t], vs[t]);
                 pv(2, c);
 #pragma unroll
-                for (int t = 0; t < 8; ++t) c[t] = to_f16<3>(x.v[t], vs[t]);
+                for (int t = 0; t < 8; ++t) c[t] = Prob<T>::template decode<3>(x.v[t], vs[t]);
                 pv(3, c);
             } else {
                 uint32_t c[8];
 #pragma unroll
                 for (int t = 0; t < 8; ++t)
-                    c[t] = t & 1 ? to_f16<2>(x.v[t / 2], vs[t]) : to_f16<0>(x.v[t / 2], vs[t]);
+                    c[t] = t & 1 ? Prob<T>::template decode<2>(x.v[t / 2], vs[t]) : Prob<T>::template decode<0>(x.v[t / 2], vs[t]);
                 pv(0, c);
 #pragma unroll
                 for (int t = 0; t < 8; ++t)
-                    c[t] = t & 1 ? to_f16<3>(x.v[t / 2], vs[t]) : to_f16<1>(x.v[t / 2], vs[t]);
+                    c[t] = t & 1 ? Prob<T>::template decode<3>(x.v[t / 2], vs[t]) : Prob<T>::template decode<1>(x.v[t / 2], vs[t]);
                 pv(1, c);
             }
         }

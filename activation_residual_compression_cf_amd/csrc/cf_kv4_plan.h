@@ -15,6 +15,7 @@ namespace cf {
 namespace {
 
 typedef _Float16 vh8 __attribute__((ext_vector_type(8)));
+typedef float vf16 __attribute__((ext_vector_type(16)));
 typedef uint32_t vu4 __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 256;
@@ -260,6 +261,53 @@ template <int B>
 __device__ __forceinline__ uint32_t to_f16(uint32_t c, float s) {
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, s, B));
 }
+
+// What probabilities and V are multiplied in.  bf16 queries: P rounded to fp16 (half a step is 2^-11 of it).
+// fp32 queries: three bf16 parts that add up to P, whatever its size (two fp16 parts run out of exponents: a
+// tail e^-22 below one key was 10% off, and one e^-26 below was lost).
+template <typename T>
+struct Prob;
+
+template <>
+struct Prob<__bf16> {
+    static constexpr int kParts = 1;
+    using Frag = vh8;
+    template <int K>
+    static __device__ __forceinline__ void set(Frag (&f)[K], int i, float e) {
+        f[0][i] = static_cast<_Float16>(e);
+    }
+    template <int B>
+    static __device__ __forceinline__ uint32_t decode(uint32_t c, float s) {
+        return to_f16<B>(c, s);
+    }
+    static __device__ __forceinline__ vf4 mul16(Frag a, Frag b, vf4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ vf16 mul32(Frag a, Frag b, vf16 c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+    }
+};
+
+template <>
+struct Prob<float> {
+    static constexpr int kParts = 3;
+    using Frag = vb8;
+    template <int K>
+    static __device__ __forceinline__ void set(Frag (&f)[K], int i, float e) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) f[k][i] = take_bf16(&e);
+    }
+    template <int B>
+    static __device__ __forceinline__ uint32_t decode(uint32_t c, float s) {
+        return to_bf16<B>(c, s);
+    }
+    static __device__ __forceinline__ vf4 mul16(Frag a, Frag b, vf4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ vf16 mul32(Frag a, Frag b, vf16 c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+    }
+};
 
 // log sum exp of a row from its reference, in units of log2, and its sum.
 __device__ __forceinline__ float lse_of(float m, float l) {

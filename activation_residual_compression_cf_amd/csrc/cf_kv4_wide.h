@@ -6,10 +6,9 @@
 namespace cf {
 namespace {
 
-typedef float vf16 __attribute__((ext_vector_type(16)));
-
 // Four waves, each with 32 rows of its own, over tiles of 64 keys that all of them
-// decode once, into shared memory: K as bf16 [key][channel], V as fp16 [channel][key].
+// decode once, into shared memory: K as bf16 [key][channel], V as fp16 (bf16 for fp32 queries)
+// [channel][key].
 // Decoding in registers, as the kernel for few rows does, took a third of the vector units'
 // time at 64 rows a wave (165 us for 1024 queries over 4608 keys in 24 heads of 128, where the
 // tiles take 88).  64 rows a wave here leave one wave a SIMD, which nothing overlaps: 229 us.
@@ -19,7 +18,7 @@ struct Wide {
     using Type = T;
     static constexpr int kDim = D;
     static constexpr int kParts = sizeof(T) == 4 ? 3 : 1;
-    static constexpr int kP = sizeof(T) == 4 ? 2 : 1;
+    static constexpr int kP = Prob<T>::kParts;
     static constexpr int kRows = 32 * kWaves;
     static constexpr int kKeys = 64;
     // Whether the order of reads and products is fixed, four reads ahead: with two waves a SIMD each
@@ -102,9 +101,9 @@ __device__ __forceinline__ void load_share(Share<D>& x, const AttnArgs& p, const
 // Decodes a share into the tile at lds + tile_at, of whose keys the sequence has the first `left`.  Keys behind them
 // become zeros whatever their bytes, and so do groups that read NaN: returns whether the
 // wave has any of those, and then k_nan and v_nan, [key][group], say which of its keys' do.
-template <int D>
+template <typename T, int D>
 __device__ __forceinline__ bool store_share(Share<D>& x, uint8_t* lds, uint32_t tile_at, uint8_t* k_nan, uint8_t* v_nan, int left) {
-    using W = Wide<__bf16, D>;
+    using W = Wide<T, D>;
     const int kin = threadIdx.x / 4, vin = threadIdx.x / 32 * 8 + (threadIdx.x & 1) * 4, n = threadIdx.x / 2 & 15;
     uint32_t v[4];  // the channels of a key
 #pragma unroll
@@ -153,17 +152,18 @@ __device__ __forceinline__ bool store_share(Share<D>& x, uint8_t* lds, uint32_t 
         const int first = n * (D / 32), turn = W::v_turn(first) ^ vin / 8;  // pair of channels
         // a turn of the address: tiles start on 256 bytes
         const uint32_t w = static_cast<uint32_t>(W::kKeys * W::kKRow + first * 256 + (vin & 4) * 2 + 16 * turn) + tile_at;
+        using V = Prob<T>;
         const auto pair = [&](int j, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
             *reinterpret_cast<vu2*>(lds + ((w ^ 16 * j) + 256 * j)) =
                 vu2{__builtin_amdgcn_perm(b, a, 0x05040100u), __builtin_amdgcn_perm(d, c, 0x05040100u)};
             *reinterpret_cast<vu2*>(lds + ((w ^ 16 * (j ^ 8)) + 256 * j)) =
                 vu2{__builtin_amdgcn_perm(b, a, 0x07060302u), __builtin_amdgcn_perm(d, c, 0x07060302u)};
         };
-        pair(0, to_f16<0>(v[0], f[0]), to_f16<0>(v[1], f[1]), to_f16<0>(v[2], f[2]), to_f16<0>(v[3], f[3]));
-        pair(1, to_f16<1>(v[0], f[0]), to_f16<1>(v[1], f[1]), to_f16<1>(v[2], f[2]), to_f16<1>(v[3], f[3]));
+        pair(0, V::template decode<0>(v[0], f[0]), V::template decode<0>(v[1], f[1]), V::template decode<0>(v[2], f[2]), V::template decode<0>(v[3], f[3]));
+        pair(1, V::template decode<1>(v[0], f[0]), V::template decode<1>(v[1], f[1]), V::template decode<1>(v[2], f[2]), V::template decode<1>(v[3], f[3]));
         if constexpr (D == 128) {
-            pair(2, to_f16<2>(v[0], f[0]), to_f16<2>(v[1], f[1]), to_f16<2>(v[2], f[2]), to_f16<2>(v[3], f[3]));
-            pair(3, to_f16<3>(v[0], f[0]), to_f16<3>(v[1], f[1]), to_f16<3>(v[2], f[2]), to_f16<3>(v[3], f[3]));
+            pair(2, V::template decode<2>(v[0], f[0]), V::template decode<2>(v[1], f[1]), V::template decode<2>(v[2], f[2]), V::template decode<2>(v[3], f[3]));
+            pair(3, V::template decode<3>(v[0], f[0]), V::template decode<3>(v[1], f[1]), V::template decode<3>(v[2], f[2]), V::template decode<3>(v[3], f[3]));
         }
     }
     return nan;
@@ -252,7 +252,7 @@ __global__ __launch_bounds__(kThreads, (Wide<T, D>::kResident)) void wide_kernel
             for (int k = 0; k < 16; ++k) o[j][k] = 0.f;
 
         const auto store_next = [&](int buf, int key0) {
-            const bool nan = store_share<D>(next, lds, buf * W::kTile, k_nan[buf], v_nan[buf], s.len - key0);
+            const bool nan = store_share<T, D>(next, lds, buf * W::kTile, k_nan[buf], v_nan[buf], s.len - key0);
             if (lane == 0) reinterpret_cast<uint8_t*>(&flag[buf])[wave] = (nan ? 1 : 0) | (next.on ? 0 : 2);
         };
         __syncthreads();  // the last item's tiles have been read
@@ -345,28 +345,27 @@ __global__ __launch_bounds__(kThreads, (Wide<T, D>::kResident)) void wide_kernel
                 for (int j = 0; j < kDt; ++j) o[j] *= f;
             }
             const float ref = m == kNone ? 0.f : -m;
-            vh8 pf[2][kP][2];
+            using Frag = typename Prob<T>::Frag;
+            Frag pf[2][2][kP];
             // probabilities r0 .. r0 + many - 1 of half g
             const auto exps = [&](int g, int r0, int many) {
 #pragma unroll
                 for (int r = r0; r < r0 + many; ++r) {
                     const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[g][r], p.scale_log2, ref));
                     sum += e;
-                    const _Float16 y = static_cast<_Float16>(e);
-                    pf[g][0][r / 8][r % 8] = y;
-                    if constexpr (kP == 2) pf[g][1][r / 8][r % 8] = static_cast<_Float16>(e - static_cast<float>(y));
+                    Prob<T>::set(pf[g][r / 8], r % 8, e);
                 }
             };
             // V's fragments: number f is of half f / (2 kDt), terms 16 (f % 2), channels 32 (f / 2 % kDt)
             constexpr int kVFrags = 4 * kDt;
             const uint32_t vn = buf * W::kTile + kKeys * W::kKRow + n / 2 * 256 + 16 * v_lane;
-            vh8 vf[2][4];
+            Frag vf[2][4];
             const auto read_v = [&](int f0) {
 #pragma unroll
                 for (int f = f0; f < f0 + 4; ++f) {
                     const int g = f / (2 * kDt), j = f / 2 % kDt, t = f & 1;
                     vf[f / 4 & 1][f & 3] =
-                        *reinterpret_cast<const vh8*>(lds + ((vn ^ 16 * (4 * g + 2 * t ^ W::v_turn(16 * j))) + j * 4096));
+                        *reinterpret_cast<const Frag*>(lds + ((vn ^ 16 * (4 * g + 2 * t ^ W::v_turn(16 * j))) + j * 4096));
                 }
             };
             read_v(0);
@@ -382,7 +381,7 @@ __global__ __launch_bounds__(kThreads, (Wide<T, D>::kResident)) void wide_kernel
 #pragma unroll
                     for (int k = kP - 1; k >= 0; --k) {
                         vf16& x = o[f / 2 % kDt];
-                        x = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf[f / 4 & 1][f & 3], pf[f / (2 * kDt)][k][f & 1], x, 0, 0, 0);
+                        x = Prob<T>::mul32(vf[f / 4 & 1][f & 3], pf[f / (2 * kDt)][f & 1][k], x);
                     }
                 // the other half's probabilities beside this half's products
                 if (f0 < kVFrags / 2) exps(1, f0 * 32 / kVFrags, 4 * 32 / kVFrags);

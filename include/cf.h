@@ -356,7 +356,7 @@ int cf_kv4_read(int a_dtype, const uint8_t* cache, int64_t pages, int page_size,
  * 0 < scale <= 1e38; window >= 0, and 0 unless causal; q_heads a multiple of kv_heads, at most 65535;
  * total_q * q_heads <= 2^31 - 256, table_width * page_size < 2^31 - 256, 1 <= batch <= 2^24.
  * K and V enter the products exactly.  bf16: queries exactly, probabilities rounded to fp16;
- * fp32: queries exactly, probabilities to 22 bits.  Scores, sums and results are fp32 up to
+ * fp32: queries and probabilities exactly.  Scores, sums and results are fp32 up to
  * the final rounding to a_dtype.  Results are deterministic for given lengths; a row's last
  * bits depend on the batch it is computed in, which is split into equal parts.
  */

@@ -48,3 +48,59 @@ def test_largest_fp32_queries(cf, dev, nq, dim):
     c.q[0, 0, 1] = 3.3961775e38  # the first that rounds to infinity in bf16
     assert c.q.isfinite().all()
     c.check(*c.run(cf, scale=2.0 ** -108), scale=2.0 ** -108)
+
+
+class Sink:
+    """`batch` sequences that share one cache, in which all of the 8 heads hold the same: key `at` takes nearly all
+    of the weight and has V = 0, the others have V of about one.  Enough sequences that no workgroup's run of keys is
+    much shorter than a sequence.  Row r's first key lies 8 to 32 nats above the others."""
+
+    def __init__(self, cf, dev, length, nq, batch, dim, dtype, at=0, seed=0):
+        rng = np.random.default_rng(seed)
+        self.length, self.nq, self.batch, self.dim, self.dtype = length, nq, batch, dim, dtype
+        page, heads = 64, 8
+        pages = -(-length // page)
+        self.cache = cf.KV4Cache.create(pages, page, heads, dim, device=dev)
+        k, v = np.zeros((length, 1, dim), np.float32), np.ones((length, 1, dim), np.float32)
+        k[at, 0, 0] = 6
+        k[:, 0, 32] = rng.choice(ref.LEVELS, length)
+        k[at, 0, 32] = 0
+        v += rng.choice([0, 0.5, 1], (length, 1, dim)).astype(np.float32)
+        v[at] = 0
+        self.k, self.v = ref.quantize(k), ref.quantize(v)
+        wide = lambda x: torch.from_numpy(x).to(dev).expand(length, heads, dim)
+        cf.kv4_append(self.cache, wide(k), wide(v), torch.arange(length, device=dev))
+        q = np.zeros((nq, heads, dim), np.float32)
+        self.scale = dim ** -0.5
+        q[:, :, 0] = (np.linspace(8, 32, nq * heads) / (6 * self.scale)).reshape(nq, heads)
+        q[:, :, 32] = 0.05 + 0.02 * rng.random((nq, heads))
+        self.q = torch.from_numpy(q).to(DT[dtype]).to(dev)
+        self.many = self.q.repeat(batch, 1, 1)
+        self.table = torch.arange(pages, dtype=torch.int32, device=dev).expand(batch, pages).contiguous()
+        self.lens = torch.full((batch,), length, dtype=torch.int32, device=dev)
+
+    def run(self, cf):
+        lse = torch.empty(self.many.shape[:2], device=self.many.device)
+        out = cf.kv4_attention(self.many, self.cache, self.lens, table=self.table, max_q=self.nq, lse=lse)
+        torch.cuda.synchronize()
+        shape = (self.batch, self.nq, 8)
+        return host(out.double()).reshape(*shape, self.dim), host(lse.double()).reshape(shape)
+
+    def want(self):
+        """(out, lse, and their bounds without the rounding of probabilities and the last one): relative to what is
+        added up to each result, which is the result, since V is not negative."""
+        return ref.attention(host(self.q.double()), self.k, self.v, self.nq, self.scale, False, 0)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("length,nq,batch,at", [(16385, 1, 64, 0), (16385, 1, 64, 9001), (6001, 20, 32, 64), (4099, 40, 32, 0), (4099, 40, 32, 2050)])
+def test_long_tail_below_one_key_fp32(cf, dev, dim, length, nq, batch, at):
+    """Probabilities of fp32 queries are exact at any size: no term for their rounding."""
+    say(f"kv4 attention fp32 tail below key {at} of {length} nq={nq} dim={dim}")
+    c = Sink(cf, dev, length, nq, batch, dim, "f32", at)
+    out, lse = c.run(cf)
+    o, l, bo, bl = c.want()
+    far = np.abs(out - o)
+    bound = bo + ref.HALF_STEP["f32"] * o
+    assert (far <= bound).all(), f"{(far / bound).max():.3g} of the bound, {(far / o).max():.3g} of the value"
+    assert (np.abs(lse - l) <= bl).all()
