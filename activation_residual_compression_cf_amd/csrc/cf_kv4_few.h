@@ -327,12 +327,14 @@ __global__ __launch_bounds__(kThreads, (Few<T, D, NQ>::kResident)) void few_kern
                     for (int j = 0; j < kJ; ++j) o[i][j] *= f;
                 }
                 const float ref = m[i] == kNone ? 0.f : m[i];
+                float more = 0.f;  // first by itself: one by one, small ones would be lost beside a large sum
 #pragma unroll
                 for (int t = 0; t < 8; ++t) {
                     x2[t] = __builtin_amdgcn_exp2f(x2[t] - ref);
-                    sum[i] += x2[t];
+                    more += x2[t];
                     Prob<T>::set(pf[i], t, x2[t]);
                 }
+                sum[i] += more;
                 if (nans) {
                     // a NaN of V reaches the rows that see its key, and only those
                     uint32_t hit = 0;

@@ -347,12 +347,15 @@ __global__ __launch_bounds__(kThreads, (Wide<T, D>::kResident)) void wide_kernel
             const float ref = m == kNone ? 0.f : -m;
             using Frag = typename Prob<T>::Frag;
             Frag pf[2][2][kP];
+            // The tile's sum, first by itself: one by one, small probabilities would be lost beside a large
+            // sum (2e-4 of it after 16385 keys).
+            float more = 0.f;
             // probabilities r0 .. r0 + many - 1 of half g
             const auto exps = [&](int g, int r0, int many) {
 #pragma unroll
                 for (int r = r0; r < r0 + many; ++r) {
                     const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[g][r], p.scale_log2, ref));
-                    sum += e;
+                    more += e;
                     Prob<T>::set(pf[g][r / 8], r % 8, e);
                 }
             };
@@ -388,6 +391,7 @@ __global__ __launch_bounds__(kThreads, (Wide<T, D>::kResident)) void wide_kernel
                 stay<W::kAhead>();
             }
             __builtin_amdgcn_s_setprio(0);
+            sum += more;
             if (u + 1 < z) {
                 store_next(buf ^ 1, key0 + kKeys);
                 if (u + 2 < z) load_next(u + 2);

@@ -104,3 +104,24 @@ def test_long_tail_below_one_key_fp32(cf, dev, dim, length, nq, batch, at):
     bound = bo + ref.HALF_STEP["f32"] * o
     assert (far <= bound).all(), f"{(far / bound).max():.3g} of the bound, {(far / o).max():.3g} of the value"
     assert (np.abs(lse - l) <= bl).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("length,nq,batch", [(40001, 1, 128), (16385, 40, 64), (16385, 300, 16)])
+def test_sums_of_many_keys(cf, dev, dtype, length, nq, batch):
+    """One key of nearly all the weight and thousands of a few 2^-25 of it: added to the sum one by one, each would
+    be rounded away.  A lane adds up its up to 32 probabilities of 64 keys first, so a sum has the roundings of those,
+    of one addition for each 64 keys, and of joining lanes, waves and parts: under length / 64 + 100, of at most
+    the sum each, and the parts' own factors are among them."""
+    say(f"kv4 attention sum over {length} keys nq={nq} {dtype}")
+    c = Sink(cf, dev, length, nq, batch, 64, dtype)
+    _, lse = c.run(cf)
+    q, k = host(c.q.double())[:, :, [0, 32]], c.k[:, 0, [0, 32]]
+    s = q @ k.T * c.scale
+    m = s.max(-1)
+    want = m + np.log(np.exp(s - m[..., None]).sum(-1))
+    # a score's two products, scaled, shifted and raised, as in attention's bound
+    err = (64 + 8) * ref.F24 * 2 * np.abs(m)
+    far = np.abs(lse - want)
+    bound = 2 * err + (length / 64 + 100) * ref.F24
+    assert (far <= bound).all(), f"{(far / bound).max():.3g} of the bound"
