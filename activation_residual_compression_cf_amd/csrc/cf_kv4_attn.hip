@@ -7,7 +7,7 @@
 //
 // Precision.  K is exact in bf16 and V in fp16 (the cache's exponents see to that) and in bf16, and so are
 // bf16 queries; fp32 queries are split into three bf16 parts that add up to them, and so are their
-// probabilities.  With bf16 queries P is rounded to fp16 (half a step is 2^-11 of it).  Sums,
+// probabilities.  With bf16 queries P is rounded to fp16 (half a step is 2^-11 of the largest of its tile).  Sums,
 // references and O are fp32, and the sum is of unrounded probabilities.
 //
 // Work.  It is cut into units of 32 (few rows) or 64 keys of one item, an item being up to kRows

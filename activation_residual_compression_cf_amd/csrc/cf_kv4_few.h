@@ -220,10 +220,10 @@ __global__ __launch_bounds__(kThreads, (Few<T, D, NQ>::kResident)) void few_kern
         }
 
         vf4 o[NQ][kJ];
-        float m[NQ], sum[NQ];  // m: reference in units of log2, lowered by kLift
+        float m[NQ], sum[NQ], high[NQ];  // m: reference in units of log2, lowered by kLift
 #pragma unroll
         for (int i = 0; i < NQ; ++i) {
-            m[i] = kNone, sum[i] = 0.f;
+            m[i] = high[i] = kNone, sum[i] = 0.f;
 #pragma unroll
             for (int j = 0; j < kJ; ++j) o[i][j] = vf4{0.f, 0.f, 0.f, 0.f};
         }
@@ -317,9 +317,15 @@ __global__ __launch_bounds__(kThreads, (Few<T, D, NQ>::kResident)) void few_kern
                 float top = kNone;
 #pragma unroll
                 for (int t = 0; t < 8; ++t) top = fmaxf(top, x2[t]);
-                if (__any(top > m[i] + (kSlack + kLift))) {
+                uint64_t low = 0;  // rows whose lanes all lie far below, in the first sixteen bits
+                if constexpr (Prob<T>::kFalls) {
+                    low = __ballot(top < m[i] - kDrop);
+                    low &= low >> 32;
+                    low &= low >> 16;
+                }
+                if (__any(top > m[i] + (kSlack + kLift)) || (low & 0xffffu)) {
                     // the lanes of a row agree on its new reference
-                    const float r = fmaxf(across_max(top) - kLift, m[i]);
+                    const float r = next_ref<T>(across_max(top), m[i], &high[i]);
                     const float f = m[i] == r ? 1.f : __builtin_amdgcn_exp2f(m[i] - r);
                     m[i] = r;
                     sum[i] *= f;
@@ -421,6 +427,13 @@ __global__ __launch_bounds__(kThreads, (Few<T, D, NQ>::kResident)) void few_kern
         };
 #pragma unroll
         for (int i = 0; i < NQ; ++i) {
+            if (Prob<T>::kFalls && __any(m[i] != high[i])) {  // lse is more exact from the highest reference
+                const float f = m[i] == high[i] ? 1.f : __builtin_amdgcn_exp2f(m[i] - high[i]);
+                m[i] = high[i];
+                sum[i] *= f;
+#pragma unroll
+                for (int j = 0; j < kJ; ++j) o[i][j] *= f;
+            }
             sum[i] = across_sum(sum[i]);
             __syncthreads();
             float* const y = stage + (wave * 16 + n) * (D + 4) + g * (D / 4);

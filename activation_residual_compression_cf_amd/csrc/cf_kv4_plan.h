@@ -28,6 +28,13 @@ constexpr int kMinUnits = 8;
 // reference moves, and O is rescaled, only when a score exceeds it by more.  p stays below
 // 2^(kLift + kSlack) < 65504, and the lift keeps the fp16 of small p off the subnormals.
 constexpr float kLift = 7.f, kSlack = 8.f;
+// With P in fp16 the reference falls too, where a whole tile's largest p is below 2^-kDrop, fp16's smallest
+// normal number: behind a key that outweighs the rest, their p would be subnormals or zero (a tail e^-22 below
+// lost 13% in 16385 keys, one e^-26 below half or more).  So a p is off by at most 2^-11 of itself or of its
+// tile's largest.  Queries and keys with channels 20 times the others' meet falls in many tiles: 4096 over 16384
+// keys take 4% more with them, 2925 over 17550 2.7% (kDrop 10: 1% more again), few rows up to 3%.  It falls at most
+// kDeep below its highest: O, 2^(kLift + kSlack + kDeep) times 2^31 keys times 2^16, fits fp32.
+constexpr float kDrop = 14.f, kDeep = 60.f;
 constexpr float kNone = -__builtin_inff();
 
 struct AttnArgs {
@@ -271,6 +278,7 @@ struct Prob;
 template <>
 struct Prob<__bf16> {
     static constexpr int kParts = 1;
+    static constexpr bool kFalls = true;  // the reference
     using Frag = vh8;
     template <int K>
     static __device__ __forceinline__ void set(Frag (&f)[K], int i, float e) {
@@ -291,6 +299,7 @@ struct Prob<__bf16> {
 template <>
 struct Prob<float> {
     static constexpr int kParts = 3;
+    static constexpr bool kFalls = false;
     using Frag = vb8;
     template <int K>
     static __device__ __forceinline__ void set(Frag (&f)[K], int i, float e) {
@@ -308,6 +317,19 @@ struct Prob<float> {
         return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
     }
 };
+
+// Where a row's reference goes: up to its tile's largest score, in units of log2, where that is above it (lowered
+// by kLift); down to it, with P in fp16, from far above; high is the highest it has been.
+template <typename T>
+__device__ __forceinline__ float next_ref(float top, float m, float* high) {
+    float r = fmaxf(top - kLift, m);
+    if constexpr (Prob<T>::kFalls) {
+        // a tile that the row sees nothing of moves nothing
+        if (top < m - kDrop && top > kNone) r = fmaxf(top - kLift, *high - kDeep);
+        *high = fmaxf(*high, r);
+    }
+    return r;
+}
 
 // log sum exp of a row from its reference, in units of log2, and its sum.
 __device__ __forceinline__ float lse_of(float m, float l) {

@@ -245,7 +245,7 @@ __global__ __launch_bounds__(kThreads, (Wide<T, D>::kResident)) void wide_kernel
         if (row1 >= row0) full_lo = seen_lo(p, s, token_of(p, row1)), full_hi = seen_hi(p, s, token_of(p, row0));
 
         vf16 o[kDt];
-        float m = kNone, sum = 0.f;  // m: reference in units of log2, lowered by kLift
+        float m = kNone, sum = 0.f, high = kNone;  // m: reference in units of log2, lowered by kLift
 #pragma unroll
         for (int j = 0; j < kDt; ++j)
 #pragma unroll
@@ -336,8 +336,13 @@ __global__ __launch_bounds__(kThreads, (Wide<T, D>::kResident)) void wide_kernel
 #pragma unroll
             for (int r = 0; r < 32; ++r) top = fmaxf(top, sc[r / 16][r % 16]);
             top *= p.scale_log2;
-            if (__any(top > m + (kSlack + kLift))) {
-                const float r = fmaxf(fmaxf(top, __shfl_xor(top, 32, 64)) - kLift, m);
+            uint64_t low = 0;  // rows whose two lanes lie far below, in the first 32 bits
+            if constexpr (Prob<T>::kFalls) {
+                low = __ballot(top < m - kDrop);
+                low &= low >> 32;
+            }
+            if (__any(top > m + (kSlack + kLift)) || low) {
+                const float r = next_ref<T>(fmaxf(top, __shfl_xor(top, 32, 64)), m, &high);
                 const float f = m == r ? 1.f : __builtin_amdgcn_exp2f(m - r);
                 m = r;
                 sum *= f;
@@ -399,6 +404,13 @@ __global__ __launch_bounds__(kThreads, (Wide<T, D>::kResident)) void wide_kernel
             }
         }
 
+        if (Prob<T>::kFalls && __any(m != high)) {  // lse is more exact from the highest reference
+            const float f = m == high ? 1.f : __builtin_amdgcn_exp2f(m - high);
+            m = high;
+            sum *= f;
+#pragma unroll
+            for (int j = 0; j < kDt; ++j) o[j] *= f;
+        }
         const bool whole = a == 0 && z == count;
         const float l = sum + __shfl_xor(sum, 32, 64);
         if (on) {

@@ -355,8 +355,9 @@ int cf_kv4_read(int a_dtype, const uint8_t* cache, int64_t pages, int page_size,
  *     set before a call, and nothing is kept in it for the next.
  * 0 < scale <= 1e38; window >= 0, and 0 unless causal; q_heads a multiple of kv_heads, at most 65535;
  * total_q * q_heads <= 2^31 - 256, table_width * page_size < 2^31 - 256, 1 <= batch <= 2^24.
- * K and V enter the products exactly.  bf16: queries exactly, probabilities rounded to fp16;
- * fp32: queries and probabilities exactly.  Scores, sums and results are fp32 up to
+ * K and V enter the products exactly.  bf16: queries exactly, probabilities rounded to fp16, off
+ * by at most 2^-11 of the largest of the 32 or 64 keys that are taken at once, down to 2^-60 of
+ * the row's largest; fp32: queries and probabilities exactly.  Scores, sums and results are fp32 up to
  * the final rounding to a_dtype.  Results are deterministic for given lengths; a row's last
  * bits depend on the batch it is computed in, which is split into equal parts.
  */

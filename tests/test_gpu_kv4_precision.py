@@ -125,3 +125,45 @@ def test_sums_of_many_keys(cf, dev, dtype, length, nq, batch):
     far = np.abs(lse - want)
     bound = 2 * err + (length / 64 + 100) * ref.F24
     assert (far <= bound).all(), f"{(far / bound).max():.3g} of the bound"
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("length,nq,batch,at", [(16385, 1, 64, 0), (16385, 1, 64, 9001), (6001, 20, 32, 64), (4099, 40, 32, 0), (4099, 40, 32, 2050)])
+def test_long_tail_below_one_key_bf16(cf, dev, dim, length, nq, batch, at):
+    """Probabilities are rounded to fp16: off by 2^-11 of the largest of their 64 keys, which for keys of the tail alone is
+    at most 1.1 times their own size (their scores differ by at most 0.07 * 6 * 64 ** -0.5 nats); beside the first key by
+    up to 2^-32 of that (half a subnormal's step of 2^-24, where the largest is 2^7)."""
+    say(f"kv4 attention bf16 tail below key {at} of {length} nq={nq} dim={dim}")
+    c = Sink(cf, dev, length, nq, batch, dim, "bf16", at)
+    out, lse = c.run(cf)
+    o, l, bo, bl = c.want()
+    far = np.abs(out - o)
+    bound = bo + 1.1 * ref.P_STEP["bf16"] * o + 64 * 2.0 ** -32 * c.v.max() + ref.HALF_STEP["bf16"] * o
+    assert (far <= bound).all(), f"{(far / bound).max():.3g} of the bound, {(far / o).max():.3g} of the value"
+    assert (np.abs(lse - l) <= bl).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("nq", [1, 20, 50])
+def test_scores_that_rise_and_fall_by_a_lot(cf, dev, dtype, dim, nq):
+    """Runs of keys whose scores lie up to 300 nats apart, rising, falling and in turn, beside the largest values:
+    nothing overflows, and a result is off by no more than its own probabilities' rounding."""
+    say(f"kv4 attention, scores that rise and fall {dtype} dim={dim} nq={nq}")
+    rng = np.random.default_rng(nq)
+    n = 1500
+    for shape in ("falling", "rising", "in turn", "steps down"):
+        c = Case(cf, dev, [n], [nq], 1, 1, dim, dtype, page=32, seed=nq)
+        level = {"falling": 6 - np.arange(n) * 12 / n, "rising": np.arange(n) * 12 / n - 6,
+                 "in turn": np.where(np.arange(n) // 100 % 2, 6, -6), "steps down": 6 - np.arange(n) // 200 * 1.5}[shape]
+        k = np.zeros((n, 1, dim), np.float32)
+        k[:, 0, 0] = level
+        k[:, 0, 40] = rng.choice(ref.LEVELS, n)
+        v = rng.standard_normal((n, 1, dim)) * 2.0 ** 13
+        v[:, 0, 32:] = rng.standard_normal((n, dim - 32))
+        put(cf, dev, c, 0, k=k, v=v)
+        c.q[:] = 0
+        c.q[:, 0, 0] = torch.linspace(0.1, 25, nq, device=dev) if nq > 1 else 25
+        c.q[:, 0, 40] = 0.3
+        c.check(*c.run(cf, scale=1.0, max_q=nq), scale=1.0)
+        c.check(*c.run(cf, scale=1.0, max_q=nq, causal=True, window=700), scale=1.0, causal=True, window=700)
