@@ -50,6 +50,25 @@ def test_largest_fp32_queries(cf, dev, nq, dim):
     c.check(*c.run(cf, scale=2.0 ** -108), scale=2.0 ** -108)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("kv,nq", [(300, 1), (9000, 1), (250, 20), (400, 60), (9000, 40)])
+def test_values_at_the_ends_of_their_exponents(cf, dev, kv, nq, dim, dtype):
+    """V from 2^-23, which fp16 holds as a subnormal number, to 6 * 2^13, in whole items and in split ones."""
+    say(f"kv4 attention of the smallest and largest V {dtype} dim={dim} kv={kv} nq={nq}")
+    rng = np.random.default_rng(5)
+    for ends in ([-22, -21, 13, 0], [13, -22, -22, -21]):
+        c = Case(cf, dev, [kv, 17], [nq, 1], 2, 1, dim, dtype, seed=3)
+        for i in range(2):
+            e = np.array(ends)[(np.arange(dim) // 32 + i) % 4]
+            level = rng.choice(ref.LEVELS, (c.kv[i], 1, dim)) * rng.choice([-1, 1], (c.kv[i], 1, dim))
+            put(cf, dev, c, i, v=level * 2.0 ** e)
+            assert np.array_equal(c.v[i], level * 2.0 ** e)  # the least scale differs, the values do not
+        out, lse = c.run(cf, max_q=nq)
+        c.check(out, lse)
+        assert out.any(-1).all()
+
+
 class Sink:
     """`batch` sequences that share one cache, in which all of the 8 heads hold the same: key `at` takes nearly all
     of the weight and has V = 0, the others have V of about one.  Enough sequences that no workgroup's run of keys is
