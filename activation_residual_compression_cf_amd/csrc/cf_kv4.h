@@ -9,7 +9,7 @@ namespace cf {
 
 constexpr int kKvGroup = 32;  // channels that share a scale
 // Exponents of the scales.  Every value the cache can hold, +-6 * 2^13 down to 2^-23, is then
-// a half-precision number, which is what the attention multiplies V in.
+// a half-precision number, which is what the attention multiplies V in for bf16 queries.
 constexpr int kKvExpMin = -22, kKvExpMax = 13;
 constexpr uint32_t kKvNan = 255;     // scale byte of a group that holds a NaN or an infinity
 constexpr uint32_t kKvNanFrom = 192; // bytes from here on read as NaN

@@ -144,7 +144,6 @@ struct Few {
     static constexpr int kParts = sizeof(T) == 4 ? 3 : 1;  // bf16 parts of a query
     static constexpr int kP = Prob<T>::kParts;             // parts of a probability
     static constexpr int kRows = 16 * NQ;
-    static constexpr int kKeys = kUnit;
     static constexpr int kPad = 12;  // 8 takes 66 us for the 64 conversations, 12 and 14 59
     // workgroups of a compute unit, by their registers
     static constexpr int kResident = NQ == 2 ? (D == 128 ? 1 : sizeof(T) == 4 ? 2 : 3) : D == 64 ? 4 : sizeof(T) == 4 ? 2 : 3;

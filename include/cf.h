@@ -285,10 +285,9 @@ enum { CF_ROPE_NONE = 0, CF_ROPE_INTERLEAVED = 1, CF_ROPE_HALF = 2 };
  *     are.  A position of n_pos or more gives rows of NaN.
  *   cos, sin: n_pos x rot_dim/2 fp32.
  * tokens * heads at most 2^28 rows, times head_dim at most 2^33.  head_dim a multiple of 8, at
- * most 256; rot_dim a multiple of 16, at most head_dim; eps
- * finite and not negative.  q_heads or k_heads may be 0 (that side's pointers are then not
- * used).  In place (q_out the same rows as q, k_out as k) is allowed; any other overlap of an
- * output with another operand is not.
+ * most 256; rot_dim a multiple of 16, at most head_dim; eps finite and not negative.  q_heads
+ * or k_heads may be 0 (that side's pointers are then not used).  In place (q_out the same rows
+ * as q, k_out as k) is allowed; any other overlap of an output with another operand is not.
  *   weights, biases, cos, sin: 16-byte aligned; positions 4.
  */
 int cf_qk_norm_rope(int a_dtype, int64_t tokens, int q_heads, int k_heads, int head_dim, const cf_rows* q,
@@ -299,9 +298,9 @@ int cf_qk_norm_rope(int a_dtype, int64_t tokens, int q_heads, int k_heads, int h
 
 /*
  * The 4-bit K/V cache: `pages` pages of `page_size` tokens for each of kv_heads heads, in one
- * buffer of cf_kv4_cache_bytes bytes.  There are fewer than 2^31 pages.  head_dim D is 64 or 128; page_size P is 16, 32, 64, 128
- * or 256.  The block of page p and head h starts at (p * kv_heads + h) * P * D * 17/16 and
- * holds, in this order:
+ * buffer of cf_kv4_cache_bytes bytes.  There are fewer than 2^31 pages.  head_dim D is 64 or
+ * 128; page_size P is 16, 32, 64, 128 or 256.  The block of page p and head h starts at
+ * (p * kv_heads + h) * P * D * 17/16 and holds, in this order:
  *   K codes   [P][D/2]                   low nibble first
  *   V codes   [P/8][16][8 tokens][D/32]  piece n of 16: channels n*D/16 .. of each token
  *   K scales  [P][D/32]                  a byte for each 32 channels
