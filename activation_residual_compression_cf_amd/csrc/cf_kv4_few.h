@@ -131,7 +131,7 @@ __device__ __forceinline__ void load_rows(Rows<D, PARTS>& x, const AttnArgs& p, 
 // So nothing passes through shared memory, and m, the sum and the rescaling of O are a
 // lane's own.  The next unit's codes are loaded, and the page numbers of the one after it, while
 // one is worked on (with the numbers loaded beside the codes: 235 us for 64 conversations of 0
-// to 32768 keys, 233 MB, where call and join now take 56).  Three contexts of 65537 keys, 642 MB,
+// to 32768 keys, 233 MB, where call and join now take 58).  Three contexts of 65537 keys, 642 MB,
 // take 140 us with fp32 queries, 4.6 TB/s (129 with two parts of P in place of three).
 //
 // Workgroups are as many as are resident: with 1024 where 768 fit, the last 256 ran by themselves

@@ -12,7 +12,8 @@ namespace {
 // Decoding in registers, as the kernel for few rows does, took a third of the vector units'
 // time at 64 rows a wave (165 us for 1024 queries over 4608 keys in 24 heads of 128, where the
 // tiles take 88).  64 rows a wave here leave one wave a SIMD, which nothing overlaps: 229 us.
-// 4096 queries over 16384 keys run at 955 TFLOP/s at 128 channels and 775 at 64.
+// 4096 queries over 16384 keys run at 911 TFLOP/s at 128 channels and 752 at 64; with fp32 queries,
+// whose products are three each, 1024 over 4608 take 187 us.
 template <typename T, int D>
 struct Wide {
     using Type = T;
