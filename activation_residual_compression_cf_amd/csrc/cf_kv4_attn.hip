@@ -16,8 +16,9 @@
 // Items that end up in several workgroups leave partial results in the workspace, which a second
 // kernel joins in the order of the keys.
 //
-// The kernel for few rows (at most 32: decoding) is bound by the cache's bytes, the one for many
-// rows by the matrix and vector units; measured figures stand at each.
+// The kernel for few rows (at most 32: decoding) is bound by the cache's bytes, with fp32 queries by the
+// vector units beside them, the one for many rows by the matrix and vector units; measured figures stand
+// at each.
 
 #include <hip/hip_runtime.h>
 
