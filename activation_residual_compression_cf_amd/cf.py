@@ -48,6 +48,18 @@ _SIG = {
     "cf_kv4_read": ("i", "ipliii" "plrr" "p"),
     "cf_kv4_attention": ("i", "irli" "pliii" "ipipp" "liif" "rppzp"),
     "cf_kv4_attention_workspace_bytes": ("z", "iliii"),
+    "cf_kv8_cache_bytes": ("l", "liii"),
+    "cf_kv8_append": ("i", "irrlp" "liiii" "pipp" "p"),
+    "cf_kv8_read": ("i", "ipliii" "plrr" "p"),
+    "cf_kv8_attention": ("i", "irli" "pliii" "ipipp" "liif" "rppzp"),
+    "cf_kv8_attention_workspace_bytes": ("z", "iliii"),
+    "cf_attention": ("i", "irli" "rrl" "iii" "pp" "liif" "rppzp"),
+    "cf_attention_workspace_bytes": ("z", "iliii"),
+    "cf_pages_workspace_bytes": ("z", "li"),
+    "cf_pages_resize": ("i", "gg" "liii" "pp" "pzp"),
+    "cf_pages_fork": ("i", "gg" "liii" "pppp" "pzp"),
+    "cf_pages_compact": ("i", "gg" "lii" "ppp" "pzp"),
+    "cf_pages_copy": ("i", "pllil" "pplpp"),
     "cf_strerror": ("s", "i"),
     "cf_abi_version": ("i", ""),
 }
@@ -58,8 +70,13 @@ class Rows(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
-# r: a pointer to cf_rows, f: float
-_CT = {"r": ctypes.POINTER(Rows), "f": ctypes.c_float, "i": ctypes.c_int, "l": ctypes.c_int64, "p": ctypes.c_void_p, "z": ctypes.c_size_t,
+class Pages(ctypes.Structure):
+    """cf_pages: the arrays that say who holds which page."""
+    _fields_ = [("refs", ctypes.c_void_p), ("table", ctypes.c_void_p), ("lens", ctypes.c_void_p)]
+
+
+# r: a pointer to cf_rows, g: a pointer to cf_pages, f: float
+_CT = {"r": ctypes.POINTER(Rows), "g": ctypes.POINTER(Pages), "f": ctypes.c_float, "i": ctypes.c_int, "l": ctypes.c_int64, "p": ctypes.c_void_p, "z": ctypes.c_size_t,
        "s": ctypes.c_char_p}
 
 
@@ -636,6 +653,10 @@ def kv4_read(cache: KV4Cache, slots: torch.Tensor, dtype: torch.dtype = torch.bf
              k: torch.Tensor | None = None, v: torch.Tensor | None = None, stream=None):
     """The rows that the cache holds in slots (tokens,) int64, as (k, v) of (tokens, kv_heads,
     head_dim); zeros for slots that are not in the cache."""
+    return _read("cf_kv4_read", lib.cf_kv4_read, cache, slots, dtype, k, v, stream)
+
+
+def _read(fn, call, cache, slots, dtype, k, v, stream):
     tokens = slots.numel()
     want = (tokens, cache.data.shape[1], cache.head_dim)
     k = _new(cache.data, want, stream, dtype) if k is None else k
@@ -644,19 +665,23 @@ def kv4_read(cache: KV4Cache, slots: torch.Tensor, dtype: torch.dtype = torch.bf
     _shaped("k", k, k.dtype, want)
     _shaped("v", v, k.dtype, want)
     ps = _flat("slots", slots, dev, torch.int64, (tokens,))
-    rc = lib.cf_kv4_read(dt, *cache._args(dev), ps, tokens, _rows("k", k, dev), _rows("v", v, dev), _on(stream, dev))
+    rc = call(dt, *cache._args(dev), ps, tokens, _rows("k", k, dev), _rows("v", v, dev), _on(stream, dev))
     if rc:
-        raise CFError("cf_kv4_read", rc)
+        raise CFError(fn, rc)
     return k, v
 
 
-def kv4_attention_workspace_bytes(dtype: torch.dtype, max_q: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
+def _workspace_bytes(fn: str, dtype: torch.dtype, *sizes: int) -> int:
     dt = CF_BF16 if dtype == torch.bfloat16 else CF_F32 if dtype == torch.float32 else -1
-    _fit("cf_kv4_attention_workspace_bytes", -2, "qiii", max_q, q_heads, kv_heads, head_dim)
-    nb = lib.cf_kv4_attention_workspace_bytes(dt, max_q, q_heads, kv_heads, head_dim)
+    _fit(fn, -2, "qiii", *sizes)
+    nb = getattr(lib, fn)(dt, *sizes)
     if nb == 0:
-        raise CFError("cf_kv4_attention_workspace_bytes", -2)
+        raise CFError(fn, -2)
     return nb
+
+
+def kv4_attention_workspace_bytes(dtype: torch.dtype, max_q: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
+    return _workspace_bytes("cf_kv4_attention_workspace_bytes", dtype, max_q, q_heads, kv_heads, head_dim)
 
 
 def kv4_attention(q: torch.Tensor, cache: KV4Cache, kv_lens: torch.Tensor, table: torch.Tensor | None = None,
@@ -669,6 +694,12 @@ def kv4_attention(q: torch.Tensor, cache: KV4Cache, kv_lens: torch.Tensor, table
     total_q / batch queries.  lse (total_q, q_heads) fp32 is written where it is given.  Rows
     that belong to no sequence stay as they are.  max_q: the most queries of a sequence, if
     known (a bound above total_q is as good as total_q); scale: head_dim ** -0.5 if None."""
+    return _paged_attention("cf_kv4_attention", lib.cf_kv4_attention, lib.cf_kv4_attention_workspace_bytes, q, cache, kv_lens, table,
+                            q_starts, max_q, causal, window, scale, table_width, out, lse, workspace, stream)
+
+
+def _paged_attention(fn, call, workspace_bytes, q, cache, kv_lens, table, q_starts, max_q, causal, window, scale, table_width, out,
+                     lse, workspace, stream):
     if q.dim() != 3:
         raise ValueError("q must be (total_q, q_heads, head_dim)")
     total, heads, dim = q.shape
@@ -684,7 +715,7 @@ def kv4_attention(q: torch.Tensor, cache: KV4Cache, kv_lens: torch.Tensor, table
     if table is not None:
         table_width = table.shape[-1]
         pt = _flat("table", table, dev, torch.int32, (batch, table_width))
-    _fit("cf_kv4_attention", -2, "qiiiii", max_q, window, batch, table_width, heads, kv_heads)
+    _fit(fn, -2, "qiiiii", max_q, window, batch, table_width, heads, kv_heads)
     pq = _flat("q_starts", q_starts, dev, torch.int32, (batch + 1,))
     pe = _flat("lse", lse, dev, _F32, (total, heads))
     pl = _flat("kv_lens", kv_lens, dev, torch.int32, (batch,))
@@ -692,20 +723,252 @@ def kv4_attention(q: torch.Tensor, cache: KV4Cache, kv_lens: torch.Tensor, table
         out = _like(q, stream)
     else:
         _shaped("out", out, q.dtype, q.shape)
-    if workspace is None:
-        most = max_q or (total if q_starts is not None else total // max(batch, 1))
-        need = lib.cf_kv4_attention_workspace_bytes(dt, most, heads, kv_heads, dim)
-        if need and total:
-            # freed when this call returns, possibly before the launch stream has used it
-            workspace = _new(q, need, stream, _U8)
-    pw, nw = None, 0
-    if workspace is not None:
-        nw = workspace.numel() * workspace.element_size()
-        pw = _flat("workspace", workspace, dev, workspace.dtype, workspace.shape)
-    rc = lib.cf_kv4_attention(
+    workspace, pw, nw = _workspace(workspace_bytes, dt, q, max_q or (total if q_starts is not None else total // max(batch, 1)), heads, kv_heads,
+                        workspace, dev, stream)
+    rc = call(
         dt, _rows("q", q, dev), total, heads, *cache._args(dev), batch, pt, table_width, pl, pq, max_q,
         CF_ATTN_CAUSAL if causal else 0, window, dim ** -0.5 if scale is None else scale, _rows("out", out, dev), pe,
         pw, nw, _on(stream, dev))
     if rc:
-        raise CFError("cf_kv4_attention", rc)
+        raise CFError(fn, rc)
     return out
+
+
+@dataclass
+class KV8Cache:
+    """A paged K/V cache of 8-bit codes with a scale for each 16 tokens and head: ``data`` is (pages, kv_heads, 2 * page_size *
+    head_dim + max(16, page_size / 8)) uint8.  A copy of ``data`` is a checkpoint of it."""
+    data: torch.Tensor
+    page_size: int
+    head_dim: int
+
+    @staticmethod
+    def create(pages: int, page_size: int, kv_heads: int, head_dim: int, device=None) -> "KV8Cache":
+        _fit("cf_kv8_cache_bytes", -2, "qiii", pages, page_size, kv_heads, head_dim)
+        nb = lib.cf_kv8_cache_bytes(pages, page_size, kv_heads, head_dim)
+        if nb < 0:
+            raise CFError("cf_kv8_cache_bytes", nb)
+        return KV8Cache(torch.zeros((pages, kv_heads, nb // pages // kv_heads), dtype=torch.uint8,
+                                    device=device or require_device()), page_size, head_dim)
+
+    def _args(self, dev: int):
+        d = self.data
+        if d.dim() != 3 or d.shape[2] != 2 * self.page_size * self.head_dim + max(16, self.page_size // 8):
+            raise ValueError(f"cache data is {tuple(d.shape)}: want (pages, kv_heads, 2 * page_size * head_dim + max(16, page_size / 8))")
+        _fit("KV8Cache", -2, "iii", self.page_size, d.shape[1], self.head_dim)
+        return _flat("cache", d, dev, _U8, d.shape), d.shape[0], self.page_size, d.shape[1], self.head_dim
+
+
+def kv8_append(cache: KV8Cache, k: torch.Tensor, v: torch.Tensor, kv_lens: torch.Tensor, table: torch.Tensor | None = None,
+               starts: torch.Tensor | None = None, table_width: int = 0, stream=None):
+    """Quantize rows k, v (tokens, kv_heads, head_dim), the last tokens of sequences, into the cache.  kv_lens (batch,) are the
+    sequences' tokens with them, starts (batch + 1,) where each one's rows begin, table (batch, pages) their pages, all
+    int32; without a table sequence b has pages b * table_width and on, without starts every sequence gets
+    tokens / batch."""
+    tokens = k.shape[0] if k.dim() == 3 else -1
+    want = (tokens, cache.data.shape[1], cache.head_dim)
+    dt, dev, batch = _act_dtype(k), _device(k), kv_lens.numel()
+    _shaped("k", k, k.dtype, want)
+    _shaped("v", v, k.dtype, want)
+    pt = None
+    if table is not None:
+        table_width = table.shape[-1]
+        pt = _flat("table", table, dev, torch.int32, (batch, table_width))
+    _fit("cf_kv8_append", -2, "ii", batch, table_width)
+    ps = _flat("starts", starts, dev, torch.int32, (batch + 1,))
+    pl = _flat("kv_lens", kv_lens, dev, torch.int32, (batch,))
+    rc = lib.cf_kv8_append(dt, _rows("k", k, dev), _rows("v", v, dev), tokens, *cache._args(dev), batch, pt, table_width, pl, ps,
+                           _on(stream, dev))
+    if rc:
+        raise CFError("cf_kv8_append", rc)
+
+
+def kv8_read(cache: KV8Cache, slots: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
+             k: torch.Tensor | None = None, v: torch.Tensor | None = None, stream=None):
+    """The rows that the cache holds in slots (tokens,) int64 (page * page_size + place), as (k, v) of (tokens, kv_heads,
+    head_dim); zeros for slots that are not in the cache."""
+    return _read("cf_kv8_read", lib.cf_kv8_read, cache, slots, dtype, k, v, stream)
+
+
+def kv8_attention_workspace_bytes(dtype: torch.dtype, max_q: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
+    return _workspace_bytes("cf_kv8_attention_workspace_bytes", dtype, max_q, q_heads, kv_heads, head_dim)
+
+
+def kv8_attention(q: torch.Tensor, cache: KV8Cache, kv_lens: torch.Tensor, table: torch.Tensor | None = None,
+                  q_starts: torch.Tensor | None = None, max_q: int = 0, causal: bool = False, window: int = 0,
+                  scale: float | None = None, table_width: int = 0, out: torch.Tensor | None = None,
+                  lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """Attention of q (total_q, q_heads, head_dim) over an 8-bit cache; arguments and results as for kv4_attention."""
+    return _paged_attention("cf_kv8_attention", lib.cf_kv8_attention, lib.cf_kv8_attention_workspace_bytes, q, cache, kv_lens, table,
+                            q_starts, max_q, causal, window, scale, table_width, out, lse, workspace, stream)
+
+
+def attention_workspace_bytes(dtype: torch.dtype, max_q: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
+    return _workspace_bytes("cf_attention_workspace_bytes", dtype, max_q, q_heads, kv_heads, head_dim)
+
+
+def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_starts: torch.Tensor | None = None,
+              k_starts: torch.Tensor | None = None, batch: int = 1, max_q: int = 0, causal: bool = False, window: int = 0,
+              scale: float | None = None, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+              workspace: torch.Tensor | None = None, stream=None):
+    """Attention of q (total_q, q_heads, head_dim) over k and v (total_k, kv_heads, head_dim), packed sequences of which
+    sequence b has rows q_starts[b] .. q_starts[b + 1] - 1 of q and likewise k_starts of k and v (batch + 1 int32 each);
+    without starts each of `batch` sequences has as many.  Returns out; lse (total_q, q_heads) fp32 is written where it is given.
+    Slices of a packed projection and head-major views are taken as they are.  Rows that belong to no sequence stay as they are.
+    max_q: the most queries of a sequence, if known (a bound above total_q is as good as total_q); scale: head_dim ** -0.5
+    if None."""
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q must be (total_q, q_heads, head_dim), k and v (total_k, kv_heads, head_dim)")
+    total, heads, dim = q.shape
+    keys, kv_heads = k.shape[:2]
+    dt, dev = _act_dtype(q), _device(q)
+    _shaped("k", k, q.dtype, (keys, kv_heads, dim))
+    _shaped("v", v, q.dtype, (keys, kv_heads, dim))
+    if q_starts is not None:
+        batch = q_starts.numel() - 1
+    elif k_starts is not None:
+        batch = k_starts.numel() - 1
+    if max_q > total:
+        max_q = total
+    _fit("cf_attention", -2, "qiiiii", max_q, window, batch, heads, kv_heads, dim)
+    pq = _flat("q_starts", q_starts, dev, torch.int32, (batch + 1,))
+    pk = _flat("k_starts", k_starts, dev, torch.int32, (batch + 1,))
+    pe = _flat("lse", lse, dev, _F32, (total, heads))
+    if out is None:
+        out = _like(q, stream)
+    else:
+        _shaped("out", out, q.dtype, q.shape)
+    workspace, pw, nw = _workspace(lib.cf_attention_workspace_bytes, dt, q, max_q or (total if q_starts is not None else total // max(batch, 1)), heads,
+                        kv_heads, workspace, dev, stream)
+    rc = lib.cf_attention(
+        dt, _rows("q", q, dev), total, heads, _rows("k", k, dev), _rows("v", v, dev), keys, kv_heads, dim, batch, pq, pk, max_q,
+        CF_ATTN_CAUSAL if causal else 0, window, dim ** -0.5 if scale is None else scale, _rows("out", out, dev), pe, pw, nw,
+        _on(stream, dev))
+    if rc:
+        raise CFError("cf_attention", rc)
+    return out
+
+
+def _workspace(workspace_bytes, dt, q, most, heads, kv_heads, workspace, dev, stream):
+    """An attention call's workspace, the caller's or one to be held until the call has returned: (tensor, address, bytes)."""
+    if workspace is None:
+        need = workspace_bytes(dt, most, heads, kv_heads, q.shape[2])
+        if not need or not q.shape[0]:
+            return None, None, 0
+        # freed when the call returns, possibly before the launch stream has used it
+        workspace = _new(q, need, stream, _U8)
+    return workspace, _flat("workspace", workspace, dev, workspace.dtype, workspace.shape), workspace.numel() * workspace.element_size()
+
+
+@dataclass
+class PageTable:
+    """Who holds which page of a cache: refs (pages,) how many entries hold each, table (rows, width) the pages of each
+    sequence, lens (rows,) its tokens, all int32.  The same table serves every cache whose pages it numbers (each layer's)."""
+    refs: torch.Tensor
+    table: torch.Tensor
+    lens: torch.Tensor
+    page_size: int
+
+    @staticmethod
+    def create(pages: int, rows: int, width: int, page_size: int, device=None) -> "PageTable":
+        """All pages free, all sequences empty."""
+        dev = device or require_device()
+        return PageTable(torch.zeros(pages, dtype=torch.int32, device=dev),
+                         torch.full((rows, width), -1, dtype=torch.int32, device=dev),
+                         torch.zeros(rows, dtype=torch.int32, device=dev), page_size)
+
+    def _pages(self, name: str, dev: int, shape: tuple) -> Pages:
+        pages, rows, width = shape
+        i32 = torch.int32
+        return Pages(_flat(name + ".refs", self.refs, dev, i32, (pages,)), _flat(name + ".table", self.table, dev, i32, (rows, width)),
+                     _flat(name + ".lens", self.lens, dev, i32, (rows,)))
+
+    def _like(self, stream) -> "PageTable":
+        return PageTable(_like(self.refs, stream), _like(self.table, stream), _like(self.lens, stream), self.page_size)
+
+
+def _pages_call(fn: str, have: PageTable, out: PageTable | None, workspace, stream):
+    """Of an operation on pages: the sequences in and out, out, sizes, the workspace's address and bytes, the device, and
+    the workspace, to be held until the call has returned."""
+    if have.table.dim() != 2 or have.refs.dim() != 1:
+        raise ValueError("table must be (rows, width), refs (pages,)")
+    dev = _device(have.table)
+    rows, width = have.table.shape
+    shape = (have.refs.numel(), rows, width)
+    _fit(fn, -2, "qiii", *shape, have.page_size)
+    out = have._like(stream) if out is None else out
+    if out.page_size != have.page_size:
+        raise ValueError(f"pages of {have.page_size} tokens in, of {out.page_size} out")
+    need = lib.cf_pages_workspace_bytes(shape[0], rows)
+    if workspace is None:
+        workspace = _new(have.table, max(need, 4) // 4, stream)
+    ws = (_flat("workspace", workspace, dev, workspace.dtype, workspace.shape), workspace.numel() * workspace.element_size())
+    return have._pages("have", dev, shape), out._pages("out", dev, shape), out, shape, ws, dev, workspace
+
+
+def _words(like: torch.Tensor, n: int, t: torch.Tensor | None, name: str, dev: int, stream):
+    """(a buffer of n int32, its address)."""
+    t = _new(like, n, stream) if t is None else t
+    return t, _flat(name, t, dev, torch.int32, (n,))
+
+
+def pages_resize(have: PageTable, want: torch.Tensor, out: PageTable | None = None, missing: torch.Tensor | None = None,
+                 workspace: torch.Tensor | None = None, stream=None):
+    """Sequences of want (rows,) int32 tokens each (negative: as it is): those that shrink let go pages, then those that
+    grow take the first free ones.  Returns (out, missing): missing (1,) int32 says how many rows found too few and stay as they
+    are.  out may be `have`."""
+    pin, pout, out, shape, ws, dev, workspace = _pages_call("cf_pages_resize", have, out, workspace, stream)
+    missing, pm = _words(have.table, 1, missing, "missing", dev, stream)
+    rc = lib.cf_pages_resize(pin, pout, *shape, have.page_size, _flat("want", want, dev, torch.int32, (shape[1],)), pm, *ws, _on(stream, dev))
+    if rc:
+        raise CFError("cf_pages_resize", rc)
+    return out, missing
+
+
+def pages_fork(have: PageTable, parents: torch.Tensor, out: PageTable | None = None, src: torch.Tensor | None = None,
+               dst: torch.Tensor | None = None, missing: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+               stream=None):
+    """Row r becomes a copy of row parents[r] (rows,) int32 (itself: it stays; outside the rows: empty).  Whole pages are
+    shared.  Returns (out, src, dst, missing): pages src[r] have to be copied to dst[r], with pages_copy in every cache, before
+    anything is appended; missing (1,) says how many rows found no page for that and end before it."""
+    pin, pout, out, shape, ws, dev, workspace = _pages_call("cf_pages_fork", have, out, workspace, stream)
+    src, p1 = _words(have.table, shape[1], src, "src", dev, stream)
+    dst, p2 = _words(have.table, shape[1], dst, "dst", dev, stream)
+    missing, pm = _words(have.table, 1, missing, "missing", dev, stream)
+    rc = lib.cf_pages_fork(pin, pout, *shape, have.page_size, _flat("parents", parents, dev, torch.int32, (shape[1],)), p1, p2, pm,
+                           *ws, _on(stream, dev))
+    if rc:
+        raise CFError("cf_pages_fork", rc)
+    return out, src, dst, missing
+
+
+def pages_compact(have: PageTable, out: PageTable | None = None, src: torch.Tensor | None = None, dst: torch.Tensor | None = None,
+                  count: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """The pages that are held become the first ones.  Returns (out, src, dst, count): the first count (1,) of src and dst
+    (pages / 2 each) are the pages to copy, with pages_copy in every cache.  out may be `have`."""
+    pin, pout, out, shape, ws, dev, workspace = _pages_call("cf_pages_compact", have, out, workspace, stream)
+    src, p1 = _words(have.table, shape[0] // 2, src, "src", dev, stream)
+    dst, p2 = _words(have.table, shape[0] // 2, dst, "dst", dev, stream)
+    count, pm = _words(have.table, 1, count, "count", dev, stream)
+    rc = lib.cf_pages_compact(pin, pout, *shape, p1, p2, pm, *ws, _on(stream, dev))
+    if rc:
+        raise CFError("cf_pages_compact", rc)
+    return out, src, dst, count
+
+
+def pages_copy(data: torch.Tensor, src: torch.Tensor, dst: torch.Tensor, count: torch.Tensor | None = None, stream=None):
+    """Copies page src[i] to page dst[i] (int32) of data, (layers, pages, bytes) uint8 of one or
+    several caches that are numbered alike; with count (1,) int32 the first of them.  Pairs with a -1 copy nothing."""
+    if data.dtype != _U8 or data.dim() != 3:
+        raise TypeError("data must be (layers, pages, bytes) uint8; of one cache: cache.data.flatten(1)[None]")
+    dev = _device(data)
+    layers, pages, size = data.shape
+    n = src.numel()
+    _fit("cf_pages_copy", -2, "i", layers)
+    _here("data", data, dev)
+    if data.stride(2) != 1 or data.stride(1) != size:
+        raise ValueError("a layer's pages must lie behind each other")
+    rc = lib.cf_pages_copy(data.data_ptr(), pages, size, layers, data.stride(0), _flat("src", src, dev, torch.int32, (n,)),
+                           _flat("dst", dst, dev, torch.int32, (n,)), n, _flat("count", count, dev, torch.int32, (1,)), _on(stream, dev))
+    if rc:
+        raise CFError("cf_pages_copy", rc)

@@ -150,6 +150,10 @@ constexpr wide kMaxExtent = wide(1) << 46;  // bytes: beyond any device's memory
 constexpr int kMaxSequences = 1 << 24;
 // Query tokens times query heads of one: a tile of up to 128 rows behind the last still counts in 32 bits.
 constexpr int64_t kMaxAttnRows = (int64_t(1) << 31) - 256;
+// Tokens that cf_kv8_append takes at once: a wave for each in a dispatch of 2^32 - 1 work-items, and head by head.
+constexpr int64_t kMaxAppend = int64_t(1) << 27;
+// Bytes between the keys of cf_attention: 63 of them in 32 bits.
+constexpr int64_t kMaxKeyStride = int64_t(1) << 26;
 
 // NULL, strides, alignment of one operand's rows, in this order.
 int check_rows(const cf_rows* r, int64_t tokens, int64_t heads, int64_t dim, int64_t esz, bool written, RowsOf* x) {
@@ -202,11 +206,15 @@ cf::KvCache kv4_cache(const uint8_t* cache, int64_t pages, int page_size, int kv
     return {const_cast<uint8_t*>(cache), pages, kv_heads, {page_size, head_dim}, __builtin_ctz(page_size)};
 }
 
-// cf_kv4_append, and cf_kv4_read, whose rows are written.
-int kv4_rows(bool read, int a_dtype, const cf_rows* k, const cf_rows* v, const int64_t* slots, int64_t tokens,
-             const uint8_t* cache, int64_t pages, int page_size, int kv_heads, int head_dim, void* stream) {
+cf::Kv8Cache kv8_cache(const uint8_t* cache, int64_t pages, int page_size, int kv_heads, int head_dim) {
+    return {const_cast<uint8_t*>(cache), pages, kv_heads, {page_size, head_dim}, __builtin_ctz(page_size)};
+}
+
+// cf_kv4_append, and the readers, whose rows are written: f is the launch for a checked call.
+template <typename F>
+int slot_rows(bool read, int a_dtype, const cf_rows* k, const cf_rows* v, const int64_t* slots, int64_t tokens,
+              const uint8_t* cache, int64_t bytes, int kv_heads, int head_dim, F f) {
     if (a_dtype != CF_BF16 && a_dtype != CF_F32) return CF_E_ARG;
-    const int64_t bytes = cf_kv4_cache_bytes(pages, page_size, kv_heads, head_dim);
     if (bytes < 0) return CF_E_SHAPE;
     if (tokens < 0 || tokens > kMaxNumel / head_dim / kv_heads) return CF_E_SHAPE;
     if (tokens == 0) return CF_OK;
@@ -220,11 +228,94 @@ int kv4_rows(bool read, int a_dtype, const cf_rows* k, const cf_rows* v, const i
         return CF_E_ALIAS;
     if (overlap(x[0].range(), rc) || overlap(x[1].range(), rc)) return CF_E_ALIAS;
     if (int e = check_device()) return e;
-    const auto f = read ? cf::launch_kv4_read : cf::launch_kv4_append;
-    return f(a_dtype, x[0].r, x[1].r, slots, tokens, kv4_cache(cache, pages, page_size, kv_heads, head_dim),
-             static_cast<hipStream_t>(stream)) == hipSuccess
-               ? CF_OK
-               : CF_E_HIP;
+    return f(x[0].r, x[1].r) == hipSuccess ? CF_OK : CF_E_HIP;
+}
+
+// Attention over a paged cache, of `cache_bytes` bytes; f is the launch for a checked call.
+template <typename F>
+int paged_attention(int a_dtype, const cf_rows* q, int64_t total_q, int q_heads, const uint8_t* cache, int64_t cache_bytes,
+                    int64_t pages, int page_size, int kv_heads, int head_dim, int batch, const int32_t* table,
+                    int table_width, const int32_t* kv_lens, const int32_t* q_starts, int64_t max_q, int flags,
+                    int window, float scale, const cf_rows* out, float* lse, void* workspace, size_t ws_bytes,
+                    size_t (*workspace_bytes)(int, int64_t, int, int, int), F f) {
+    if (a_dtype != CF_BF16 && a_dtype != CF_F32) return CF_E_ARG;
+    if ((flags & ~CF_ATTN_CAUSAL) || window < 0 || (window && !(flags & CF_ATTN_CAUSAL))) return CF_E_ARG;
+    if (!(scale > 0.f) || scale > 1e38f) return CF_E_ARG;
+    if (cache_bytes < 0) return CF_E_SHAPE;
+    if (q_heads < 1 || q_heads > 65535 || q_heads % kv_heads || total_q < 0 || total_q > kMaxAttnRows / q_heads ||
+        max_q < 0)
+        return CF_E_SHAPE;
+    if (total_q == 0) return CF_OK;
+    if (max_q > total_q) return CF_E_SHAPE;
+    if (batch < 1 || batch > kMaxSequences || table_width < 1 || int64_t(table_width) * page_size > INT32_MAX - 256 ||
+        (!table && int64_t(batch) * table_width > pages) || (!q_starts && total_q % batch))
+        return CF_E_SHAPE;
+    if (!cache || !kv_lens || !workspace) return CF_E_NULL;
+    const int64_t esz = elem_bytes(a_dtype);
+    RowsOf x[2];
+    if (int rc = check_rows(q, total_q, q_heads, head_dim, esz, false, &x[0])) return rc;
+    if (int rc = check_rows(out, total_q, q_heads, head_dim, esz, true, &x[1])) return rc;
+    if (!aligned16(cache) || !aligned4(table) || !aligned4(kv_lens) || !aligned4(q_starts) || !aligned4(lse) ||
+        (reinterpret_cast<uintptr_t>(workspace) & 255u))
+        return CF_E_ALIGN;
+    if (max_q == 0) max_q = q_starts ? total_q : total_q / batch;
+    const size_t need = workspace_bytes(a_dtype, max_q, q_heads, kv_heads, head_dim);
+    if (ws_bytes < need) return CF_E_WORKSPACE;
+    if (!apart(x[0], x[1])) return CF_E_ALIAS;
+    const Range r[8] = {x[0].range(),
+                        range_of(cache, cache_bytes),
+                        range_of(table, table ? int64_t(batch) * table_width * 4 : 0),
+                        range_of(kv_lens, int64_t(batch) * 4),
+                        range_of(q_starts, q_starts ? (int64_t(batch) + 1) * 4 : 0),
+                        x[1].range(),
+                        range_of(lse, lse ? total_q * q_heads * 4 : 0),
+                        range_of(workspace, static_cast<int64_t>(need))};
+    for (int i = 5; i < 8; ++i)
+        for (int j = i == 5 ? 1 : 0; j < i; ++j)  // q and out were looked at row by row
+            if (r[i].hi > r[i].lo && r[j].hi > r[j].lo && overlap(r[i], r[j])) return CF_E_ALIAS;
+    if (int rc = check_device()) return rc;
+    return f(x[0].r, x[1].r, max_q) == hipSuccess ? CF_OK : CF_E_HIP;
+}
+
+// Heads and rows that an attention call's workspace is asked for.
+bool attention_dims(int a_dtype, int64_t max_q, int q_heads, int kv_heads, int head_dim) {
+    return (a_dtype == CF_BF16 || a_dtype == CF_F32) && kv4_dims(16, kv_heads, head_dim) && q_heads >= 1 &&
+           q_heads <= 65535 && q_heads % kv_heads == 0 && max_q >= 1 && max_q <= kMaxAttnRows / q_heads;
+}
+
+// ---- pages
+
+constexpr int kMaxPageRows = 1 << 20;
+
+// The three arrays of a call's sequences, in and out, and up to four others of its own: reads, then writes.
+int check_pages(const cf_pages* in, const cf_pages* out, int64_t pages, int rows, int width, int page_size, bool in_place,
+                const void* want, const int32_t* const (&written)[3], const int64_t (&places)[3], const void* workspace,
+                size_t ws_bytes) {
+    if (pages < 1 || pages > INT32_MAX || rows < 1 || rows > kMaxPageRows || width < 1 || int64_t(rows) * width > (1 << 30) ||
+        page_size < 1 || int64_t(width) * page_size > INT32_MAX - 256)
+        return CF_E_SHAPE;
+    if (!in || !out || !in->refs || !in->table || !in->lens || !out->refs || !out->table || !out->lens || !workspace)
+        return CF_E_NULL;
+    for (int i = 0; i < 3; ++i)
+        if (!written[i] && places[i] > 0) return CF_E_NULL;
+    const int64_t entries = int64_t(rows) * width;
+    const size_t need = cf_pages_workspace_bytes(pages, rows);
+    const Range r[11] = {range_of(in->refs, pages * 4),   range_of(in->table, entries * 4),
+                         range_of(in->lens, int64_t(rows) * 4), range_of(want, want ? int64_t(rows) * 4 : 0),
+                         range_of(out->refs, pages * 4),  range_of(out->table, entries * 4),
+                         range_of(out->lens, int64_t(rows) * 4), range_of(written[0], places[0] * 4),
+                         range_of(written[1], places[1] * 4), range_of(written[2], places[2] * 4),
+                         range_of(workspace, static_cast<int64_t>(need))};
+    for (const Range& x : r)
+        if (x.lo & 3u) return CF_E_ALIGN;
+    if (ws_bytes < need) return CF_E_WORKSPACE;
+    for (int i = 4; i < 11; ++i)
+        for (int j = 0; j < i; ++j) {
+            if (r[i].hi <= r[i].lo || r[j].hi <= r[j].lo || !overlap(r[i], r[j])) continue;
+            if (j == i - 4 && i < 7 && r[i].lo == r[j].lo && (in_place || i == 4)) continue;
+            return CF_E_ALIAS;
+        }
+    return CF_OK;
 }
 
 }  // namespace
@@ -509,19 +600,28 @@ int64_t cf_kv4_cache_bytes(int64_t pages, int page_size, int kv_heads, int head_
 
 int cf_kv4_append(int a_dtype, const cf_rows* k, const cf_rows* v, const int64_t* slots, int64_t tokens,
                   uint8_t* cache, int64_t pages, int page_size, int kv_heads, int head_dim, void* stream) {
-    return kv4_rows(false, a_dtype, k, v, slots, tokens, cache, pages, page_size, kv_heads, head_dim, stream);
+    return slot_rows(false, a_dtype, k, v, slots, tokens, cache, cf_kv4_cache_bytes(pages, page_size, kv_heads, head_dim),
+                     kv_heads, head_dim, [&](const cf_rows& kr, const cf_rows& vr) {
+                         return cf::launch_kv4_append(a_dtype, kr, vr, slots, tokens,
+                                                      kv4_cache(cache, pages, page_size, kv_heads, head_dim),
+                                                      static_cast<hipStream_t>(stream));
+                     });
 }
 
 int cf_kv4_read(int a_dtype, const uint8_t* cache, int64_t pages, int page_size, int kv_heads, int head_dim,
                 const int64_t* slots, int64_t tokens, const cf_rows* k, const cf_rows* v, void* stream) {
-    return kv4_rows(true, a_dtype, k, v, slots, tokens, cache, pages, page_size, kv_heads, head_dim, stream);
+    return slot_rows(true, a_dtype, k, v, slots, tokens, cache, cf_kv4_cache_bytes(pages, page_size, kv_heads, head_dim),
+                     kv_heads, head_dim, [&](const cf_rows& kr, const cf_rows& vr) {
+                         return cf::launch_kv4_read(a_dtype, kr, vr, slots, tokens,
+                                                    kv4_cache(cache, pages, page_size, kv_heads, head_dim),
+                                                    static_cast<hipStream_t>(stream));
+                     });
 }
 
 size_t cf_kv4_attention_workspace_bytes(int a_dtype, int64_t max_q, int q_heads, int kv_heads, int head_dim) {
-    if ((a_dtype != CF_BF16 && a_dtype != CF_F32) || !kv4_dims(16, kv_heads, head_dim) || q_heads < 1 ||
-        q_heads > 65535 || q_heads % kv_heads || max_q < 1 || max_q > kMaxAttnRows / q_heads)
-        return 0;
-    return cf::kv4_attention_workspace(a_dtype, head_dim, max_q * (q_heads / kv_heads));
+    return attention_dims(a_dtype, max_q, q_heads, kv_heads, head_dim)
+               ? cf::kv4_attention_workspace(a_dtype, head_dim, max_q * (q_heads / kv_heads))
+               : 0;
 }
 
 int cf_kv4_attention(int a_dtype, const cf_rows* q, int64_t total_q, int q_heads, const uint8_t* cache,
@@ -529,59 +629,187 @@ int cf_kv4_attention(int a_dtype, const cf_rows* q, int64_t total_q, int q_heads
                      int table_width, const int32_t* kv_lens, const int32_t* q_starts, int64_t max_q, int flags,
                      int window, float scale, const cf_rows* out, float* lse, void* workspace, size_t ws_bytes,
                      void* stream) {
+    return paged_attention(a_dtype, q, total_q, q_heads, cache, cf_kv4_cache_bytes(pages, page_size, kv_heads, head_dim), pages,
+                           page_size, kv_heads, head_dim, batch, table, table_width, kv_lens, q_starts, max_q, flags,
+                           window, scale, out, lse, workspace, ws_bytes, cf_kv4_attention_workspace_bytes,
+                           [&](const cf_rows& qr, const cf_rows& outr, int64_t most) {
+                               const cf::Kv4Attention call{qr,     outr,  kv4_cache(cache, pages, page_size, kv_heads, head_dim),
+                                                           table,  kv_lens, q_starts, lse, total_q, most, batch, table_width, q_heads,
+                                                           flags & CF_ATTN_CAUSAL, window, scale};
+                               return cf::launch_kv4_attention(a_dtype, call, workspace, static_cast<hipStream_t>(stream));
+                           });
+}
+
+int64_t cf_kv8_cache_bytes(int64_t pages, int page_size, int kv_heads, int head_dim) {
+    if (!kv4_dims(page_size, kv_heads, head_dim) || pages < 1 || pages > INT32_MAX) return CF_E_SHAPE;
+    const wide bytes = wide(pages) * kv_heads * cf::Kv8Block{page_size, head_dim}.bytes();
+    return bytes <= kMaxExtent ? static_cast<int64_t>(bytes) : CF_E_SHAPE;
+}
+
+int cf_kv8_append(int a_dtype, const cf_rows* k, const cf_rows* v, int64_t tokens, uint8_t* cache, int64_t pages,
+                  int page_size, int kv_heads, int head_dim, int batch, const int32_t* table, int table_width,
+                  const int32_t* kv_lens, const int32_t* starts, void* stream) {
+    if (a_dtype != CF_BF16 && a_dtype != CF_F32) return CF_E_ARG;
+    const int64_t bytes = cf_kv8_cache_bytes(pages, page_size, kv_heads, head_dim);
+    if (bytes < 0) return CF_E_SHAPE;
+    if (tokens < 0 || tokens > kMaxAppend || tokens > kMaxNumel / head_dim / kv_heads) return CF_E_SHAPE;
+    if (tokens == 0) return CF_OK;
+    if (batch < 1 || batch > kMaxSequences || table_width < 1 || int64_t(table_width) * page_size > INT32_MAX - 256 ||
+        (!table && int64_t(batch) * table_width > pages) || (!starts && tokens % batch))
+        return CF_E_SHAPE;
+    if (!cache || !kv_lens) return CF_E_NULL;
+    RowsOf x[2];
+    if (int rc = check_rows(k, tokens, kv_heads, head_dim, elem_bytes(a_dtype), false, &x[0])) return rc;
+    if (int rc = check_rows(v, tokens, kv_heads, head_dim, elem_bytes(a_dtype), false, &x[1])) return rc;
+    if (!aligned16(cache) || !aligned4(table) || !aligned4(kv_lens) || !aligned4(starts)) return CF_E_ALIGN;
+    const Range rc = range_of(cache, bytes);
+    const Range read[5] = {x[0].range(), x[1].range(), range_of(table, table ? int64_t(batch) * table_width * 4 : 0),
+                           range_of(kv_lens, int64_t(batch) * 4), range_of(starts, starts ? (int64_t(batch) + 1) * 4 : 0)};
+    for (const Range& r : read)
+        if (r.hi > r.lo && overlap(r, rc)) return CF_E_ALIAS;
+    if (int e = check_device()) return e;
+    return cf::launch_kv8_append(a_dtype, x[0].r, x[1].r, tokens, kv8_cache(cache, pages, page_size, kv_heads, head_dim), batch, table,
+                                 table_width, kv_lens, starts, static_cast<hipStream_t>(stream)) == hipSuccess
+               ? CF_OK
+               : CF_E_HIP;
+}
+
+int cf_kv8_read(int a_dtype, const uint8_t* cache, int64_t pages, int page_size, int kv_heads, int head_dim,
+                const int64_t* slots, int64_t tokens, const cf_rows* k, const cf_rows* v, void* stream) {
+    return slot_rows(true, a_dtype, k, v, slots, tokens, cache, cf_kv8_cache_bytes(pages, page_size, kv_heads, head_dim),
+                     kv_heads, head_dim, [&](const cf_rows& kr, const cf_rows& vr) {
+                         return cf::launch_kv8_read(a_dtype, kr, vr, slots, tokens,
+                                                    kv8_cache(cache, pages, page_size, kv_heads, head_dim),
+                                                    static_cast<hipStream_t>(stream));
+                     });
+}
+
+size_t cf_kv8_attention_workspace_bytes(int a_dtype, int64_t max_q, int q_heads, int kv_heads, int head_dim) {
+    return attention_dims(a_dtype, max_q, q_heads, kv_heads, head_dim)
+               ? cf::kv8_attention_workspace(a_dtype, head_dim, max_q * (q_heads / kv_heads))
+               : 0;
+}
+
+int cf_kv8_attention(int a_dtype, const cf_rows* q, int64_t total_q, int q_heads, const uint8_t* cache,
+                     int64_t pages, int page_size, int kv_heads, int head_dim, int batch, const int32_t* table,
+                     int table_width, const int32_t* kv_lens, const int32_t* q_starts, int64_t max_q, int flags,
+                     int window, float scale, const cf_rows* out, float* lse, void* workspace, size_t ws_bytes,
+                     void* stream) {
+    return paged_attention(a_dtype, q, total_q, q_heads, cache, cf_kv8_cache_bytes(pages, page_size, kv_heads, head_dim), pages,
+                           page_size, kv_heads, head_dim, batch, table, table_width, kv_lens, q_starts, max_q, flags,
+                           window, scale, out, lse, workspace, ws_bytes, cf_kv8_attention_workspace_bytes,
+                           [&](const cf_rows& qr, const cf_rows& outr, int64_t most) {
+                               const cf::Kv8Attention call{qr,     outr,  kv8_cache(cache, pages, page_size, kv_heads, head_dim),
+                                                           table,  kv_lens, q_starts, lse, total_q, most, batch, table_width, q_heads,
+                                                           flags & CF_ATTN_CAUSAL, window, scale};
+                               return cf::launch_kv8_attention(a_dtype, call, workspace, static_cast<hipStream_t>(stream));
+                           });
+}
+
+size_t cf_attention_workspace_bytes(int a_dtype, int64_t max_q, int q_heads, int kv_heads, int head_dim) {
+    return attention_dims(a_dtype, max_q, q_heads, kv_heads, head_dim)
+               ? cf::attention_workspace(a_dtype, head_dim, max_q * (q_heads / kv_heads))
+               : 0;
+}
+
+int cf_attention(int a_dtype, const cf_rows* q, int64_t total_q, int q_heads, const cf_rows* k, const cf_rows* v,
+                 int64_t total_k, int kv_heads, int head_dim, int batch, const int32_t* q_starts,
+                 const int32_t* k_starts, int64_t max_q, int flags, int window, float scale, const cf_rows* out,
+                 float* lse, void* workspace, size_t ws_bytes, void* stream) {
     if (a_dtype != CF_BF16 && a_dtype != CF_F32) return CF_E_ARG;
     if ((flags & ~CF_ATTN_CAUSAL) || window < 0 || (window && !(flags & CF_ATTN_CAUSAL))) return CF_E_ARG;
     if (!(scale > 0.f) || scale > 1e38f) return CF_E_ARG;
-    const int64_t cache_bytes = cf_kv4_cache_bytes(pages, page_size, kv_heads, head_dim);
-    if (cache_bytes < 0) return CF_E_SHAPE;
-    if (q_heads < 1 || q_heads > 65535 || q_heads % kv_heads || total_q < 0 || total_q > kMaxAttnRows / q_heads ||
-        max_q < 0)
+    if (!kv4_dims(16, kv_heads, head_dim) || q_heads < 1 || q_heads > 65535 || q_heads % kv_heads || total_q < 0 ||
+        total_q > kMaxAttnRows / q_heads || max_q < 0 || total_k < 0 || total_k > kMaxAttnRows)
         return CF_E_SHAPE;
     if (total_q == 0) return CF_OK;
-    if (max_q > total_q) return CF_E_SHAPE;
-    if (batch < 1 || batch > kMaxSequences || table_width < 1 || int64_t(table_width) * page_size > INT32_MAX - 256 ||
-        (!table && int64_t(batch) * table_width > pages) || (!q_starts && total_q % batch))
+    if (max_q > total_q || batch < 1 || batch > kMaxSequences || (!q_starts && total_q % batch) || (!k_starts && total_k % batch))
         return CF_E_SHAPE;
-    if (!cache || !kv_lens || !workspace) return CF_E_NULL;
+    if (!workspace) return CF_E_NULL;
     const int64_t esz = elem_bytes(a_dtype);
-    RowsOf x[2];
+    RowsOf x[4];
     if (int rc = check_rows(q, total_q, q_heads, head_dim, esz, false, &x[0])) return rc;
-    if (int rc = check_rows(out, total_q, q_heads, head_dim, esz, true, &x[1])) return rc;
-    if (!aligned16(cache) || !aligned4(table) || !aligned4(kv_lens) || !aligned4(q_starts) || !aligned4(lse) ||
-        (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    if (int rc = check_rows(k, total_k, kv_heads, head_dim, esz, false, &x[1])) return rc;
+    if (int rc = check_rows(v, total_k, kv_heads, head_dim, esz, false, &x[2])) return rc;
+    if (int rc = check_rows(out, total_q, q_heads, head_dim, esz, true, &x[3])) return rc;
+    // rows of a tile are reached by 32-bit offsets
+    if (total_k && (x[1].r.token_stride > kMaxKeyStride / esz || x[2].r.token_stride > kMaxKeyStride / esz)) return CF_E_SHAPE;
+    if (!aligned4(q_starts) || !aligned4(k_starts) || !aligned4(lse) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
         return CF_E_ALIGN;
     if (max_q == 0) max_q = q_starts ? total_q : total_q / batch;
-    const size_t need = cf_kv4_attention_workspace_bytes(a_dtype, max_q, q_heads, kv_heads, head_dim);
+    const size_t need = cf_attention_workspace_bytes(a_dtype, max_q, q_heads, kv_heads, head_dim);
     if (ws_bytes < need) return CF_E_WORKSPACE;
-    if (!apart(x[0], x[1])) return CF_E_ALIAS;
+    for (int i = 0; i < 3; ++i)
+        if (!apart(x[i], x[3])) return CF_E_ALIAS;
     const Range r[8] = {x[0].range(),
-                        range_of(cache, cache_bytes),
-                        range_of(table, table ? int64_t(batch) * table_width * 4 : 0),
-                        range_of(kv_lens, int64_t(batch) * 4),
-                        range_of(q_starts, q_starts ? (int64_t(batch) + 1) * 4 : 0),
                         x[1].range(),
+                        x[2].range(),
+                        range_of(q_starts, q_starts ? (int64_t(batch) + 1) * 4 : 0),
+                        range_of(k_starts, k_starts ? (int64_t(batch) + 1) * 4 : 0),
+                        x[3].range(),
                         range_of(lse, lse ? total_q * q_heads * 4 : 0),
                         range_of(workspace, static_cast<int64_t>(need))};
     for (int i = 5; i < 8; ++i)
-        for (int j = i == 5 ? 1 : 0; j < i; ++j)  // q and out were looked at row by row
+        for (int j = i == 5 ? 3 : 0; j < i; ++j)  // rows and out were looked at row by row
             if (r[i].hi > r[i].lo && r[j].hi > r[j].lo && overlap(r[i], r[j])) return CF_E_ALIAS;
     if (int rc = check_device()) return rc;
-    const cf::Kv4Attention call{x[0].r,
-                                x[1].r,
-                                kv4_cache(cache, pages, page_size, kv_heads, head_dim),
-                                table,
-                                kv_lens,
-                                q_starts,
-                                lse,
-                                total_q,
-                                max_q,
-                                batch,
-                                table_width,
-                                q_heads,
-                                flags & CF_ATTN_CAUSAL,
-                                window,
-                                scale};
-    return cf::launch_kv4_attention(a_dtype, call, workspace, static_cast<hipStream_t>(stream)) == hipSuccess
+    const cf::RowsAttention call{x[0].r, x[1].r, x[2].r, x[3].r, q_starts, k_starts, lse, total_q, total_k, max_q, batch, q_heads, kv_heads,
+                                 head_dim, flags & CF_ATTN_CAUSAL, window, scale};
+    return cf::launch_attention(a_dtype, call, workspace, static_cast<hipStream_t>(stream)) == hipSuccess ? CF_OK : CF_E_HIP;
+}
+
+size_t cf_pages_workspace_bytes(int64_t pages, int rows) {
+    return pages < 1 || pages > INT32_MAX || rows < 1 || rows > kMaxPageRows ? 0 : cf::pages_workspace(pages, rows);
+}
+
+int cf_pages_resize(const cf_pages* in, const cf_pages* out, int64_t pages, int rows, int width, int page_size,
+                    const int32_t* want, int32_t* missing, void* workspace, size_t ws_bytes, void* stream) {
+    if (int rc = check_pages(in, out, pages, rows, width, page_size, true, want, {missing, nullptr, nullptr}, {1, 0, 0}, workspace, ws_bytes))
+        return rc;
+    if (!want) return CF_E_NULL;
+    if (int rc = check_device()) return rc;
+    const cf::PagesCall call{*in, *out, pages, rows, width, page_size, want, nullptr, nullptr, missing};
+    return cf::launch_pages_resize(call, workspace, static_cast<hipStream_t>(stream)) == hipSuccess ? CF_OK : CF_E_HIP;
+}
+
+int cf_pages_fork(const cf_pages* in, const cf_pages* out, int64_t pages, int rows, int width, int page_size,
+                  const int32_t* parents, int32_t* src, int32_t* dst, int32_t* missing, void* workspace, size_t ws_bytes,
+                  void* stream) {
+    if (int rc = check_pages(in, out, pages, rows, width, page_size, false, parents, {src, dst, missing}, {rows, rows, 1}, workspace, ws_bytes))
+        return rc;
+    if (!parents) return CF_E_NULL;
+    if (int rc = check_device()) return rc;
+    const cf::PagesCall call{*in, *out, pages, rows, width, page_size, parents, src, dst, missing};
+    return cf::launch_pages_fork(call, workspace, static_cast<hipStream_t>(stream)) == hipSuccess ? CF_OK : CF_E_HIP;
+}
+
+int cf_pages_compact(const cf_pages* in, const cf_pages* out, int64_t pages, int rows, int width, int32_t* src,
+                     int32_t* dst, int32_t* count, void* workspace, size_t ws_bytes, void* stream) {
+    if (int rc = check_pages(in, out, pages, rows, width, 1, true, nullptr, {src, dst, count}, {pages / 2, pages / 2, 1}, workspace, ws_bytes))
+        return rc;
+    if (int rc = check_device()) return rc;
+    const cf::PagesCall call{*in, *out, pages, rows, width, 1, nullptr, src, dst, count};
+    return cf::launch_pages_compact(call, workspace, static_cast<hipStream_t>(stream)) == hipSuccess ? CF_OK : CF_E_HIP;
+}
+
+int cf_pages_copy(void* data, int64_t pages, int64_t page_bytes, int layers, int64_t layer_stride, const int32_t* src,
+                  const int32_t* dst, int64_t n, const int32_t* count, void* stream) {
+    if (pages < 1 || pages > INT32_MAX || page_bytes < 16 || page_bytes % 16 || page_bytes > (int64_t(1) << 40) || layers < 1 ||
+        layers > 65535 || n < 0 || n > (1 << 30))
+        return CF_E_SHAPE;
+    const wide one = wide(pages) * page_bytes;
+    if (layers == 1) layer_stride = static_cast<int64_t>(one <= kMaxExtent ? one : 0);
+    if (one > kMaxExtent || layer_stride < one || layer_stride % 16 || wide(layers - 1) * layer_stride + one > kMaxExtent ||
+        wide(layers) * (page_bytes / 16384 + 1) > INT32_MAX)
+        return CF_E_SHAPE;
+    if (n == 0) return CF_OK;
+    if (!data || !src || !dst) return CF_E_NULL;
+    if (!aligned16(data) || !aligned4(src) || !aligned4(dst) || !aligned4(count)) return CF_E_ALIGN;
+    const Range d = range_of(data, static_cast<int64_t>(wide(layers - 1) * layer_stride + one));
+    if (overlap(d, range_of(src, n * 4)) || overlap(d, range_of(dst, n * 4)) || (count && overlap(d, range_of(count, 4)))) return CF_E_ALIAS;
+    if (int rc = check_device()) return rc;
+    return cf::launch_pages_copy(data, pages, page_bytes, layers, layer_stride, src, dst, n, count, static_cast<hipStream_t>(stream)) ==
+                   hipSuccess
                ? CF_OK
                : CF_E_HIP;
 }

@@ -7,6 +7,7 @@
 
 #include "cf.h"
 #include "cf_kv4.h"
+#include "cf_kv8.h"
 
 namespace cf {
 
@@ -79,10 +80,11 @@ hipError_t launch_kv4_append(int a_dtype, const RowSet& k, const RowSet& v, cons
 hipError_t launch_kv4_read(int a_dtype, const RowSet& k, const RowSet& v, const int64_t* slots, int64_t tokens,
                            const KvCache& cache, hipStream_t stream);
 
-// One attention call over the 4-bit cache.
-struct Kv4Attention {
+// One attention call over a paged cache.
+template <typename CACHE>
+struct PagedAttention {
     RowSet q, out;
-    KvCache cache;
+    CACHE cache;
     const int32_t* table;     // batch x table_width, or null: sequence b has pages b * table_width ..
     const int32_t* kv_lens;   // batch
     const int32_t* q_starts;  // batch + 1, or null: total_q / batch queries each
@@ -91,8 +93,47 @@ struct Kv4Attention {
     int batch, table_width, q_heads, causal, window;
     float scale;
 };
+using Kv4Attention = PagedAttention<KvCache>;
+using Kv8Attention = PagedAttention<Kv8Cache>;
 // max_rows: the most query tokens of a sequence times the query heads of a K/V head.
 size_t kv4_attention_workspace(int a_dtype, int head_dim, int64_t max_rows);
 hipError_t launch_kv4_attention(int a_dtype, const Kv4Attention& call, void* workspace, hipStream_t stream);
+size_t kv8_attention_workspace(int a_dtype, int head_dim, int64_t max_rows);
+hipError_t launch_kv8_attention(int a_dtype, const Kv8Attention& call, void* workspace, hipStream_t stream);
+
+hipError_t launch_kv8_append(int a_dtype, const RowSet& k, const RowSet& v, int64_t tokens, const Kv8Cache& cache,
+                             int batch, const int32_t* table, int table_width, const int32_t* kv_lens,
+                             const int32_t* starts, hipStream_t stream);
+hipError_t launch_kv8_read(int a_dtype, const RowSet& k, const RowSet& v, const int64_t* slots, int64_t tokens,
+                           const Kv8Cache& cache, hipStream_t stream);
+
+// One attention call over rows of keys and values.
+struct RowsAttention {
+    RowSet q, k, v, out;
+    const int32_t* q_starts;  // batch + 1, or null: total_q / batch queries each
+    const int32_t* k_starts;  // batch + 1, or null: total_k / batch keys each
+    float* lse;               // total_q x q_heads, or null
+    int64_t total_q, total_k, max_q;
+    int batch, q_heads, kv_heads, head_dim, causal, window;
+    float scale;
+};
+size_t attention_workspace(int a_dtype, int head_dim, int64_t max_rows);
+hipError_t launch_attention(int a_dtype, const RowsAttention& call, void* workspace, hipStream_t stream);
+
+// One operation on the pages of a cache: sequences in and out (refs, table, lens), and what it reads and says besides.
+using Pages = cf_pages;
+struct PagesCall {
+    Pages in, out;
+    int64_t pages;
+    int rows, width, page_size;
+    const int32_t* want;  // tokens, or parents
+    int32_t *src, *dst, *count;
+};
+size_t pages_workspace(int64_t pages, int rows);
+hipError_t launch_pages_resize(const PagesCall& call, void* workspace, hipStream_t stream);
+hipError_t launch_pages_fork(const PagesCall& call, void* workspace, hipStream_t stream);
+hipError_t launch_pages_compact(const PagesCall& call, void* workspace, hipStream_t stream);
+hipError_t launch_pages_copy(void* data, int64_t pages, int64_t page_bytes, int layers, int64_t layer_stride, const int32_t* src,
+                             const int32_t* dst, int64_t n, const int32_t* count, hipStream_t stream);
 
 }  // namespace cf

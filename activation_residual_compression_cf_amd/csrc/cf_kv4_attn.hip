@@ -30,77 +30,6 @@
 namespace cf {
 namespace {
 
-// Joins the parts of the items that ended up in several workgroups: block (w, y) some rows
-// of the item whose last keys were workgroup w's.  A few microseconds of latency, and with many
-// rows the parts' bytes (46 MB, 12 us, for 1024 queries over 4608 keys in 24 heads): eight
-// parts are in flight at once (one at a time 12 us where it now takes 4).
-template <typename T, int D, int ROWS>
-__global__ __launch_bounds__(kThreads) void join_kernel(const AttnArgs p) {
-    const int me = blockIdx.x;
-    const int32_t* const left = p.joins + me * kJoin;
-    const int first = scalar_load(left), head = scalar_load(left + 1), q0 = scalar_load(left + 2),
-              row0 = scalar_load(left + 3), rows = scalar_load(left + 4);
-    if (first < 0) return;  // and the rest says nothing
-    constexpr int kLanes = D / 4, kAtOnce = kThreads / kLanes;
-    const int l0 = threadIdx.x % kLanes, c = 4 * l0, self = threadIdx.x & 63 & ~(kLanes - 1);
-    for (int r0 = blockIdx.y * kAtOnce; r0 < rows; r0 += gridDim.y * kAtOnce) {
-        const int r = min(r0 + static_cast<int>(threadIdx.x) / kLanes, rows - 1);
-        const auto part = [&](int w) {
-            return p.part + (2 * int64_t(w) + (w == first)) * part_floats<D>(ROWS) + int64_t(r) * (D + 2);
-        };
-        // a row's lanes look at a part each
-        float top = kNone;
-        for (int w = first + l0; w <= me; w += kLanes) top = fmaxf(top, part(w)[D]);
-#pragma unroll
-        for (int d = 1; d < kLanes; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
-        float v[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f;
-        for (int w0 = first; w0 <= me; w0 += kLanes) {
-            const int w = w0 + l0;
-            float f = 0.f, lw = 0.f;
-            if (w <= me) {
-                const float2 ml = *reinterpret_cast<const float2*>(part(w) + D);
-                f = ml.x == kNone ? 0.f : __builtin_amdgcn_exp2f(ml.x - top);
-                lw = ml.y;
-            }
-            const int many = min(kLanes, me + 1 - w0);
-            for (int i = 0; i < many; i += 8) {  // eight parts in flight
-                float2 x0[8], x1[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float* const x = part(w0 + min(i + k, many - 1));  // again, for nothing: f is 0
-                    x0[k] = *reinterpret_cast<const float2*>(x + c), x1[k] = *reinterpret_cast<const float2*>(x + c + 2);
-                }
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float fi = __shfl(f, self + i + k, 64);
-                    l = __builtin_fmaf(__shfl(lw, self + i + k, 64), fi, l);
-                    v[0] = __builtin_fmaf(x0[k].x, fi, v[0]);
-                    v[1] = __builtin_fmaf(x0[k].y, fi, v[1]);
-                    v[2] = __builtin_fmaf(x1[k].x, fi, v[2]);
-                    v[3] = __builtin_fmaf(x1[k].y, fi, v[3]);
-                }
-            }
-        }
-        if (r0 + static_cast<int>(threadIdx.x) / kLanes >= rows) continue;
-        const int row = row0 + r, token = token_of(p, row), qh = head * p.share + row - token * p.share;
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        T* const o = row_ptr<T>(p.out, q0 + token, qh) + c;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) o[k] = static_cast<T>(v[k] * inv);
-        if (p.lse && c == 0)
-            p.lse[int64_t(q0 + token) * p.q_heads + qh] =
-                lse_of(top, l);
-    }
-}
-
-// A kernel's rows of an item, and its workgroups: as many as are resident at once.
-struct Plan {
-    int rows, groups, dim;
-    size_t bytes() const {
-        return size_t(groups) * (2 * (dim == 64 ? part_floats<64>(rows) : part_floats<128>(rows)) * 4 + 4 * kJoin);
-    }
-};
-
 // Calls f with the kernel's shape and the kernel for a call whose longest sequence has max_rows rows.
 template <typename T, int D, typename F>
 auto with_kernel(int64_t max_rows, F f) {
@@ -114,11 +43,6 @@ auto with_kernel(int a_dtype, int head_dim, int64_t max_rows, F f) {
     if (a_dtype == CF_BF16)
         return head_dim == 64 ? with_kernel<__bf16, 64>(max_rows, f) : with_kernel<__bf16, 128>(max_rows, f);
     return head_dim == 64 ? with_kernel<float, 64>(max_rows, f) : with_kernel<float, 128>(max_rows, f);
-}
-
-template <typename S>
-Plan plan_of(int head_dim) {
-    return {S::kRows, kUnitsOfGpu * S::kResident, head_dim};
 }
 
 }  // namespace
@@ -142,7 +66,7 @@ hipError_t launch_kv4_attention(int a_dtype, const Kv4Attention& c, void* worksp
     p.q = c.q, p.out = c.out, p.cache = c.cache, p.table = c.table, p.width = c.table_width;
     p.kv_lens = c.kv_lens, p.q_starts = c.q_starts, p.total_q = static_cast<int>(c.total_q);
     p.q_each = c.q_starts ? 0 : static_cast<int>(c.total_q / c.batch);
-    p.batch = c.batch, p.q_heads = c.q_heads, p.share = share;
+    p.batch = c.batch, p.q_heads = c.q_heads, p.kv_heads = c.cache.heads, p.share = share;
     p.causal = c.causal, p.window = c.window;
     p.scale_log2 = c.scale * 1.44269504088896341f;
     p.lse = c.lse;
@@ -154,10 +78,7 @@ hipError_t launch_kv4_attention(int a_dtype, const Kv4Attention& c, void* worksp
         p.part = reinterpret_cast<float*>(p.joins + kJoin * p.groups);
         kernel<<<p.groups, kThreads, 0, stream>>>(p);
         if (hipError_t e = hipGetLastError()) return e;
-        const int at_once = kThreads / (S::kDim / 4), rows = max_rows < S::kRows ? static_cast<int>(max_rows) : S::kRows;
-        join_kernel<typename S::Type, S::kDim, S::kRows>
-            <<<dim3(p.groups, (rows + at_once - 1) / at_once), kThreads, 0, stream>>>(p);
-        return hipGetLastError();
+        return launch_join<S>(p, max_rows, stream);
     });
 }
 

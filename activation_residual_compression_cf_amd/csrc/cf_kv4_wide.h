@@ -153,18 +153,17 @@ __device__ __forceinline__ bool store_share(Share<D>& x, uint8_t* lds, uint32_t 
         const int first = n * (D / 32), turn = W::v_turn(first) ^ vin / 8;  // pair of channels
         // a turn of the address: tiles start on 256 bytes
         const uint32_t w = static_cast<uint32_t>(W::kKeys * W::kKRow + first * 256 + (vin & 4) * 2 + 16 * turn) + tile_at;
-        using V = Prob<T>;
         const auto pair = [&](int j, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
             *reinterpret_cast<vu2*>(lds + ((w ^ 16 * j) + 256 * j)) =
                 vu2{__builtin_amdgcn_perm(b, a, 0x05040100u), __builtin_amdgcn_perm(d, c, 0x05040100u)};
             *reinterpret_cast<vu2*>(lds + ((w ^ 16 * (j ^ 8)) + 256 * j)) =
                 vu2{__builtin_amdgcn_perm(b, a, 0x07060302u), __builtin_amdgcn_perm(d, c, 0x07060302u)};
         };
-        pair(0, V::template decode<0>(v[0], f[0]), V::template decode<0>(v[1], f[1]), V::template decode<0>(v[2], f[2]), V::template decode<0>(v[3], f[3]));
-        pair(1, V::template decode<1>(v[0], f[0]), V::template decode<1>(v[1], f[1]), V::template decode<1>(v[2], f[2]), V::template decode<1>(v[3], f[3]));
+        pair(0, decode4<T, 0>(v[0], f[0]), decode4<T, 0>(v[1], f[1]), decode4<T, 0>(v[2], f[2]), decode4<T, 0>(v[3], f[3]));
+        pair(1, decode4<T, 1>(v[0], f[0]), decode4<T, 1>(v[1], f[1]), decode4<T, 1>(v[2], f[2]), decode4<T, 1>(v[3], f[3]));
         if constexpr (D == 128) {
-            pair(2, V::template decode<2>(v[0], f[0]), V::template decode<2>(v[1], f[1]), V::template decode<2>(v[2], f[2]), V::template decode<2>(v[3], f[3]));
-            pair(3, V::template decode<3>(v[0], f[0]), V::template decode<3>(v[1], f[1]), V::template decode<3>(v[2], f[2]), V::template decode<3>(v[3], f[3]));
+            pair(2, decode4<T, 2>(v[0], f[0]), decode4<T, 2>(v[1], f[1]), decode4<T, 2>(v[2], f[2]), decode4<T, 2>(v[3], f[3]));
+            pair(3, decode4<T, 3>(v[0], f[0]), decode4<T, 3>(v[1], f[1]), decode4<T, 3>(v[2], f[2]), decode4<T, 3>(v[3], f[3]));
         }
     }
     return nan;

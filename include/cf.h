@@ -373,6 +373,128 @@ int cf_kv4_attention(int a_dtype, const cf_rows* q, int64_t total_q, int q_heads
  * workspace of one call's bytes serves every call with fewer queries. */
 size_t cf_kv4_attention_workspace_bytes(int a_dtype, int64_t max_q, int q_heads, int kv_heads, int head_dim);
 
+/*
+ * The 8-bit K/V cache: pages, sizes and limits as the 4-bit one's, in a buffer of cf_kv8_cache_bytes bytes.  The
+ * block of page p and head h starts at (p * kv_heads + h) * B, B = 2 * P * D + max(16, P / 8), and holds, in this order:
+ *   K codes   [P][D]
+ *   V codes   [P/8][D][8 tokens]
+ *   K scales  [P/16]              a byte for each 16 tokens
+ *   V scales  [P/16]
+ * A code is E4M3: bit 7 the sign, four exponent bits of bias 7, three of the fraction; magnitudes up to 448, and 127
+ * reads NaN.  It stands for that times 2^(byte - 127).
+ *
+ * cf_kv8_append takes the last tokens of sequences: of sequence b, which has kv_lens[b] tokens with them, rows
+ * starts[b] .. starts[b+1] - 1 of k and v (tokens x kv_heads rows).  Token j of it lies in page table[b * table_width +
+ * j / page_size], as for cf_kv4_attention, and with 15 others of that page in one block of a scale.  For each block that
+ * gets tokens, and each head, for K and for V:
+ *   e = the least integer with max|x| <= 448 * 2^e over the finite values that come, but within [-15, 7];
+ *   where the block's first token is not among those that come: no less than the block's e before; if that grows, the
+ *     codes before those that come are rounded again, from what they stand for, as below;
+ *   byte = e + 127;  code = the nearest to x * 2^-e, ties to the even code, 448 above 448; 127 for NaN and infinities
+ * So values are held with an error of at most 2^-4 of themselves or 2^(e - 10), and magnitudes beyond 448 * 2^7 saturate.
+ * Places of a block behind the tokens that came hold nothing.  Rows with no place (kv_lens[b] is less than their number,
+ * a page outside the cache, rows of no sequence) are not kept.  Sequences of a call must not share a page that gets tokens.
+ *   k, v: tokens x kv_heads rows;  table, kv_lens, starts: as in cf_kv4_attention, the rows being the queries there;
+ *   tokens <= 2^27, 1 <= batch <= 2^24, table_width * page_size < 2^31 - 256.
+ * cf_kv8_read is as cf_kv4_read.
+ */
+int64_t cf_kv8_cache_bytes(int64_t pages, int page_size, int kv_heads, int head_dim);
+
+int cf_kv8_append(int a_dtype, const cf_rows* k, const cf_rows* v, int64_t tokens, uint8_t* cache, int64_t pages,
+                  int page_size, int kv_heads, int head_dim, int batch, const int32_t* table, int table_width,
+                  const int32_t* kv_lens, const int32_t* starts, void* stream);
+
+int cf_kv8_read(int a_dtype, const uint8_t* cache, int64_t pages, int page_size, int kv_heads, int head_dim,
+                const int64_t* slots, int64_t tokens, const cf_rows* k, const cf_rows* v, void* stream);
+
+/*
+ * Attention of ragged queries over the 8-bit cache: arguments, results and limits are cf_kv4_attention's.
+ * K and V enter the products exactly.  bf16: queries exactly, probabilities rounded, in calls of at most 32 rows (max_q
+ * times the query heads of a K/V head) to fp16 as there, in others to bf16 (2^-8 of each); fp32: queries and
+ * probabilities exactly.  A NaN of V reaches its channel in the rows that see it.
+ */
+int cf_kv8_attention(int a_dtype, const cf_rows* q, int64_t total_q, int q_heads, const uint8_t* cache,
+                     int64_t pages, int page_size, int kv_heads, int head_dim, int batch, const int32_t* table,
+                     int table_width, const int32_t* kv_lens, const int32_t* q_starts, int64_t max_q, int flags,
+                     int window, float scale, const cf_rows* out, float* lse, void* workspace, size_t ws_bytes,
+                     void* stream);
+
+size_t cf_kv8_attention_workspace_bytes(int a_dtype, int64_t max_q, int q_heads, int kv_heads, int head_dim);
+
+/*
+ * Attention over whole prompts: keys and values are rows of heads, of packed sequences.  Sequence b has the query tokens
+ * q_starts[b] .. q_starts[b+1] - 1 of the total_q rows of q and the keys k_starts[b] .. k_starts[b+1] - 1 of the total_k
+ * rows of k and v.  Masks, out and lse are as for cf_kv4_attention, with len = the sequence's keys.
+ *   q, out: total_q x q_heads rows of a_dtype;  k, v: total_k x kv_heads rows of a_dtype;
+ *   q_starts, k_starts: batch + 1 int32, or NULL: total_q / batch queries, total_k / batch keys each, without a rest;
+ *   max_q: the most query tokens of a sequence, as there;  lse: total_q x q_heads fp32, or NULL;
+ *   workspace: cf_attention_workspace_bytes, 256-byte aligned, as there.
+ * Rows of out and lse that belong to no sequence stay as they are.  head_dim is 64 or 128;  total_k <= 2^31 - 256, and
+ * token strides of k and v are at most 2^26 bytes;  the other limits are cf_kv4_attention's.  total_k = 0 is a call whose rows see no key.
+ * bf16: queries, keys and values enter the products exactly, probabilities rounded to bf16, off by at most 2^-8 of
+ * each.  fp32 (magnitudes up to 2^127): as six products of bf16 parts, off by at most 2^-24 of their factors.  Scores, sums and results are fp32
+ * up to the final rounding to a_dtype.  Magnitudes of V up to 2^100.  An infinity or NaN of a key or value reaches only rows that see
+ * it; a NaN gives NaN there, an infinity infinities or NaN, or, of a key, weight 0.  Deterministic as cf_kv4_attention.
+ */
+int cf_attention(int a_dtype, const cf_rows* q, int64_t total_q, int q_heads, const cf_rows* k, const cf_rows* v,
+                 int64_t total_k, int kv_heads, int head_dim, int batch, const int32_t* q_starts,
+                 const int32_t* k_starts, int64_t max_q, int flags, int window, float scale, const cf_rows* out,
+                 float* lse, void* workspace, size_t ws_bytes, void* stream);
+
+size_t cf_attention_workspace_bytes(int a_dtype, int64_t max_q, int q_heads, int kv_heads, int head_dim);
+
+/*
+ * Who holds which page of a cache.  `rows` sequences of up to `width` pages of page_size tokens: row r has lens[r] tokens
+ * in pages table[r * width] .. ; refs[p] counts the entries that hold page p, and a page with 0 is free.  The same
+ * three arrays serve every cache whose pages they number (4 or 8 bits, each layer's).  The calls below read `in` and write
+ * `out`; entries behind a row's last page are written as -1.  Entries that are no page of the cache are handed on and counted
+ * nowhere, and lens are taken within [0, width * page_size].  refs not less than 0.
+ *
+ * cf_pages_resize: row r gets want[r] tokens (negative: it stays as it is).  First rows that shrink let go the pages they
+ *   no longer need (all of them at 0 tokens); then those that grow, in the order of rows, take free pages in the order of
+ *   their numbers.  A row whose pages, behind those of the rows before it, are not all there, or that wants more than
+ *   width * page_size, stays as it is.  missing: how many those are.
+ * cf_pages_fork: row r becomes a copy of row parents[r] as it was (itself: it stays; outside [0, rows): it becomes empty).
+ *   Whole pages are shared.  A last, partly filled page goes on with the parent itself, or else the first of the rows; every
+ *   other row, in the order of rows, takes the first free page in its place, src[r] and dst[r] being the pages to copy, for
+ *   cf_pages_copy (-1 both where there is nothing to copy).  Pages that no row keeps are let go before that.  A row that
+ *   finds no free page ends with its last whole page.  missing: how many those are.
+ * cf_pages_compact: the pages that are held are made the first ones: the k-th of those behind, page src[k], goes to the
+ *   k-th free one before, dst[k], for cf_pages_copy; refs and every table entry follow.  count: how many; src and dst have
+ *   pages / 2 places, the rest -1.  lens stay.
+ *   out may be in, array by array, for resize and compact; fork's table and lens must be other arrays.
+ *   want, parents: rows int32;  src, dst: rows int32 (fork), pages / 2 (compact);  missing, count: one int32.
+ *   workspace: cf_pages_workspace_bytes, 4-byte aligned.
+ *   1 <= pages < 2^31, 1 <= rows <= 2^20, width >= 1, rows * width <= 2^30, width * page_size < 2^31 - 256, page_size >= 1.
+ *   All arrays 4-byte aligned.
+ *
+ * cf_pages_copy: page src[i] to page dst[i], in each of `layers` caches that lie layer_stride bytes apart, for i < n and,
+ *   where count is not NULL, i < *count.  Pairs of which one is no page, or both the same, copy nothing.  A page
+ *   that is copied to must not be in another pair.
+ *   page_bytes and layer_stride multiples of 16, layer_stride >= pages * page_bytes (with one layer it does not
+ *   matter), data 16-byte aligned; 0 <= n <= 2^30, 1 <= layers <= 65535.
+ */
+typedef struct cf_pages {
+    int32_t* refs;
+    int32_t* table;
+    int32_t* lens;
+} cf_pages;
+
+size_t cf_pages_workspace_bytes(int64_t pages, int rows);
+
+int cf_pages_resize(const cf_pages* in, const cf_pages* out, int64_t pages, int rows, int width, int page_size,
+                    const int32_t* want, int32_t* missing, void* workspace, size_t ws_bytes, void* stream);
+
+int cf_pages_fork(const cf_pages* in, const cf_pages* out, int64_t pages, int rows, int width, int page_size,
+                  const int32_t* parents, int32_t* src, int32_t* dst, int32_t* missing, void* workspace, size_t ws_bytes,
+                  void* stream);
+
+int cf_pages_compact(const cf_pages* in, const cf_pages* out, int64_t pages, int rows, int width, int32_t* src,
+                     int32_t* dst, int32_t* count, void* workspace, size_t ws_bytes, void* stream);
+
+int cf_pages_copy(void* data, int64_t pages, int64_t page_bytes, int layers, int64_t layer_stride, const int32_t* src,
+                  const int32_t* dst, int64_t n, const int32_t* count, void* stream);
+
 /* Workspace bytes cf_lowrank_compress needs (0 for arguments outside the limits). */
 size_t cf_lowrank_workspace_bytes(int64_t m, int64_t n, int rank, int batch);
 
