@@ -53,26 +53,33 @@ __device__ __forceinline__ Seq seq_at(const RowsArgs& p, int b) {
 
 // Tiles of rows: K and V both [key][D] bf16, fp32 as three planes of each.  V is read across its rows by the
 // transposing reads of shared memory.
-template <typename T, int D>
+template <typename T, int D, int WAVES>
 struct RowSource {
+    static constexpr int kWaves = WAVES;
     using Type = T;
     using Args = RowsArgs;
     static constexpr int kDim = D;
     static constexpr int kQueryParts = sizeof(T) == 4 ? 3 : 1, kKeyParts = kQueryParts;
     static constexpr int kKeys = sizeof(T) == 4 ? 32 : 64;
     static constexpr int kPad = 4;
-    static constexpr int kResident = 1;
+    // workgroups of a compute unit, by their registers and shared memory
+    static constexpr int kResident = sizeof(T) == 2 && D == 64 && WAVES == 4 ? 3 : 1;
     static constexpr int kPlane = kKeys * D * 2;
     static constexpr int kBytes = 2 * kKeyParts * kPlane;
     // a thread's loads: 16 bytes of kPasses rows, kStep apart
-    static constexpr int kChunks = D * sizeof(T) / 16, kStep = kThreads / kChunks, kPasses = kKeys / kStep;
+    static constexpr int kChunks = D * sizeof(T) / 16, kStep = 64 * WAVES / kChunks, kPasses = kKeys / kStep;
     static constexpr int kTurn = D == 128 ? 7 : 3;
+
+    static constexpr int kGroup = 64 * WAVES, kBad = kGroup * kPasses;
+    static constexpr bool kOrdered = true;
+    static constexpr int kPieces = 2 * kPasses;  // of a thread's loads and stores of a tile: K's, and V's
 
     const char* k;  // the sequence's first key
     const char* v;
     uint32_t k_stride, v_stride, k_off, v_off;
-    uint32_t k_lane, v_lane[2];
-    vu4 kr[kPasses], vr[kPasses];
+    uint32_t k_lane, v_lane[2], k_store, v_store;
+    __amdgpu_buffer_rsrc_t k_tile, v_tile;
+    vu4 r[kPieces];
 
     // rounded parts: what the products leave out is then at most 2^-24 of their factors
     static __device__ __forceinline__ __bf16 part(float* rest) { return round_bf16(rest); }
@@ -83,66 +90,103 @@ struct RowSource {
     __device__ __forceinline__ void begin(const RowsArgs& p) {
         const int lane = threadIdx.x & 63, n = lane & 31, h = lane >> 5;
         k_stride = static_cast<uint32_t>(p.k.token_stride * sizeof(T)), v_stride = static_cast<uint32_t>(p.v.token_stride * sizeof(T));
-        const uint32_t row = threadIdx.x / kChunks, c = threadIdx.x % kChunks * 16;
-        k_off = row * k_stride + c, v_off = row * v_stride + c;
+        const uint32_t row = threadIdx.x / kChunks, c = threadIdx.x % kChunks;
+        k_off = row * k_stride + 16 * c, v_off = row * v_stride + 16 * c;
+        if constexpr (sizeof(T) == 2)
+            k_store = KeyRows<D>::chunk(row, c), v_store = run(row, c >> 1) + (c & 1) * 16;
+        else
+            k_store = KeyRows<D>::chunk(row, c >> 1) + (c & 1) * 8, v_store = run(row, c >> 2) + (c & 3) * 8;
         k_lane = KeyRows<D>::chunk(KeyRows<D>::key_of(n), h);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
             v_lane[i] = run(8 * h + 4 * i + ((lane & 15) >> 2), lane >> 4 & 1) + (lane & 3) * 8;
     }
-    __device__ __forceinline__ void item(const RowsArgs& p, const Seq& s, int, int head) {
+    __device__ __forceinline__ void item(const RowsArgs& p, const Seq& s, int, int head, int) {
         k = reinterpret_cast<const char*>(row_ptr<T>(p.k, s.k0, head));
         v = reinterpret_cast<const char*>(row_ptr<T>(p.v, s.k0, head));
     }
-    // rows behind the sequence's last are its last again, and masked later
-    __device__ __forceinline__ void load(const RowsArgs&, const Seq& s, int key0) {
-        const int last = s.len - 1 - key0;
-        if (last >= kKeys - 1) {
+    // Loads are cut off behind the sequence's last row, by the hardware: what lies there reads as zeros.
+    __device__ __forceinline__ void next_tile(const RowsArgs&, const Seq& s, int key0, bool on) {
+        const int rows = on ? min(s.len - key0, kKeys) : 0;
+        const auto tile = [&](const char* first, uint32_t stride) {
+            const int64_t at = reinterpret_cast<int64_t>(first) + int64_t(key0) * stride;
+            return stream_rsrc(reinterpret_cast<void*>(uniform(at)), rows > 0 ? (rows - 1) * stride + D * sizeof(T) : 0u);
+        };
+        k_tile = tile(k, k_stride), v_tile = tile(v, v_stride);
+    }
+    __device__ __forceinline__ void load(int i) {
+        r[i] = i < kPasses ? __builtin_amdgcn_raw_buffer_load_b128(k_tile, k_off + i * (kStep * k_stride), 0, 0)
+                           : __builtin_amdgcn_raw_buffer_load_b128(v_tile, v_off + (i - kPasses) * (kStep * v_stride), 0, 0);
+    }
+    __device__ __forceinline__ void store(uint8_t* lds, int buf, int i) {
+        const bool is_k = i < kPasses;
+        const int further = (is_k ? i : i - kPasses) * kStep;
+        // rows 16 further turn as these do, and rows 8 further in one bit
+        const uint32_t turn = is_k ? (D == 128 && further & 8 ? 128u : 0u) : 0u;
+        static_assert(kStep % 16 == 0 || (D == 128 && kStep == 8), "");
+        uint8_t* const at = lds + buf * kBytes + (is_k ? k_store ^ turn : v_store + kKeyParts * kPlane) + further * (2 * D);
+        if constexpr (sizeof(T) == 2) {
+            *reinterpret_cast<vu4*>(at) = r[i];
+        } else {
+            vf4 x = __builtin_bit_cast(vf4, r[i]);
+            typedef __bf16 vb4 __attribute__((ext_vector_type(4)));
 #pragma unroll
-            for (int i = 0; i < kPasses; ++i) {
-                kr[i] = *reinterpret_cast<const vu4*>(k + int64_t(key0 + i * kStep) * k_stride + k_off);
-                vr[i] = *reinterpret_cast<const vu4*>(v + int64_t(key0 + i * kStep) * v_stride + v_off);
+            for (int k = 0; k < kKeyParts; ++k) {
+                vb4 a;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float f = x[j];
+                    a[j] = part(&f);
+                    x[j] = f;
+                }
+                *reinterpret_cast<vb4*>(at + k * kPlane) = a;
             }
-            return;
-        }
-        const int c = threadIdx.x % kChunks * 16;
-#pragma unroll
-        for (int i = 0; i < kPasses; ++i) {
-            const int row = key0 + min(static_cast<int>(threadIdx.x) / kChunks + i * kStep, last);
-            kr[i] = vr[i] = vu4{0, 0, 0, 0};
-            if (s.len == 0) continue;  // no row at all
-            kr[i] = *reinterpret_cast<const vu4*>(k + int64_t(row) * k_stride + c);
-            vr[i] = *reinterpret_cast<const vu4*>(v + int64_t(row) * v_stride + c);
         }
     }
-    __device__ __forceinline__ void store(const RowsArgs&, const Seq&, uint8_t* lds, uint8_t*, int buf, int) {
-        const int row = threadIdx.x / kChunks, c = threadIdx.x % kChunks;
-        uint8_t* const at = lds + buf * kBytes;
+    // Where some of the item's rows do not see all of the tile (part), a probability of zero times an infinity or NaN of V
+    // would be NaN: zeros take their place, and bits, a byte for a thread's 16 bytes, say where.
+    __device__ __forceinline__ void stored(const RowsArgs&, const Seq&, uint8_t* flag, uint8_t* bads, uint8_t* lds, int buf, bool part) {
+        uint32_t any = 0;
+        if (part) {
+            const auto bits = [&](int i) {
+                uint32_t b = 0;
 #pragma unroll
-        for (int i = 0; i < kPasses; ++i) {
-            const int r = row + i * kStep;
-            if constexpr (sizeof(T) == 2) {
-                *reinterpret_cast<vu4*>(at + KeyRows<D>::chunk(r, c)) = kr[i];
-                *reinterpret_cast<vu4*>(at + kPlane + run(r, c >> 1) + (c & 1) * 16) = vr[i];
-            } else {
-                vf4 x = __builtin_bit_cast(vf4, kr[i]), y = __builtin_bit_cast(vf4, vr[i]);
-                typedef __bf16 vb4 __attribute__((ext_vector_type(4)));
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t w = r[kPasses + i][j];
+                    b |= sizeof(T) == 4 ? static_cast<uint32_t>((w & 0x7f800000u) == 0x7f800000u) << j
+                                        : static_cast<uint32_t>((w & 0x7f80u) == 0x7f80u) << (2 * j) |
+                                              static_cast<uint32_t>((w & 0x7f800000u) == 0x7f800000u) << (2 * j + 1);
+                }
+                return b;
+            };
 #pragma unroll
-                for (int k = 0; k < kKeyParts; ++k) {
-                    vb4 a, b;
+            for (int i = 0; i < kPasses; ++i) any |= bits(i);
+            if (__any(any != 0)) {
+                any = 1;
+#pragma unroll
+                for (int i = 0; i < kPasses; ++i) {
+                    const uint32_t b = bits(i);
+                    bads[i * kGroup + threadIdx.x] = static_cast<uint8_t>(b);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        float f = x[j], g = y[j];
-                        a[j] = part(&f), b[j] = part(&g);
-                        x[j] = f, y[j] = g;
+                        if constexpr (sizeof(T) == 4)
+                            r[kPasses + i][j] = b >> j & 1u ? 0u : r[kPasses + i][j];
+                        else
+                            r[kPasses + i][j] &= (b >> (2 * j) & 1u ? 0u : 0xffffu) | (b >> (2 * j + 1) & 1u ? 0u : 0xffff0000u);
                     }
-                    *reinterpret_cast<vb4*>(at + k * kPlane + KeyRows<D>::chunk(r, c >> 1) + (c & 1) * 8) = a;
-                    *reinterpret_cast<vb4*>(at + (kKeyParts + k) * kPlane + run(r, c >> 2) + (c & 3) * 8) = b;
+                    store(lds, buf, kPasses + i);
                 }
             }
         }
+        if ((threadIdx.x & 63) == 0) flag[threadIdx.x >> 6] = static_cast<uint8_t>(any);
     }
-    static __device__ __forceinline__ uint32_t none(const uint8_t*, int) { return 0; }
+    static __device__ __forceinline__ uint32_t none(FlagWord) { return 0; }
+    static __device__ __forceinline__ bool found(FlagWord flag) { return flag != 0; }
+    // whether a channel of a key of a tile is infinite or NaN
+    static __device__ __forceinline__ bool bad(FlagWord flag, const uint8_t* bads, int key, int c) {
+        const int thread = key % kStep * kChunks + c / (16 / int(sizeof(T)));
+        return (flag >> (8 * (thread >> 6)) & 1u) && (bads[key / kStep * kGroup + thread] >> (c % (16 / int(sizeof(T)))) & 1u);
+    }
     // terms 16 c .. of a product's 32 keys
     __device__ __forceinline__ vb8 k_frag(const uint8_t* lds, int buf, int half, int part, int c) const {
         return *reinterpret_cast<const vb8*>(lds + buf * kBytes + (k_lane ^ 32 * c) + part * kPlane + half * 64 * D);
@@ -159,17 +203,18 @@ struct RowSource {
         }
         return __builtin_bit_cast(vb8, __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7));
     }
-    // whether a channel of key t of a half is infinite or NaN
-    __device__ __forceinline__ bool v_bad(const uint8_t* lds, int buf, int half, int t, int c) const {
-        const int r = 32 * half + t;
-        const uint16_t x = *reinterpret_cast<const uint16_t*>(lds + buf * kBytes + kKeyParts * kPlane + run(r, c >> 4) + (c & 15) * 2);
-        return (x & 0x7f80u) == 0x7f80u;
-    }
 };
 
+// Calls f with the kernel's shape and the kernel for a call whose longest sequence has max_rows rows.
 template <typename T, int D, typename F>
-auto with_kernel(int64_t, F f) {
-    using K = Tile<RowSource<T, D>, 1>;
+auto with_kernel(int64_t max_rows, F f) {
+    if constexpr (sizeof(T) == 2) {
+        if (max_rows > 128) {
+            using K = Tile<RowSource<T, D, 8>, 1>;
+            return f(K(), tile_kernel<K>);
+        }
+    }
+    using K = Tile<RowSource<T, D, 4>, 1>;
     return f(K(), tile_kernel<K>);
 }
 
@@ -182,9 +227,16 @@ auto with_kernel(int a_dtype, int head_dim, int64_t max_rows, F f) {
 
 }  // namespace
 
+// The largest of what the kernels for up to so many rows use, so that a workspace serves every call with fewer rows too.
 size_t attention_workspace(int a_dtype, int head_dim, int64_t max_rows) {
-    return with_kernel(a_dtype, head_dim, max_rows,
-                       [&](auto shape, auto) { return plan_of<decltype(shape)>(head_dim).bytes(); });
+    size_t most = 0;
+    for (const int64_t rows : {1, 129}) {  // the fewest of each kernel
+        if (rows > max_rows) break;
+        const size_t n = with_kernel(a_dtype, head_dim, rows,
+                                     [&](auto shape, auto) { return plan_of<decltype(shape)>(head_dim).bytes(); });
+        most = n > most ? n : most;
+    }
+    return most;
 }
 
 hipError_t launch_attention(int a_dtype, const RowsAttention& c, void* workspace, hipStream_t stream) {
@@ -204,7 +256,7 @@ hipError_t launch_attention(int a_dtype, const RowsAttention& c, void* workspace
         p.groups = plan_of<S>(c.head_dim).groups;
         p.joins = static_cast<int32_t*>(workspace);
         p.part = reinterpret_cast<float*>(p.joins + kJoin * p.groups);
-        kernel<<<p.groups, kThreads, 0, stream>>>(p);
+        kernel<<<p.groups, S::kGroup, 0, stream>>>(p);
         if (hipError_t e = hipGetLastError()) return e;
         return launch_join<S>(p, max_rows, stream);
     });

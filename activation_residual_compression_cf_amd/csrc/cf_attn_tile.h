@@ -14,15 +14,14 @@ namespace {
 //   S^T = K Q^T   K's rows are keys, in such an order that lane (h, n) ends up with the scores of keys 8 h .. 8 h + 7
 //                 and 16 + 8 h .. for row n
 //   O^T = V^T P^T the terms are keys: the lane has them.
-// A step multiplies the next 32 keys by the queries and this 32 keys' probabilities by V: the products of the one go
-// beside the exponentials of the other, in one wave, so that the matrix units need no second wave to be kept busy.
 template <typename SRC, int RB>
 struct Tile {
+    static constexpr int kGroup = 64 * SRC::kWaves;  // threads
     using Source = SRC;
     using Type = typename SRC::Type;
     static constexpr int kDim = SRC::kDim;
     static constexpr int kRB = RB;
-    static constexpr int kRows = 32 * RB * kWaves;
+    static constexpr int kRows = 32 * RB * SRC::kWaves;
     static constexpr int kKeys = SRC::kKeys;  // of a tile: 32 or 64
     static constexpr int kSub = kKeys / 32;
     static constexpr int kPad = SRC::kPad;
@@ -52,14 +51,31 @@ __device__ __forceinline__ __bf16 round_bf16(float* rest) {
     return b;
 }
 
-// bf16 that is infinite or NaN, in a word of two: its bits all set.
-__device__ __forceinline__ uint32_t not_finite2(uint32_t w) {
-    const uint32_t lo = (w & 0x7f80u) == 0x7f80u ? 0xffffu : 0u, hi = (w & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u;
-    return lo | hi;
+// A byte of each wave, about its share of a tile.
+typedef uint64_t FlagWord;
+
+// Nothing moves across: what is read before is in flight while what stands before is worked on.
+template <bool ON>
+__device__ __forceinline__ void stay() {
+    if constexpr (ON) __builtin_amdgcn_sched_barrier(0);
+}
+
+// Keeps the computation of a value where it stands: left alone, the compiler moves it behind the branches to its use, and
+// nothing goes beside the products any more.
+template <typename V>
+__device__ __forceinline__ void here(V& x) {
+    asm volatile("" : "+v"(x));
+}
+
+// A barrier for what is in shared memory: loads of global memory stay under way.
+__device__ __forceinline__ void share_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
 template <typename K>
-__global__ __launch_bounds__(kThreads, K::kResident) void tile_kernel(const typename K::Source::Args p) {
+__global__ __launch_bounds__(K::kGroup, K::kResident * K::Source::kWaves / 4) void tile_kernel(const typename K::Source::Args p) {
     using S = typename K::Source;
     using T = typename K::Type;
     constexpr int D = K::kDim, RB = K::kRB, kRows = K::kRows, kKeys = K::kKeys, kSub = K::kSub, kPad = K::kPad;
@@ -67,7 +83,9 @@ __global__ __launch_bounds__(kThreads, K::kResident) void tile_kernel(const type
     constexpr int kC = D / 16, kDt = D / 32;
     const int lane = threadIdx.x & 63, wave = uniform(static_cast<int>(threadIdx.x) >> 6), n = lane & 31, h = lane >> 5;
     __shared__ __align__(256) uint8_t lds[K::kBuffers * S::kBytes];
-    __shared__ uint8_t flags[K::kBuffers][4];
+    // of each buffer's tile: a byte for each wave's share, and which of V's elements are infinite or NaN
+    __shared__ __align__(8) uint8_t flags[K::kBuffers][8];
+    __shared__ uint8_t bads[K::kBuffers][S::kBad];
 
     Place w;
     const bool work = place_of<kRows, kKeys, kPad>(p, &w);
@@ -89,8 +107,10 @@ __global__ __launch_bounds__(kThreads, K::kResident) void tile_kernel(const type
         const int row0 = w.tile * kRows + wave * 32 * RB;  // the wave's first
         const int tiles = z - a, base = (u0 + a) * kKeys;   // the run's first key
 
-        src.item(p, s, w.b, w.head);
-        src.load(p, s, base);
+        src.item(p, s, w.b, w.head, base);
+        src.next_tile(p, s, base, true);
+#pragma unroll
+        for (int i = 0; i < S::kPieces; ++i) src.load(i);
 
         vb8 q[RB][QP][kC];
         int lo[RB], hi[RB];
@@ -131,164 +151,221 @@ __global__ __launch_bounds__(kThreads, K::kResident) void tile_kernel(const type
                 for (int k = 0; k < 16; ++k) o[b][j][k] = 0.f;
         }
 
-        vf16 now[RB], next[RB];  // scores
-        uint32_t none_now = 0, none_next = 0;  // 16 keys without a page, a bit each
+        uint64_t bad[RB];  // the lane's channels (a bit for each of o) that an infinity or NaN of V has reached
+#pragma unroll
+        for (int b = 0; b < RB; ++b) bad[b] = 0;
+        int wg_lo = 0, wg_hi = INT32_MAX;  // keys that all of the item's rows see
+        {
+            const int r0 = w.tile * kRows, r1 = min(r0 + kRows, rows) - 1;
+            if (r1 >= r0) wg_lo = seen_lo(p, s, token_of(p, r1)), wg_hi = seen_hi(p, s, token_of(p, r0));
+        }
+        // The tile from key0 is all on its way to a buffer.
+        const auto stored = [&](int buf, int key0) {
+            src.stored(p, s, flags[buf], bads[buf], lds, buf, key0 < wg_lo || key0 + kKeys > wg_hi);
+        };
+        // The operands of a tile's products, in their order: K's terms 16 (f % kC) of half f / kC of the keys, then V's of half
+        // v / (2 kDt), terms 16 (v / kDt % 2), channels 32 (v % kDt), then the next tile's.  They are read kAhead before they
+        // are used.
+        constexpr int kKs = kSub * kC, kVs = kSub * 2 * kDt, kAhead = KP == 1 ? 4 : 2, kRing = 2 * kAhead;
+        static_assert((kKs + kVs) % kRing == 0, "a ring's places are the same in every tile");
+        vb8 ring[kRing][KP];
+        const auto fetch = [&](int f, int buf, int next_buf) {
+            const int v = f - kKs, n = v - kVs;
+#pragma unroll
+            for (int k = 0; k < KP; ++k)
+                ring[f % kRing][k] = f < kKs  ? src.k_frag(lds, buf, f / kC, k, f % kC)
+                                     : v < kVs ? src.v_frag(lds, buf, v / (2 * kDt), k, v / kDt % 2, v % kDt)
+                                               : src.k_frag(lds, next_buf, n / kC, k, n % kC);
+        };
 
-        // scores of keys 32 half .. of the tile in a buffer
-        const auto qk = [&](vf16 (&x)[RB], int buf, int half) {
+        // Tile t is in buffer t % 3.  One barrier a tile, in its middle: before it waves read K of tile t, write tile t + 1
+        // and may still read V of tile t - 1; behind it they read V of tile t and the first of K of tile t + 1.
+        share_barrier();  // the last item's tiles have been read
 #pragma unroll
-            for (int b = 0; b < RB; ++b)
+        for (int i = 0; i < S::kPieces; ++i) src.store(lds, 0, i);
+        stored(0, base);
+        src.next_tile(p, s, base + kKeys, tiles > 1);
 #pragma unroll
-                for (int r = 0; r < 16; ++r) x[b][r] = 0.f;
+        for (int i = 0; i < S::kPieces; ++i) src.load(i);
+        share_barrier();
 #pragma unroll
-            for (int c = 0; c < kC; ++c) {
-                vb8 kf[KP];
+        for (int f = 0; f < kAhead; ++f) fetch(f, 0, 1);
+        int buf = 0, next_buf = 1;  // of tiles t and t + 1
+#pragma unroll 1
+        for (int t = 0; t < tiles; ++t) {
+            const int key0 = base + t * kKeys;
+            FlagWord flag = static_cast<uint32_t>(uniform(static_cast<int>(*reinterpret_cast<const uint32_t*>(flags[buf]))));
+            if constexpr (S::kWaves > 4) flag |= static_cast<FlagWord>(static_cast<uint32_t>(uniform(static_cast<int>(*reinterpret_cast<const uint32_t*>(flags[buf] + 4))))) << 32;
+            const bool edge = key0 < full_lo || key0 + kKeys > full_hi || S::none(flag) != 0;
+
+            vf16 x[kSub][RB];           // scores: r of half g is of key key0 + 32 g + 8 h + 16 (r / 8) + r % 8
+            vu4 pf[kSub][RB][2][QP];    // their probabilities: bf16 in pairs
+            float ref[RB], more[RB];
+            const auto key_product = [&](int f) {
+                if (f % kC == 0)
 #pragma unroll
-                for (int k = 0; k < KP; ++k) kf[k] = src.k_frag(lds, buf, half, k, c);
+                    for (int b = 0; b < RB; ++b)
 #pragma unroll
-                for (int t = kMost; t >= 0; --t)  // the smallest parts first
+                        for (int r = 0; r < 16; ++r) x[f / kC][b][r] = 0.f;
+                fetch(f + kAhead, buf, next_buf);
+#pragma unroll
+                for (int i = kMost; i >= 0; --i)  // the smallest parts first
 #pragma unroll
                     for (int k = 0; k < KP; ++k) {
-                        if (t - k < 0 || t - k >= QP) continue;
+                        if (i - k < 0 || i - k >= QP) continue;
 #pragma unroll
                         for (int b = 0; b < RB; ++b)
-                            x[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[k], q[b][t - k][c], x[b], 0, 0, 0);
+                            x[f / kC][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ring[f % kRing][k], q[b][i - k][f % kC], x[f / kC][b], 0, 0, 0);
                     }
-            }
-        };
-        // score r is of key key0 + 8 h + 16 (r / 8) + r % 8
-        const auto mask = [&](vf16 (&x)[RB], int key0, uint32_t none) {
+            };
+            const auto value_product = [&](int v) {
+                fetch(kKs + v + kAhead, buf, next_buf);
 #pragma unroll
-            for (int b = 0; b < RB; ++b)
+                for (int i = kMost; i >= 0; --i)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int key = key0 + 8 * h + 16 * (r / 8) + r % 8;
-                    if ((none >> (r / 8) & 1u) || key < lo[b] || key >= hi[b]) x[b][r] = kNone;
-                }
-        };
-        const auto on_edge = [&](int key0, uint32_t none) { return key0 < full_lo || key0 + 32 > full_hi || none != 0; };
-        // moves the references to new scores
-        const auto refer = [&](vf16 (&x)[RB]) {
+                    for (int k = 0; k < KP; ++k) {
+                        if (i - k < 0 || i - k >= QP) continue;
 #pragma unroll
-            for (int b = 0; b < RB; ++b) {
-                float top = kNone;
+                        for (int b = 0; b < RB; ++b)
+                            o[b][v % kDt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ring[(kKs + v) % kRing][k], __builtin_bit_cast(vb8, pf[v / (2 * kDt)][b][v / kDt % 2][i - k]),
+                                                                                    o[b][v % kDt], 0, 0, 0);
+                    }
+            };
+            // pairs i0 .. i1 - 1 of half g's probabilities
+            const auto exps = [&](int g, int i0, int i1) {
 #pragma unroll
-                for (int r = 0; r < 16; ++r) top = fmaxf(top, x[b][r]);
-                top *= p.scale_log2;
-                if (__any(top > m[b] + kRise)) {
-                    const float r = fmaxf(fmaxf(top, __shfl_xor(top, 32, 64)), m[b]);
-                    const float f = m[b] == r ? 1.f : __builtin_amdgcn_exp2f(m[b] - r);
-                    m[b] = r;
-                    sum[b] *= f;
+                for (int i = i0; i < i1; ++i)
 #pragma unroll
-                    for (int j = 0; j < kDt; ++j) o[b][j] *= f;
-                }
-            }
-        };
-        // probabilities of scores, times V of their keys
-        const auto pv = [&](vf16 (&x)[RB], int buf, int half, int key0, bool edge) {
-            vb8 pf[RB][2][QP];
+                    for (int b = 0; b < RB; ++b) {
+                        float e[2];
 #pragma unroll
-            for (int b = 0; b < RB; ++b) {
-                const float ref = m[b] == kNone ? 0.f : -m[b];
-                float more = 0.f;  // first by itself: one by one, small ones would be lost beside a large sum
+                        for (int j = 0; j < 2; ++j) {
+                            e[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[g][b][2 * i + j], p.scale_log2, ref[b]));
+                            more[b] += e[j];
+                        }
+                        here(more[b]);
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    float e = __builtin_amdgcn_exp2f(__builtin_fmaf(x[b][r], p.scale_log2, ref));
-                    more += e;
-                    if constexpr (QP == 1)
-                        pf[b][r / 8][0][r % 8] = static_cast<__bf16>(e);
-                    else
-#pragma unroll
-                        for (int k = 0; k < QP; ++k) pf[b][r / 8][k][r % 8] = S::part(&e);
-                }
-                sum[b] += more;
-            }
-            bool bad = false;
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int j = 0; j < kDt; ++j) {
-                    vb8 vf[KP];
-#pragma unroll
-                    for (int k = 0; k < KP; ++k) vf[k] = src.v_frag(lds, buf, half, k, t, j);
-                    if (edge) {
-                        // a probability of zero times an infinity or NaN would be NaN
-#pragma unroll
-                        for (int k = 0; k < KP; ++k) {
-                            vu4 y = __builtin_bit_cast(vu4, vf[k]);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const uint32_t z2 = not_finite2(y[i]);
-                                bad |= z2 != 0;
-                                y[i] &= ~z2;
-                            }
-                            vf[k] = __builtin_bit_cast(vb8, y);
+                        for (int k = 0; k < QP; ++k) {
+                            const vb2 y = QP == 1 ? vb2{static_cast<__bf16>(e[0]), static_cast<__bf16>(e[1])} : vb2{S::part(&e[0]), S::part(&e[1])};
+                            uint32_t word = __builtin_bit_cast(uint32_t, y);
+                            here(word);
+                            pf[g][b][i / 4][k][i % 4] = word;
                         }
                     }
+            };
+            // masks new scores and moves the references to them: to whole numbers, so that what is moved with them stays as exact
+            const auto settle = [&](int g) {
+                if (edge) {
 #pragma unroll
-                    for (int i = kMost; i >= 0; --i)
+                    for (int b = 0; b < RB; ++b)
 #pragma unroll
-                        for (int k = 0; k < KP; ++k) {
-                            if (i - k < 0 || i - k >= QP) continue;
+                        for (int r = 0; r < 16; ++r) {
+                            const int run = 2 * g + r / 8, key = key0 + 8 * h + 16 * run + r % 8;
+                            if ((S::none(flag) >> run & 1u) || key < lo[b] || key >= hi[b]) x[g][b][r] = kNone;
+                        }
+                }
+                float top[RB];
+                bool rise = false;
+#pragma unroll
+                for (int b = 0; b < RB; ++b) {
+                    top[b] = kNone;
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) top[b] = fmaxf(top[b], x[g][b][r]);
+                    top[b] *= p.scale_log2;
+                    rise |= top[b] > m[b] + kRise;
+                }
+                if (__any(rise))
+#pragma unroll
+                    for (int b = 0; b < RB; ++b) {
+                        const float r = fmaxf(__builtin_ceilf(fmaxf(top[b], __shfl_xor(top[b], 32, 64))), m[b]);
+                        const float f = m[b] == r ? 1.f : __builtin_amdgcn_exp2f(m[b] - r);
+                        m[b] = r;
+                        sum[b] *= f;
+                        if (g > 0) {
+                            more[b] *= f;
+#pragma unroll
+                            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                                for (int k = 0; k < QP; ++k)
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) {
+                                        const uint32_t word = pf[0][b][t][k][i];  // a cast of the element itself reads the first one
+                                        const vb2 y = __builtin_bit_cast(vb2, word);
+                                        pf[0][b][t][k][i] = __builtin_bit_cast(
+                                            uint32_t, vb2{static_cast<__bf16>(static_cast<float>(y.x) * f), static_cast<__bf16>(static_cast<float>(y.y) * f)});
+                                    }
+                        }
+#pragma unroll
+                        for (int j = 0; j < kDt; ++j) o[b][j] *= f;
+                    }
+#pragma unroll
+                for (int b = 0; b < RB; ++b) ref[b] = m[b] == kNone ? 0.f : -m[b];
+            };
+
+            // the next tile's stores go beside the last of K's products, the loads of the one behind it beside the first of V's
+            const auto store_beside = [&](int f) {
+#pragma unroll
+                for (int i = S::kPieces * f / kC; i < S::kPieces * (f + 1) / kC; ++i) src.store(lds, next_buf, i);
+            };
+            const auto load_beside = [&](int v) {
+#pragma unroll
+                for (int i = S::kPieces * v / (2 * kDt); i < S::kPieces * (v + 1) / (2 * kDt); ++i) src.load(i);
+            };
+#pragma unroll
+            for (int f = 0; f < kC; ++f) {
+                key_product(f);
+                if constexpr (kSub == 1) store_beside(f);
+                stay<S::kOrdered>();
+            }
+#pragma unroll
+            for (int b = 0; b < RB; ++b) more[b] = 0.f;  // a tile's sum first by itself: one by one, small ones would be lost beside a large sum
+            settle(0);
+            if constexpr (kSub == 2) {
+                // a half's probabilities beside the other half's products
+#pragma unroll
+                for (int f = kC; f < 2 * kC; ++f) {
+                    key_product(f);
+                    exps(0, 8 * (f - kC) / kC, 8 * (f - kC + 1) / kC);
+                    store_beside(f - kC);
+                    stay<S::kOrdered>();
+                }
+                settle(1);
+            } else {
+                exps(0, 0, 4);
+            }
+            stored(next_buf, key0 + kKeys);
+            src.next_tile(p, s, key0 + 2 * kKeys, t + 2 < tiles);
+            share_barrier();
+#pragma unroll
+            for (int v = 0; v < kVs; ++v) {
+                value_product(v);
+                if (kSub == 2 && v < 2 * kDt) exps(1, 8 * v / (2 * kDt), 8 * (v + 1) / (2 * kDt));
+                if (kSub == 1 && v < kDt) exps(0, 4 + 4 * v / kDt, 4 + 4 * (v + 1) / kDt);
+                if (v < 2 * kDt) load_beside(v);
+                stay<S::kOrdered>();
+            }
+#pragma unroll
+            for (int b = 0; b < RB; ++b) sum[b] += more[b];
+            if (S::found(flag)) {
+                // infinities and NaN of V, zeros in the products, reach the rows that see their keys, and only those
+#pragma unroll 1
+                for (int i = 0; i < kKeys; ++i)
+#pragma unroll 1
+                    for (int c = 0; c < 16 * kDt; ++c)  // register c % 16 of o[c / 16]
+                        if (S::bad(flag, bads[buf], i, c / 16 * 32 + c % 16 / 4 * 8 + 4 * h + c % 4))
 #pragma unroll
                             for (int b = 0; b < RB; ++b)
-                                o[b][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[k], pf[b][t][i - k], o[b][j], 0, 0, 0);
-                        }
-                }
-            if (edge && __any(bad)) {
-                // they reach the rows that see their keys, and only those
-#pragma unroll 1
-                for (int t = 0; t < 32; ++t) {
-                    const int key = key0 + t;
-#pragma unroll
-                    for (int j = 0; j < kDt; ++j)
-#pragma unroll
-                        for (int r = 0; r < 16; ++r)
-                            if (src.v_bad(lds, buf, half, t, 32 * j + 8 * (r / 4) + 4 * h + r % 4))
-#pragma unroll
-                                for (int b = 0; b < RB; ++b)
-                                    if (key >= lo[b] && key < hi[b]) o[b][j][r] = __builtin_nanf("");
-                }
-            }
-        };
-
-        // Tile t is read from buffer t % 3, and written there two barriers after the tile before it there was read.
-        __syncthreads();  // the last item's tiles have been read
-        src.store(p, s, lds, flags[0], 0, base);
-        if (tiles > 1) src.load(p, s, base + kKeys);
-        int buf = 0, next_buf = 1;  // of tile t, and of the one that is stored
-#pragma unroll 1
-        for (int t = 0; t <= tiles; ++t) {
-            const int key0 = base + t * kKeys;
-            const int last_buf = buf == 0 ? 2 : buf - 1;
-            if (t < tiles) {
-                __syncthreads();
-                if (t + 1 < tiles) src.store(p, s, lds, flags[next_buf], next_buf, key0 + kKeys);
-                if (t + 2 < tiles) src.load(p, s, key0 + 2 * kKeys);
-                none_next = S::none(flags[buf], 0);
-                qk(next, buf, 0);
-            }
-            if (t > 0) pv(now, last_buf, kSub - 1, key0 - 32, on_edge(key0 - 32, none_now));
-            if (t == tiles) break;
-            if (on_edge(key0, none_next)) mask(next, key0, none_next);
-            refer(next);
-#pragma unroll
-            for (int b = 0; b < RB; ++b) now[b] = next[b];
-            none_now = none_next;
-            if constexpr (kSub == 2) {
-                none_next = S::none(flags[buf], 1);
-                qk(next, buf, 1);
-                pv(now, buf, 0, key0, on_edge(key0, none_now));
-                if (on_edge(key0 + 32, none_next)) mask(next, key0 + 32, none_next);
-                refer(next);
-#pragma unroll
-                for (int b = 0; b < RB; ++b) now[b] = next[b];
-                none_now = none_next;
+                                if (key0 + i >= lo[b] && key0 + i < hi[b]) bad[b] |= uint64_t(1) << c;
             }
             buf = next_buf;
             next_buf = next_buf == 2 ? 0 : next_buf + 1;
         }
+#pragma unroll
+        for (int b = 0; b < RB; ++b)
+            if (__any(bad[b] != 0))
+#pragma unroll
+                for (int c = 0; c < 16 * kDt; ++c)
+                    if (bad[b] >> c & 1) o[b][c / 16][c % 16] = __builtin_nanf("");
 
         const bool whole = a == 0 && z == count;
 #pragma unroll

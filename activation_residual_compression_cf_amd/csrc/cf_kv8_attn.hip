@@ -22,29 +22,37 @@ namespace cf {
 namespace {
 
 // Tiles of 64 keys of a cache, decoded: K as [key][D], V as [channel][64 keys] in runs of eight keys, which is how the
-// cache holds them.
-template <typename T, int D>
+// cache holds them.  A wave takes 16 or 8 keys of a tile, all of one page and scale.
+template <typename T, int D, int WAVES>
 struct Kv8Source {
     using Type = T;
     using Args = Attn8Args;
-    static constexpr int kDim = D;
+    static constexpr int kDim = D, kWaves = WAVES;
     static constexpr int kQueryParts = sizeof(T) == 4 ? 3 : 1, kKeyParts = 1;
     static constexpr int kKeys = 64;
     static constexpr int kPad = 5;
     static constexpr int kResident = 1;
     static constexpr int kPlane = kKeys * D * 2;
     static constexpr int kBytes = 2 * kPlane;
+    // a thread's share: codes of a key, and of eight keys of so many channels; in pieces of 16 or 8 bytes
+    static constexpr int kShare = D / WAVES, kChannels = kShare / 8, kPiece = kShare < 16 ? kShare : 16, kPieces = 2 * kShare / kPiece;
+    static constexpr int kGroup = 64 * WAVES, kMine = kKeys / WAVES, kLanes = 8 * WAVES;  // keys of a wave; lanes of eight keys
+    static constexpr int kBad = kGroup * kChannels;
+    static constexpr bool kOrdered = true;
 
-    int b, head, wave, page;  // page: of the wave's 16 keys of the tile to load next
-    uint32_t k_lane, v_lane;
-    uint32_t k[D / 16], v[D / 16];
+    int b, head, wave;
+    int pages;  // of the four runs of 16 keys of the tile to load next, in lanes 0 .. 3
+    uint32_t k_lane, v_lane, k_store, v_store[kChannels];
+    const uint8_t *k_at, *v_at, *k_scale, *v_scale;
+    vu2 r[kPieces][kPiece / 8];
     uint32_t ks, vs;
+    uint64_t keep;  // of V's eight keys: the sequence's
     bool on;
 
     static __device__ __forceinline__ __bf16 part(float* rest) { return take_bf16(rest); }
 
     // a channel's eight runs of eight keys lie turned: the 16 channels that a product's lanes read at once, and the
-    // four or two channels apart that are written at once, are on different banks
+    // channels that are written at once, are on different banks
     static __device__ constexpr uint32_t run(int c, int r) { return c * (2 * kKeys) + ((r ^ ((c >> 1 & 7) ^ (c >> 4 & 1))) << 4); }
 
     __device__ __forceinline__ void begin(const Attn8Args&) {
@@ -52,49 +60,94 @@ struct Kv8Source {
         wave = uniform(static_cast<int>(threadIdx.x) >> 6);
         k_lane = KeyRows<D>::chunk(KeyRows<D>::key_of(n), h);
         v_lane = run(n, h);
+        k_store = KeyRows<D>::chunk(kMine * wave + lane / WAVES, lane % WAVES * kChannels);
+#pragma unroll
+        for (int i = 0; i < kChannels; ++i) v_store[i] = run(lane % kLanes * kChannels + i, kMine / 8 * wave + lane / kLanes);
     }
-    __device__ __forceinline__ void item(const Attn8Args&, const Seq&, int seq, int kv_head) { b = seq, head = kv_head; }
-    __device__ __forceinline__ void load(const Attn8Args& p, const Seq& s, int key0) {
-        const int lane = threadIdx.x & 63, key = key0 + 16 * wave;
-        // keys behind the last are read from its page (and masked later): always inside the cache
+    // Lanes ask for a tile's four pages, and a wave takes its own: a scalar load, which shares its counter with shared
+    // memory, would be waited for at the next barrier.  Keys behind the last are read from its page (and masked later):
+    // always inside the cache.
+    __device__ __forceinline__ int page_at(const Attn8Args& p, const Seq& s, int key0) const {
+        const int key = key0 + 16 * static_cast<int>(threadIdx.x & 3);
         const int64_t at = int64_t(b) * p.width + (min(key, max(s.len - 1, 0)) >> p.cache.shift);
-        const int page = p.table ? scalar_load(p.table + at) : static_cast<int>(at);  // at < pages < 2^31 without a table
+        return p.table ? p.table[at] : static_cast<int>(at);  // at < pages < 2^31 without a table
+    }
+    __device__ __forceinline__ void item(const Attn8Args& p, const Seq& s, int seq, int kv_head, int key0) {
+        b = seq, head = kv_head;
+        pages = page_at(p, s, key0);
+    }
+    __device__ __forceinline__ void next_tile(const Attn8Args& p, const Seq& s, int key0, bool) {
+        const int lane = threadIdx.x & 63, key = key0 + kMine * wave;
+        const int page = __builtin_amdgcn_readlane(pages, kMine * wave / 16);
+        pages = page_at(p, s, key0 + kKeys);
         on = page_on(p, s, page);
         const uint8_t* const base = p.cache.at(on ? page : 0, head);
         const Kv8Block blk{p.cache.block.page, D};
         const int in = key & (blk.page - 1);
-        const uint8_t* const kc = base + blk.k_code(in + lane / 4) + (lane & 3) * (D / 4);
-        const uint8_t* const vc = base + blk.v_code(in + 8 * (lane >> 5), (lane & 31) * (D / 32));
-#pragma unroll
-        for (int i = 0; i < D / 16; i += 4) {
-            const vu4 x = *reinterpret_cast<const vu4*>(kc + 4 * i), y = *reinterpret_cast<const vu4*>(vc + 4 * i);
-            k[i] = x.x, k[i + 1] = x.y, k[i + 2] = x.z, k[i + 3] = x.w;
-            v[i] = y.x, v[i + 1] = y.y, v[i + 2] = y.z, v[i + 3] = y.w;
-        }
-        ks = base[blk.k_scale(in)], vs = base[blk.v_scale(in)];
+        k_at = base + blk.k_code(in + lane / WAVES) + lane % WAVES * kShare;
+        v_at = base + blk.v_code(in + 8 * (lane / kLanes), lane % kLanes * kChannels);
+        k_scale = base + blk.k_scale(in), v_scale = base + blk.v_scale(in);
+        // V behind the sequence's last key is whatever an earlier owner of the page left
+        const int valid = on ? min(max(s.len - key - 8 * (lane / kLanes), 0), 8) : 0;
+        keep = valid == 8 ? ~uint64_t(0) : (uint64_t(1) << (8 * valid)) - 1;
     }
-    __device__ __forceinline__ void store(const Attn8Args&, const Seq& s, uint8_t* lds, uint8_t* flag, int buf, int key0) {
-        const int lane = threadIdx.x & 63, oct = 8 * (lane >> 5), key = 16 * wave + lane / 4;
-        if (lane == 0) flag[wave] = on ? 0 : 1;
-        if (!on || s.len - key0 < 16 * wave + 16) {
-            // V behind the sequence's last key is whatever an earlier owner of the page left
-            const int valid = on ? min(max(s.len - key0 - 16 * wave - oct, 0), 8) : 0;
-            const uint64_t keep = valid == 8 ? ~uint64_t(0) : (uint64_t(1) << (8 * valid)) - 1;
-            if (valid == 0) vs = 127u;
+    __device__ __forceinline__ void load(int i) {
+        typedef uint32_t Piece __attribute__((ext_vector_type(kPiece / 4)));
+        const Piece x = *reinterpret_cast<const Piece*>(i < kPieces / 2 ? k_at + kPiece * i : v_at + kPiece * (i - kPieces / 2));
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) v[i] &= static_cast<uint32_t>(i & 1 ? keep >> 32 : keep);
-        }
+        for (int j = 0; j < kPiece / 8; ++j) r[i][j] = vu2{x[2 * j], x[2 * j + 1]};
+        if (i == 0) ks = *k_scale, vs = *v_scale;
+    }
+    __device__ __forceinline__ void store(uint8_t* lds, int buf, int i) {
         uint8_t* const at = lds + buf * kBytes;
-        const float kf = scale_of(ks), vf = scale_of(vs);
+        const bool is_k = i < kPieces / 2;
+        const float f = is_k ? scale_of(ks) : keep ? scale_of(vs) : 1.f;
+        const uint32_t lo = static_cast<uint32_t>(keep), hi = static_cast<uint32_t>(keep >> 32);
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-            *reinterpret_cast<vb8*>(at + KeyRows<D>::chunk(key, (lane & 3) * (D / 32) + i)) = bf16_codes(k[2 * i], k[2 * i + 1], kf);
-            *reinterpret_cast<vb8*>(at + kPlane + run((lane & 31) * (D / 32) + i, 2 * wave + (lane >> 5))) =
-                bf16_codes(v[2 * i], v[2 * i + 1], vf);
+        for (int j = 0; j < kPiece / 8; ++j) {
+            const int c = (is_k ? i : i - kPieces / 2) * (kPiece / 8) + j;
+            if (is_k)  // chunks of a key are turned by exclusive or
+                *reinterpret_cast<vb8*>(at + (k_store ^ 16 * c)) = bf16_codes(r[i][j].x, r[i][j].y, f);
+            else
+                *reinterpret_cast<vb8*>(at + kPlane + v_store[c]) = bf16_codes(r[i][j].x & lo, r[i][j].y & hi, f);
         }
     }
-    static __device__ __forceinline__ uint32_t none(const uint8_t* flag, int half) {
-        return uniform(static_cast<int>(flag[2 * half] | flag[2 * half + 1] << 1));
+    // As for rows (cf_attn.hip): a byte for eight keys of a channel.
+    __device__ __forceinline__ void stored(const Attn8Args&, const Seq&, uint8_t* flag, uint8_t* bads, uint8_t* lds, int buf, bool part) {
+        uint32_t any = 0;
+        if (part) {
+            const uint32_t lo = static_cast<uint32_t>(keep), hi = static_cast<uint32_t>(keep >> 32);
+#pragma unroll
+            for (int i = kPieces / 2; i < kPieces; ++i)
+#pragma unroll
+                for (int j = 0; j < kPiece / 8; ++j) any |= nan_codes(r[i][j].x & lo) | nan_codes(r[i][j].y & hi);
+            any = __any(any != 0) ? 2 : 0;
+            if (any)
+#pragma unroll
+                for (int i = kPieces / 2; i < kPieces; ++i) {
+#pragma unroll
+                    for (int j = 0; j < kPiece / 8; ++j) {
+                        const uint32_t x = nan_codes(r[i][j].x & lo), y = nan_codes(r[i][j].y & hi);
+                        bads[((i - kPieces / 2) * (kPiece / 8) + j) * kGroup + threadIdx.x] = static_cast<uint8_t>(four_bits(x) | four_bits(y) << 4);
+                        r[i][j].x &= ~full_bytes(x), r[i][j].y &= ~full_bytes(y);
+                    }
+                    store(lds, buf, i);
+                }
+        }
+        if ((threadIdx.x & 63) == 0) flag[wave] = static_cast<uint8_t>(any | (on ? 0 : 1));
+    }
+    // 16 keys without a page, a bit each
+    static __device__ __forceinline__ uint32_t none(FlagWord flag) {
+        uint32_t x = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x |= static_cast<uint32_t>(flag >> (8 * (16 * i / kMine)) & 1) << i;
+        return x;
+    }
+    static __device__ __forceinline__ bool found(FlagWord flag) { return (flag & 0x0202020202020202u) != 0; }
+    // whether a channel of a key of a tile is NaN
+    static __device__ __forceinline__ bool bad(FlagWord flag, const uint8_t* bads, int key, int c) {
+        const int of = key / kMine, lane = key % kMine / 8 * kLanes + c / kChannels;
+        return (flag >> (8 * of) & 2u) && (bads[c % kChannels * kGroup + of * 64 + lane] >> (key & 7) & 1u);
     }
     __device__ __forceinline__ vb8 k_frag(const uint8_t* lds, int buf, int half, int, int c) const {
         return *reinterpret_cast<const vb8*>(lds + buf * kBytes + (k_lane ^ 32 * c) + half * 64 * D);
@@ -103,10 +156,6 @@ struct Kv8Source {
         // run 4 half + 2 t + h of channel 32 j + n: 32 j turns as 0 does
         return *reinterpret_cast<const vb8*>(lds + buf * kBytes + kPlane + (v_lane ^ 16 * (4 * half + 2 * t)) + j * 64 * kKeys);
     }
-    __device__ __forceinline__ bool v_bad(const uint8_t* lds, int buf, int half, int t, int c) const {
-        const uint16_t x = *reinterpret_cast<const uint16_t*>(lds + buf * kBytes + kPlane + run(c, 4 * half + t / 8) + t % 8 * 2);
-        return (x & 0x7f80u) == 0x7f80u;
-    }
 };
 
 // Calls f with the kernel's shape and the kernel for a call whose longest sequence has max_rows rows.
@@ -114,7 +163,7 @@ template <typename T, int D, typename F>
 auto with_kernel(int64_t max_rows, F f) {
     if (max_rows <= 16) return f(Few8<T, D, 1>(), few8_kernel<T, D, 1>);
     if (max_rows <= 32) return f(Few8<T, D, 2>(), few8_kernel<T, D, 2>);
-    using K = Tile<Kv8Source<T, D>, 1>;
+    using K = Tile<Kv8Source<T, D, sizeof(T) == 2 ? 8 : 4>, 1>;
     return f(K(), tile_kernel<K>);
 }
 
@@ -154,7 +203,7 @@ hipError_t launch_kv8_attention(int a_dtype, const Kv8Attention& c, void* worksp
         p.groups = plan_of<S>(c.cache.block.dim).groups;
         p.joins = static_cast<int32_t*>(workspace);
         p.part = reinterpret_cast<float*>(p.joins + kJoin * p.groups);
-        kernel<<<p.groups, kThreads, 0, stream>>>(p);
+        kernel<<<p.groups, S::kGroup, 0, stream>>>(p);
         if (hipError_t e = hipGetLastError()) return e;
         return launch_join<S>(p, max_rows, stream);
     });

@@ -89,6 +89,7 @@ struct Few8 {
     static constexpr int kParts = sizeof(T) == 4 ? 3 : 1;  // bf16 parts of a query
     static constexpr int kP = Prob<T>::kParts;             // parts of a probability
     static constexpr int kRows = 16 * NQ;
+    static constexpr int kGroup = kThreads;
     static constexpr int kPad = 12;
     static constexpr int kResident = NQ == 2 ? (D == 128 ? 1 : 2) : D == 64 ? 3 : 2;  // workgroups of a compute unit, by their registers
 };
