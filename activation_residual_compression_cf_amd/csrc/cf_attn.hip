@@ -61,7 +61,7 @@ struct RowSource {
     static constexpr int kDim = D;
     static constexpr int kQueryParts = sizeof(T) == 4 ? 3 : 1, kKeyParts = kQueryParts;
     static constexpr int kKeys = sizeof(T) == 4 ? 32 : 64;
-    static constexpr int kPad = 4;
+    static constexpr int kPad = 6, kLeast = 6;  // what an item costs besides its units, and the shortest run
     // workgroups of a compute unit, by their registers and shared memory
     static constexpr int kResident = sizeof(T) == 2 && D == 64 && WAVES == 4 ? 3 : 1;
     static constexpr int kPlane = kKeys * D * 2;

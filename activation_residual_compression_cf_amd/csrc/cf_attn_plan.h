@@ -21,8 +21,6 @@ constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kUnit = 32;  // keys
 constexpr int kUnitsOfGpu = 256;  // compute units
-// A workgroup takes at least so many units, or joining would cost more than it saves.
-constexpr int kMinUnits = 8;
 // p = 2^(x - m + kLift) where m is at most kSlack below the row's largest score so far: the
 // reference moves, and O is rescaled, only when a score exceeds it by more.  p stays below
 // 2^(kLift + kSlack) < 65504, and the lift keeps the fp16 of small p off the subnormals.
@@ -182,7 +180,8 @@ struct Place {
 };
 
 // Every wave works it out by itself: a group of lanes takes a sequence and shares its tiles.
-template <int ROWS, int UNIT, int PAD, typename P>
+// LEAST: the shortest run.
+template <int ROWS, int UNIT, int PAD, int LEAST, typename P>
 __device__ __forceinline__ bool place_of(const P& p, Place* x) {
     const int lane = threadIdx.x & 63;
     int sub = 64;  // lanes of a sequence
@@ -209,7 +208,7 @@ __device__ __forceinline__ bool place_of(const P& p, Place* x) {
         total += uniform(shfl64(sum, 63));
     }
     int64_t chunk = (total + p.groups - 1) / p.groups;
-    chunk = max(chunk, int64_t(kMinUnits * kUnit / UNIT + PAD));
+    chunk = max(chunk, int64_t(LEAST));
     x->chunk = chunk;
     // Workgroups are dealt to the eight XCDs in turn.  Neighbours in the order of the work share keys:
     // each XCD takes an eighth of the runs there are, side by side, and so one part of L2's keys.

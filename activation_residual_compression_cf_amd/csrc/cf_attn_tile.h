@@ -88,7 +88,7 @@ __global__ __launch_bounds__(K::kGroup, K::kResident * K::Source::kWaves / 4) vo
     __shared__ uint8_t bads[K::kBuffers][S::kBad];
 
     Place w;
-    const bool work = place_of<kRows, kKeys, kPad>(p, &w);
+    const bool work = place_of<kRows, kKeys, kPad, S::kLeast>(p, &w);
     const int me = w.me;
     if (threadIdx.x == 0) p.joins[me * kJoin] = -1;
     if (!work) return;

@@ -132,7 +132,7 @@ __global__ __launch_bounds__(kThreads, (Few<T, D, NQ>::kResident)) void few_kern
     __shared__ float stage[kWaves * 16 * (D + 4)], stage_m[kWaves * 16], stage_l[kWaves * 16];
 
     Place w;
-    const bool work = place_of<kRows, kUnit, kPad>(p, &w);
+    const bool work = place_of<kRows, kUnit, kPad, kMinUnits + kPad>(p, &w);
     const int me = w.me;
     if (threadIdx.x == 0) p.joins[me * kJoin] = -1;
     if (!work) return;

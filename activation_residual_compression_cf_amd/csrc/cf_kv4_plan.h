@@ -9,6 +9,9 @@ namespace {
 
 using AttnArgs = PagedArgs<KvCache>;
 
+// A workgroup takes at least so many units of 32 keys, or joining would cost more than it saves.
+constexpr int kMinUnits = 8;
+
 // bf16 pair of byte B of codes c.
 template <int B>
 __device__ __forceinline__ uint32_t to_bf16(uint32_t c, float s) {

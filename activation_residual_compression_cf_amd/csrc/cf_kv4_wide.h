@@ -190,7 +190,7 @@ __global__ __launch_bounds__(kThreads, (Wide<T, D>::kResident)) void wide_kernel
     __shared__ uint8_t k_nan[2][kKeys * 4], v_nan[2][kKeys * kDt];
 
     Place w;
-    const bool work = place_of<kRows, kKeys, kPad>(p, &w);
+    const bool work = place_of<kRows, kKeys, kPad, kMinUnits * kUnit / kKeys + kPad>(p, &w);
     const int me = w.me;
     if (threadIdx.x == 0) p.joins[me * kJoin] = -1;
     if (!work) return;

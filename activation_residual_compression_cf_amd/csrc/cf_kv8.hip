@@ -85,18 +85,40 @@ __device__ __forceinline__ vf2 decode2(uint32_t c, float scale) {
     return __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c, scale, HIGH);
 }
 
-// The sequence of a token of the call: the last whose first token is not behind it.
+// The last sequence whose first token is not behind t, the same in every lane: 64 of them are looked at at a time.
 __device__ __forceinline__ int sequence_of(const AppendArgs& p, int t) {
     if (!p.starts) return t / p.each;
-    int lo = 0, hi = p.batch;  // starts[lo] <= t, or lo = 0
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (p.starts[mid] <= t)
-            lo = mid;
-        else
-            hi = mid;
+    const int lane = threadIdx.x & 63;
+    int first = 0;
+    for (int n = p.batch; n > 1;) {
+        const int step = (n + 63) / 64, i = lane * step;
+        const bool before = i < n && p.starts[first + min(i, n - 1)] <= t;
+        const int many = static_cast<int>(__popcll(__ballot(before)));
+        const int at = many > 0 ? (many - 1) * step : 0;
+        first += at;
+        n = min(step, n - at);
     }
-    return lo;
+    return first;
+}
+
+// The same for the token of each lane, t0 + lane: the sequences behind b, which is t0's, begin with some of them.
+template <int TILE>
+__device__ __forceinline__ int sequence_from(const AppendArgs& p, int b, int t0) {
+    const int lane = threadIdx.x & 63;
+    if (!p.starts) return (t0 + lane) / p.each;
+    if constexpr (TILE == 1) return b;
+    const bool there = b + 1 + lane < p.batch;
+    const int start = p.starts[there ? b + 1 + lane : b];
+    int more = 0;
+#pragma unroll
+    for (int i = 0; i < TILE; ++i) {
+        const int n = static_cast<int>(__popcll(__ballot(there && start <= t0 + i)));
+        if (lane == i) more = n;
+    }
+    int of = b + more;
+    if (more == 64)  // empty ones, more than were looked at
+        while (of + 1 < p.batch && p.starts[of + 1] <= t0 + lane) ++of;
+    return of;
 }
 
 // A wave writes what a call has of one block (16 tokens of one head).  Lane (o, c) of 2 x 32 holds places 8 o ..
@@ -112,8 +134,8 @@ __global__ __launch_bounds__(kThreads) void append_kernel(const AppendArgs p) {
     const Kv8Block blk{p.cache.block.page, D};
     int place = 0, many = 0, page = -1;  // a first token's place in its page, the block's tokens in this call, the page
     const int mine = blockIdx.x * TILE + lane;
+    const int b = sequence_from<TILE>(p, sequence_of(p, blockIdx.x * TILE), blockIdx.x * TILE);
     if (lane < TILE && mine < p.tokens) {
-        const int b = sequence_of(p, mine);
         const int lo = p.starts ? max(p.starts[b], 0) : b * p.each;
         const int hi = p.starts ? min(p.starts[b + 1], p.tokens) : (b + 1) * p.each;
         const int len = min(max(p.kv_lens[b], 0), p.width << p.cache.shift);

@@ -30,7 +30,7 @@ struct Kv8Source {
     static constexpr int kDim = D, kWaves = WAVES;
     static constexpr int kQueryParts = sizeof(T) == 4 ? 3 : 1, kKeyParts = 1;
     static constexpr int kKeys = 64;
-    static constexpr int kPad = 5;
+    static constexpr int kPad = 6, kLeast = 6;  // what an item costs besides its units, and the shortest run
     static constexpr int kResident = 1;
     static constexpr int kPlane = kKeys * D * 2;
     static constexpr int kBytes = 2 * kPlane;

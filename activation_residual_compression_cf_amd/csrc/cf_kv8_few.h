@@ -90,8 +90,12 @@ struct Few8 {
     static constexpr int kP = Prob<T>::kParts;             // parts of a probability
     static constexpr int kRows = 16 * NQ;
     static constexpr int kGroup = kThreads;
-    static constexpr int kPad = 12;
-    static constexpr int kResident = NQ == 2 ? (D == 128 ? 1 : 2) : D == 64 ? 3 : 2;  // workgroups of a compute unit, by their registers
+    // What an item costs besides its units, and the shortest run (one of 20 units takes 15.3 us for one token over 4097
+    // keys, of 12 13.9, of 8 13.4, of 4 14.7).
+    static constexpr int kPad = 12, kLeast = 8;
+    // workgroups of a compute unit, by their registers: 64 conversations of 0 to 32768 keys take 89 us with two, 137 with
+    // one and 105 with three, which spill
+    static constexpr int kResident = NQ == 2 ? (D == 128 ? 1 : 2) : D == 64 ? 3 : 2;
 };
 
 template <typename T, int D, int NQ>
@@ -104,7 +108,7 @@ __global__ __launch_bounds__(kThreads, (Few8<T, D, NQ>::kResident)) void few8_ke
     __shared__ float stage[kWaves * 16 * (D + 4)], stage_m[kWaves * 16], stage_l[kWaves * 16];
 
     Place w;
-    const bool work = place_of<kRows, kUnit, kPad>(p, &w);
+    const bool work = place_of<kRows, kUnit, kPad, S::kLeast>(p, &w);
     if (threadIdx.x == 0) p.joins[w.me * kJoin] = -1;
     if (!work) return;
     Seq s = seq_at(p, w.b);
@@ -149,10 +153,11 @@ __global__ __launch_bounds__(kThreads, (Few8<T, D, NQ>::kResident)) void few8_ke
         }
 
         vf4 o[NQ][kJ];
+        uint32_t bad[NQ];                // of the lane's values of O, a bit each: what a NaN of V has reached
         float m[NQ], sum[NQ], high[NQ];  // m: reference in units of log2, lowered by kLift
 #pragma unroll
         for (int i = 0; i < NQ; ++i) {
-            m[i] = high[i] = kNone, sum[i] = 0.f;
+            m[i] = high[i] = kNone, sum[i] = 0.f, bad[i] = 0;
 #pragma unroll
             for (int j = 0; j < kJ; ++j) o[i][j] = vf4{0.f, 0.f, 0.f, 0.f};
         }
@@ -165,8 +170,6 @@ __global__ __launch_bounds__(kThreads, (Few8<T, D, NQ>::kResident)) void few8_ke
             const int mine0 = key0 + 8 * g;  // the lane's own eight keys
             const bool ok = lane & 32 ? x.ok[1] : x.ok[0];
             const bool edge = key0 < full_lo || key0 + kUnit > full_hi || !x.ok[0] || !x.ok[1];
-            bool nans = false;        // codes of V that some rows see and some do not are NaN
-            uint32_t bad[D / 16];     // a byte for each key and channel: which
             if (edge) {
                 // V behind the sequence's last key is whatever an earlier owner of the page left
                 const int valid = ok ? min(max(s.len - mine0, 0), 8) : 0;
@@ -178,13 +181,26 @@ __global__ __launch_bounds__(kThreads, (Few8<T, D, NQ>::kResident)) void few8_ke
                     x.v[i] &= static_cast<uint32_t>(i & 1 ? keep >> 32 : keep);
                     any |= nan_codes(x.v[i]);
                 }
-                nans = __any(any != 0);
-                if (nans) {
+                if (__any(any != 0)) {
+                    // zeros in the products, and NaN of V reaches the rows that see its key, and only those
 #pragma unroll
-                    for (int c = 0; c < D / 16; ++c) {
-                        const uint32_t l = nan_codes(x.v[2 * c]), h = nan_codes(x.v[2 * c + 1]);
-                        x.v[2 * c] &= ~full_bytes(l), x.v[2 * c + 1] &= ~full_bytes(h);
-                        bad[c] = four_bits(l) | four_bits(h) << 4;
+                    for (int j = 0; j < kJ; ++j) {
+                        const uint32_t l = nan_codes(x.v[2 * j]), h = nan_codes(x.v[2 * j + 1]);
+                        x.v[2 * j] &= ~full_bytes(l), x.v[2 * j + 1] &= ~full_bytes(h);
+                        const int mine = static_cast<int>(four_bits(l) | four_bits(h) << 4);
+#pragma unroll 1
+                        for (int k = 0; k < 16; ++k) {
+                            const int hit = __shfl(mine, 16 * (k >> 2) + 4 * g + (k & 3), 64);  // row 4 g + k % 4 of the tile, keys 8 (k / 4) ..
+#pragma unroll
+                            for (int i = 0; i < NQ; ++i) {
+                                uint32_t see = 0;
+                                for (int t = 0; t < 8; ++t) {
+                                    const int key = key0 + 8 * (k >> 2) + t;
+                                    see |= static_cast<uint32_t>(key >= lo[i] && key < hi[i]) << t;
+                                }
+                                if (hit & see) bad[i] |= 1u << (4 * j + (k & 3));
+                            }
+                        }
                     }
                 }
             }
@@ -216,11 +232,10 @@ __global__ __launch_bounds__(kThreads, (Few8<T, D, NQ>::kResident)) void few8_ke
                 float x2[8];  // scores in units of log2
 #pragma unroll
                 for (int t = 0; t < 8; ++t) x2[t] = sc[i][t >> 2][t & 3] * p.scale_log2;
-                uint32_t see = 0xff;
                 if (edge) {
 #pragma unroll
                     for (int t = 0; t < 8; ++t)
-                        if (!ok || mine0 + t < lo[i] || mine0 + t >= hi[i]) x2[t] = kNone, see &= ~(1u << t);
+                        if (!ok || mine0 + t < lo[i] || mine0 + t >= hi[i]) x2[t] = kNone;
                 }
                 float top = kNone;
 #pragma unroll
@@ -249,19 +264,6 @@ __global__ __launch_bounds__(kThreads, (Few8<T, D, NQ>::kResident)) void few8_ke
                     Prob<T>::set(pf[i], t, x2[t]);
                 }
                 sum[i] += more;
-                if (nans) {
-                    // a NaN of V reaches the rows that see its key, and only those
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint32_t seen = __shfl(static_cast<int>(see), 16 * k + n, 64);
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-#pragma unroll
-                            for (int j = 0; j < kJ; ++j)
-                                if (static_cast<uint32_t>(__shfl(static_cast<int>(bad[j]), 16 * k + 4 * g + r, 64)) & seen)
-                                    o[i][j][r] = __builtin_nanf("");
-                    }
-                }
             }
 
             const float vs = scale_of(x.vs);
@@ -275,6 +277,14 @@ __global__ __launch_bounds__(kThreads, (Few8<T, D, NQ>::kResident)) void few8_ke
             }
         }
 
+#pragma unroll
+        for (int i = 0; i < NQ; ++i)
+            if (__any(bad[i] != 0))
+#pragma unroll
+                for (int j = 0; j < kJ; ++j)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (bad[i] >> (4 * j + r) & 1u) o[i][j][r] = __builtin_nanf("");
         finish_few<T, D, NQ>(p, w, s, a, z, count, o, m, sum, high, stage, stage_m, stage_l, [&](int i, int c) {
             return o[i][2 * (c >> 3) + (c & 1)][c >> 1 & 3];
         });
