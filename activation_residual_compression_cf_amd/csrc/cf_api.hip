@@ -6,12 +6,29 @@
 
 #include <hip/hip_runtime.h>
 
+#include <atomic>
+#include <chrono>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
 
 #include "cf.h"
 #include "cf_internal.h"
+
+namespace cf {
+
+uint64_t call_number() {
+    static std::atomic<uint64_t> next{static_cast<uint64_t>(std::chrono::system_clock::now().time_since_epoch().count()) ^
+                                      reinterpret_cast<uintptr_t>(&next)};
+    // a mixing of all 64 bits that can be undone: different counts, different numbers
+    uint64_t x = next.fetch_add(1, std::memory_order_relaxed);
+    x ^= x >> 32, x *= 0x9e3779b97f4a7c15u;
+    x ^= x >> 29, x *= 0xd1342543de82ef95u;
+    x ^= x >> 32;
+    return x == 0 ? 1 : x;  // 0: of the count 0
+}
+
+}  // namespace cf
 
 namespace {
 

@@ -45,6 +45,8 @@ struct AttnRows {
     float* lse;
     float* part;    // partial O, m and sum
     int32_t* joins; // what each workgroup leaves to be joined, kJoin numbers each
+    uint64_t* marks; // in their place, where the kernel joins by itself: one of each workgroup
+    uint64_t call;   // what a mark says, this call's own number
     int groups;
 };
 

@@ -3,7 +3,7 @@
 // cache's pages).
 #pragma once
 
-#include "cf_attn_plan.h"
+#include "cf_attn_join.h"
 
 namespace cf {
 namespace {
@@ -27,6 +27,7 @@ struct Tile {
     static constexpr int kPad = SRC::kPad;
     static constexpr int kResident = SRC::kResident;
     static constexpr int kBuffers = 3;
+    static constexpr bool kJoins = true;  // by itself
 };
 
 // The reference follows a row's largest score when that has risen by more than 2^kRise.
@@ -89,8 +90,6 @@ __global__ __launch_bounds__(K::kGroup, K::kResident * K::Source::kWaves / 4) vo
 
     Place w;
     const bool work = place_of<kRows, kKeys, kPad, S::kLeast>(p, &w);
-    const int me = w.me;
-    if (threadIdx.x == 0) p.joins[me * kJoin] = -1;
     if (!work) return;
     Seq s = seq_at(p, w.b);
     S src;
@@ -367,46 +366,73 @@ __global__ __launch_bounds__(K::kGroup, K::kResident * K::Source::kWaves / 4) vo
                 for (int c = 0; c < 16 * kDt; ++c)
                     if (bad[b] >> c & 1) o[b][c / 16][c % 16] = __builtin_nanf("");
 
+        float l[RB];
+#pragma unroll
+        for (int b = 0; b < RB; ++b) l[b] = sum[b] + __shfl_xor(sum[b], 32, 64);
+        // A part: a wave's values in its own order, side by side over the lanes, and behind all waves' each row's m and l.
+        const auto part_at = [&](int64_t slot, int b) {
+            return p.part + slot * part_floats<D>(kRows) + int64_t(wave * RB + b) * (32 * D) + 2 * lane;
+        };
+        const auto row_at = [&](int64_t slot, int b) {
+            return p.part + slot * part_floats<D>(kRows) + kRows * D + 2 * ((wave * RB + b) * 32 + n);
+        };
         const bool whole = a == 0 && z == count;
+        const bool mine = whole || join_parts(p, w, z, count,
+            [&](int64_t slot) {
 #pragma unroll
-        for (int b = 0; b < RB; ++b) {
-            const float l = sum[b] + __shfl_xor(sum[b], 32, 64);
-            const int row = row0 + 32 * b + n;
-            if (row >= rows) continue;
-            const int token = token_of(p, row), q_head = w.head * p.share + row - token * p.share;
-            const float inv = l == 0.f ? 0.f : 1.f / l;
-            T* const dst = row_ptr<T>(p.out, s.q0 + token, q_head);
-            float* const y = p.part + (2 * int64_t(me) + (a == 0)) * part_floats<D>(kRows) + int64_t(row - w.tile * kRows) * (D + 2);
-            // registers 4 k .. are channels 8 k + 4 h ..
+                for (int b = 0; b < RB; ++b) {
+                    if (row0 + 32 * b >= rows) continue;
+                    float* const y = part_at(slot, b);
 #pragma unroll
-            for (int j = 0; j < kDt; ++j)
+                    for (int i = 0; i < 8 * kDt; ++i) store_far(y + 128 * i, o[b][i / 8][2 * (i % 8)], o[b][i / 8][2 * (i % 8) + 1]);
+                    if (h == 0) store_far(row_at(slot, b), m[b], l[b]);
+                }
+            },
+            [&](int64_t slot) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int c = 32 * j + 8 * k + 4 * h;
-                    const vf4 x{o[b][j][4 * k], o[b][j][4 * k + 1], o[b][j][4 * k + 2], o[b][j][4 * k + 3]};
-                    if (!whole) {
-                        *reinterpret_cast<float2*>(y + c) = float2{x[0], x[1]};
-                        *reinterpret_cast<float2*>(y + c + 2) = float2{x[2], x[3]};
-                    } else if constexpr (sizeof(T) == 4) {
-                        *reinterpret_cast<vf4*>(dst + c) = x * inv;
-                    } else {
-                        typedef __bf16 vb4 __attribute__((ext_vector_type(4)));
-                        *reinterpret_cast<vb4*>(dst + c) = __builtin_convertvector(x * inv, vb4);
+                for (int b = 0; b < RB; ++b) {
+                    if (row0 + 32 * b >= rows) continue;
+                    const float* const y = part_at(slot, b);
+                    float2 x[8 * kDt];
+                    const float2 ml = load_far(row_at(slot, b));
+#pragma unroll
+                    for (int i = 0; i < 8 * kDt; ++i) x[i] = load_far(y + 128 * i);
+                    const float top = fmaxf(m[b], ml.x);
+                    // zeros of a part that saw nothing, or NaN that must show
+                    const float f = m[b] == kNone ? 0.f : __builtin_amdgcn_exp2f(m[b] - top), g = ml.x == kNone ? 0.f : __builtin_amdgcn_exp2f(ml.x - top);
+                    m[b] = top;
+                    l[b] = l[b] * f + ml.y * g;
+#pragma unroll
+                    for (int i = 0; i < 8 * kDt; ++i) {
+                        o[b][i / 8][2 * (i % 8)] = o[b][i / 8][2 * (i % 8)] * f + x[i].x * g;
+                        o[b][i / 8][2 * (i % 8) + 1] = o[b][i / 8][2 * (i % 8) + 1] * f + x[i].y * g;
                     }
                 }
-            if (h == 0) {
-                if (!whole)
-                    *reinterpret_cast<float2*>(y + D) = float2{m[b], l};
-                else if (p.lse)
-                    p.lse[int64_t(s.q0 + token) * p.q_heads + q_head] = lse_of(m[b], l);
+            });
+        if (mine)
+#pragma unroll
+            for (int b = 0; b < RB; ++b) {
+                const int row = row0 + 32 * b + n;
+                if (row >= rows) continue;
+                const int token = token_of(p, row), q_head = w.head * p.share + row - token * p.share;
+                const float inv = l[b] == 0.f ? 0.f : 1.f / l[b];
+                T* const dst = row_ptr<T>(p.out, s.q0 + token, q_head);
+                // registers 4 k .. are channels 8 k + 4 h ..
+#pragma unroll
+                for (int j = 0; j < kDt; ++j)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int c = 32 * j + 8 * k + 4 * h;
+                        const vf4 x{o[b][j][4 * k], o[b][j][4 * k + 1], o[b][j][4 * k + 2], o[b][j][4 * k + 3]};
+                        if constexpr (sizeof(T) == 4) {
+                            *reinterpret_cast<vf4*>(dst + c) = x * inv;
+                        } else {
+                            typedef __bf16 vb4 __attribute__((ext_vector_type(4)));
+                            *reinterpret_cast<vb4*>(dst + c) = __builtin_convertvector(x * inv, vb4);
+                        }
+                    }
+                if (h == 0 && p.lse) p.lse[int64_t(s.q0 + token) * p.q_heads + q_head] = lse_of(m[b], l[b]);
             }
-        }
-        if (threadIdx.x == 0 && a > 0 && z == count) {
-            int32_t* const j = p.joins + me * kJoin;
-            j[1] = w.head, j[2] = s.q0, j[3] = w.tile * kRows, j[4] = min(kRows, rows - w.tile * kRows);
-            // the workgroup with the item's first unit
-            j[0] = static_cast<int32_t>((w.at - count) / w.chunk);
-        }
 
         w.rest = 0;
         if (w.at >= w.end) break;

@@ -136,4 +136,7 @@ hipError_t launch_pages_compact(const PagesCall& call, void* workspace, hipStrea
 hipError_t launch_pages_copy(void* data, int64_t pages, int64_t page_bytes, int layers, int64_t layer_stride, const int32_t* src,
                              const int32_t* dst, int64_t n, const int32_t* count, hipStream_t stream);
 
+// A number that no other call of this process has, and hardly anything else that memory may hold; not 0.
+uint64_t call_number();
+
 }  // namespace cf

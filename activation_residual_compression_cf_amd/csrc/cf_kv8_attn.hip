@@ -15,6 +15,7 @@
 
 #include <cstdint>
 
+#include "cf_attn_join.h"
 #include "cf_attn_tile.h"
 #include "cf_kv8_few.h"
 
@@ -199,13 +200,7 @@ hipError_t launch_kv8_attention(int a_dtype, const Kv8Attention& c, void* worksp
     p.lse = c.lse;
     const int64_t max_rows = c.max_q * p.share;
     return with_kernel(a_dtype, c.cache.block.dim, max_rows, [&](auto shape, auto kernel) {
-        using S = decltype(shape);
-        p.groups = plan_of<S>(c.cache.block.dim).groups;
-        p.joins = static_cast<int32_t*>(workspace);
-        p.part = reinterpret_cast<float*>(p.joins + kJoin * p.groups);
-        kernel<<<p.groups, S::kGroup, 0, stream>>>(p);
-        if (hipError_t e = hipGetLastError()) return e;
-        return launch_join<S>(p, max_rows, stream);
+        return launch_attn<decltype(shape)>(p, kernel, max_rows, workspace, stream);
     });
 }
 

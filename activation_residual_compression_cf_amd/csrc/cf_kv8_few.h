@@ -90,6 +90,7 @@ struct Few8 {
     static constexpr int kP = Prob<T>::kParts;             // parts of a probability
     static constexpr int kRows = 16 * NQ;
     static constexpr int kGroup = kThreads;
+    static constexpr bool kJoins = false;  // by itself
     // What an item costs besides its units, and the shortest run (one of 20 units takes 15.3 us for one token over 4097
     // keys, of 12 13.9, of 8 13.4, of 4 14.7).
     static constexpr int kPad = 12, kLeast = 8;

@@ -87,6 +87,23 @@ def test_split_over_workgroups(cf, dev, dtype, nq, nk):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]), "two calls differ"
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("nq,nk", [(30, 900), (129, 1300), (200, 2700), (256, 16411)])
+def test_an_item_in_many_parts(cf, dev, dtype, dim, nq, nk):
+    """Whatever workgroup comes last, and whatever lies in the workspace, the bits are the same."""
+    say(f"attention of one item in parts {dtype} dim={dim} {nq} queries, {nk} keys")
+    c = Case(cf, dev, [nk], [nq], 1, 1, dim, dtype, seed=nk)
+    ws = torch.empty(cf.attention_workspace_bytes(DT[dtype], nq, 1, 1, dim), dtype=torch.uint8, device=dev)
+    want = c.run(max_q=nq, workspace=ws)
+    c.check(*want)
+    for i in range(20):
+        if i % 3 == 0:
+            ws.random_(0, 256)
+        got = c.run(max_q=nq, workspace=ws)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), f"call {i} differs"
+
+
 def test_peaked_rows(cf, dev):
     say("attention peaked rows")
     for dtype in ("bf16", "f32"):
