@@ -10,6 +10,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "cf.h"
 #include "cf_internal.h"
@@ -32,20 +33,40 @@ struct AppendArgs {
     const int32_t* starts;
 };
 
-// CH consecutive channels of a row.
+// CH consecutive channels of a row, as they lie there: half the registers of fp32, where they are bf16.
 template <typename T, int CH>
-__device__ __forceinline__ void load_few(const T* p, float (&x)[CH]) {
+struct Few {
     typedef T Vec __attribute__((ext_vector_type(CH)));
-    const Vec v = *reinterpret_cast<const Vec*>(p);
+    typedef uint32_t Words __attribute__((ext_vector_type(CH * sizeof(T) / 4)));
+    Words w;
+    __device__ __forceinline__ void load(const T* p) { w = __builtin_bit_cast(Words, *reinterpret_cast<const Vec*>(p)); }
+    __device__ __forceinline__ float operator[](int j) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[j]);
+        return __uint_as_float(j & 1 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
+    }
+    // the bit patterns of the largest magnitudes so far, whatever they are: one, or of bf16 two
+    __device__ __forceinline__ uint32_t largest(uint32_t top) const {
 #pragma unroll
-    for (int i = 0; i < CH; ++i) x[i] = static_cast<float>(v[i]);
-}
+        for (int i = 0; i < static_cast<int>(CH * sizeof(T) / 4); ++i) {
+            if constexpr (sizeof(T) == 2) {
+                typedef uint16_t Two __attribute__((ext_vector_type(2)));
+                const uint32_t word = w[i] & 0x7fff7fffu;
+                top = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(Two, word), __builtin_bit_cast(Two, top)));
+            } else {
+                top = max(top, w[i] & 0x7fffffffu);
+            }
+        }
+        return top;
+    }
+};
 
 // Bit pattern of the magnitude where it is finite.
 __device__ __forceinline__ uint32_t finite_bits(float x) {
     const uint32_t b = __float_as_uint(x) & 0x7fffffffu;
     return b < 0x7f800000u ? b : 0u;
 }
+
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(v))); }
 
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
 #pragma unroll
@@ -65,12 +86,17 @@ __device__ __forceinline__ int held_exponent(uint8_t byte) {
 
 __device__ __forceinline__ float two_to(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
+// The largest number of the largest scale.
+constexpr uint32_t kLargest = 0x47600000u;  // 448 * 2^kKv8ExpMax
+
 // Codes of two values in the low or high half of c.  The conversion divides by the scale and rounds to nearest
-// even; beyond 464 it would give NaN, which infinities are left to become.
-template <bool HIGH>
+// even; beyond 464 it would give NaN, which infinities are left to become.  CUT: there may be values
+// beyond 448 of the scale, or that are not finite.
+template <bool HIGH, bool CUT>
 __device__ __forceinline__ uint32_t encode2(uint32_t c, float a, float b, float scale) {
     const float lim = 448.f * scale;
     const auto cut = [&](float x) {
+        if constexpr (!CUT) return x;
         return (__float_as_uint(x) & 0x7fffffffu) < 0x7f800000u ? __builtin_amdgcn_fmed3f(x, -lim, lim) : __builtin_inff();
     };
     typedef short vs2 __attribute__((ext_vector_type(2)));
@@ -124,7 +150,11 @@ __device__ __forceinline__ int sequence_from(const AppendArgs& p, int b, int t0)
 // A wave writes what a call has of one block (16 tokens of one head).  Lane (o, c) of 2 x 32 holds places 8 o ..
 // 8 o + 7 of D/32 channels: V's codes are eight tokens of a channel together, so a lane has its bytes whole, and
 // K's leave in runs of a row.  TILE tokens of the call are looked through for first tokens of blocks, each by a
-// lane: 16, or one where a call has about a token of each sequence.
+// lane: 16, or one where a call has few tokens of each sequence.
+// Bound by instructions and by how many waves hide the loads of starts, lengths, pages and rows that follow each other:
+// rows kept as they came (94 registers for bf16 and D = 128, 119 with fp32 values) and no value cut off that need not be
+// took 9180 prompt tokens of 24 heads from 57 to 35 us (169 MB, 4.9 TB/s), one token each of 61 sequences from 6.9
+// to 5.7.  Slower: a loop over heads, which saves their lookups and takes registers (72 us).
 template <typename T, int D, int TILE>
 __global__ __launch_bounds__(kThreads) void append_kernel(const AppendArgs p) {
     constexpr int CH = D / 32;
@@ -154,31 +184,48 @@ __global__ __launch_bounds__(kThreads) void append_kernel(const AppendArgs p) {
         const int in = __builtin_amdgcn_readlane(place, lead), n = __builtin_amdgcn_readlane(many, lead);
         uint8_t* const base = p.cache.at(__builtin_amdgcn_readlane(page, lead), head);
         const int from = in & (kKv8Block - 1), first = in - from;  // the block's first place in the page
-        float x[2][8][CH];
-        uint32_t top[2] = {0, 0};
+        Few<T, CH> x[2][8];
+        uint32_t top[2] = {0, 0};  // bits of the largest magnitude
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int at = 8 * o + i - from;
-#pragma unroll
-            for (int j = 0; j < CH; ++j) x[0][i][j] = x[1][i][j] = 0.f;
+            x[0][i].w = x[1][i].w = 0;
             if (at >= 0 && at < n) {
-                load_few<T, CH>(row_ptr<T>(p.k, t0 + at, head) + c0, x[0][i]);
-                load_few<T, CH>(row_ptr<T>(p.v, t0 + at, head) + c0, x[1][i]);
+                x[0][i].load(row_ptr<T>(p.k, t0 + at, head) + c0);
+                x[1][i].load(row_ptr<T>(p.v, t0 + at, head) + c0);
             }
         }
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < 8; ++i) top[s] = x[s][i].largest(top[s]);
 #pragma unroll
-                for (int j = 0; j < CH; ++j) top[s] = max(top[s], finite_bits(x[s][i][j]));
+        for (int s = 0; s < 2; ++s) {
+            if constexpr (sizeof(T) == 2) top[s] = max(top[s] << 16, top[s] & 0xffff0000u);
+            top[s] = uniform(wave_max(top[s]));
+        }
+        // Of finite values up to the largest scale's none needs cutting off: a scale takes its largest value.  So nearly
+        // always; doing it for each value took two thirds of the kernel's instructions.
+        const bool cut = max(top[0], top[1]) > kLargest;
+        if (cut) {
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                if (top[s] < 0x7f800000u) continue;
+                top[s] = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+#pragma unroll
+                    for (int j = 0; j < CH; ++j) top[s] = max(top[s], finite_bits(x[s][i][j]));
+                top[s] = wave_max(top[s]);
+            }
+        }
         uint8_t* const scales[2] = {base + blk.k_scale(first), base + blk.v_scale(first)};
         int e[2];
         bool raise[2];
         float old[2];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            e[s] = exponent_of(wave_max(top[s]));
+            e[s] = exponent_of(top[s]);
             const int was = from ? held_exponent(*scales[s]) : e[s];
             raise[s] = was < e[s];
             e[s] = max(e[s], was);
@@ -188,52 +235,59 @@ __global__ __launch_bounds__(kThreads) void append_kernel(const AppendArgs p) {
         uint8_t* const kc = base + blk.k_code(first + 8 * o) + c0;
         uint8_t* const vc = base + blk.v_code(first + 8 * o, c0);
         const auto fresh = [&](int i) { return 8 * o + i >= from && 8 * o + i < from + n; };
+        const auto write = [&](auto cutting) {
+            constexpr bool kCut = decltype(cutting)::value;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            uint32_t c = encode2<false>(0, x[0][i][0], x[0][i][1], ks);
-            if constexpr (CH == 4) c = encode2<true>(c, x[0][i][2], x[0][i][3], ks);
-            if (!fresh(i)) {
-                if (!raise[0] || 8 * o + i >= from) continue;  // places behind the new ones hold nothing
-                if constexpr (CH == 4) {
-                    const uint32_t h = *reinterpret_cast<const uint32_t*>(kc + i * D);
-                    const vf2 a = decode2<false>(h, old[0]), b = decode2<true>(h, old[0]);
-                    c = encode2<true>(encode2<false>(0, a.x, a.y, ks), b.x, b.y, ks);
+            for (int i = 0; i < 8; ++i) {
+                uint32_t c = encode2<false, kCut>(0, x[0][i][0], x[0][i][1], ks);
+                if constexpr (CH == 4) c = encode2<true, kCut>(c, x[0][i][2], x[0][i][3], ks);
+                if (!fresh(i)) {
+                    if (!raise[0] || 8 * o + i >= from) continue;  // places behind the new ones hold nothing
+                    if constexpr (CH == 4) {
+                        const uint32_t h = *reinterpret_cast<const uint32_t*>(kc + i * D);
+                        const vf2 a = decode2<false>(h, old[0]), b = decode2<true>(h, old[0]);
+                        c = encode2<true, true>(encode2<false, true>(0, a.x, a.y, ks), b.x, b.y, ks);
+                    } else {
+                        const vf2 a = decode2<false>(*reinterpret_cast<const uint16_t*>(kc + i * D), old[0]);
+                        c = encode2<false, true>(0, a.x, a.y, ks);
+                    }
+                }
+                if constexpr (CH == 4)
+                    *reinterpret_cast<uint32_t*>(kc + i * D) = c;
+                else
+                    *reinterpret_cast<uint16_t*>(kc + i * D) = static_cast<uint16_t>(c);
+            }
+            const bool whole = from <= 8 * o && from + n >= 8 * o + 8;
+#pragma unroll
+            for (int j = 0; j < CH; ++j) {
+                vu2 c;
+                c.x = encode2<true, kCut>(encode2<false, kCut>(0, x[1][0][j], x[1][1][j], vs), x[1][2][j], x[1][3][j], vs);
+                c.y = encode2<true, kCut>(encode2<false, kCut>(0, x[1][4][j], x[1][5][j], vs), x[1][6][j], x[1][7][j], vs);
+                vu2* const to = reinterpret_cast<vu2*>(vc + 8 * j);
+                if (whole) {
+                    *to = c;
+                } else if (raise[1]) {
+                    vu2 h = *to;
+                    const vf2 a = decode2<false>(h.x, old[1]), b = decode2<true>(h.x, old[1]);
+                    const vf2 d = decode2<false>(h.y, old[1]), f = decode2<true>(h.y, old[1]);
+                    h.x = encode2<true, true>(encode2<false, true>(0, a.x, a.y, vs), b.x, b.y, vs);
+                    h.y = encode2<true, true>(encode2<false, true>(0, d.x, d.y, vs), f.x, f.y, vs);
+                    uint64_t keep = 0;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) keep |= fresh(i) ? 0 : uint64_t(0xff) << (8 * i);
+                    const uint64_t w = (__builtin_bit_cast(uint64_t, h) & keep) | (__builtin_bit_cast(uint64_t, c) & ~keep);
+                    *to = __builtin_bit_cast(vu2, w);
                 } else {
-                    const vf2 a = decode2<false>(*reinterpret_cast<const uint16_t*>(kc + i * D), old[0]);
-                    c = encode2<false>(0, a.x, a.y, ks);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (fresh(i)) vc[8 * j + i] = static_cast<uint8_t>((i < 4 ? c.x : c.y) >> (8 * (i & 3)));
                 }
             }
-            if constexpr (CH == 4)
-                *reinterpret_cast<uint32_t*>(kc + i * D) = c;
-            else
-                *reinterpret_cast<uint16_t*>(kc + i * D) = static_cast<uint16_t>(c);
-        }
-        const bool whole = from <= 8 * o && from + n >= 8 * o + 8;
-#pragma unroll
-        for (int j = 0; j < CH; ++j) {
-            vu2 c;
-            c.x = encode2<true>(encode2<false>(0, x[1][0][j], x[1][1][j], vs), x[1][2][j], x[1][3][j], vs);
-            c.y = encode2<true>(encode2<false>(0, x[1][4][j], x[1][5][j], vs), x[1][6][j], x[1][7][j], vs);
-            vu2* const to = reinterpret_cast<vu2*>(vc + 8 * j);
-            if (whole) {
-                *to = c;
-            } else if (raise[1]) {
-                vu2 h = *to;
-                const vf2 a = decode2<false>(h.x, old[1]), b = decode2<true>(h.x, old[1]);
-                const vf2 d = decode2<false>(h.y, old[1]), f = decode2<true>(h.y, old[1]);
-                h.x = encode2<true>(encode2<false>(0, a.x, a.y, vs), b.x, b.y, vs);
-                h.y = encode2<true>(encode2<false>(0, d.x, d.y, vs), f.x, f.y, vs);
-                uint64_t keep = 0;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) keep |= fresh(i) ? 0 : uint64_t(0xff) << (8 * i);
-                const uint64_t w = (__builtin_bit_cast(uint64_t, h) & keep) | (__builtin_bit_cast(uint64_t, c) & ~keep);
-                *to = __builtin_bit_cast(vu2, w);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (fresh(i)) vc[8 * j + i] = static_cast<uint8_t>((i < 4 ? c.x : c.y) >> (8 * (i & 3)));
-            }
-        }
+        };
+        if (cut)
+            write(std::true_type());
+        else
+            write(std::false_type());
         if (lane < 2) *(lane ? scales[1] : scales[0]) = static_cast<uint8_t>((lane ? e[1] : e[0]) + 127);
     }
 }
@@ -284,9 +338,10 @@ __global__ __launch_bounds__(kThreads) void read_kernel(const ReadArgs p) {
 template <typename T, int D>
 void launch_append(const AppendArgs& p, hipStream_t stream) {
     const uint32_t y = (p.cache.heads + kWaves - 1) / kWaves;
-    // with about a token of each sequence every token begins a block, and a wave each is the quickest (a dispatch
-    // counts its work-items in 32 bits)
-    if (p.tokens <= 2 * int64_t(p.batch) && p.tokens <= 1 << 22)
+    // A wave for each token finds one block or none; for each 16 tokens, those that begin there, one after the other.
+    // 64 sequences of 1 to 5 new tokens take 6.7 and 28 us, of 1 to 40 10.5 and 21, of 1 to 100 15 and 15.  (A dispatch
+    // counts its work-items in 32 bits.)
+    if (p.tokens <= kKv8Block * int64_t(p.batch) && p.tokens <= 1 << 22)
         append_kernel<T, D, 1><<<dim3(p.tokens, y), kThreads, 0, stream>>>(p);
     else
         append_kernel<T, D, 16><<<dim3((p.tokens + 15) / 16, y), kThreads, 0, stream>>>(p);
