@@ -511,14 +511,14 @@ def _flat(name: str, t: torch.Tensor | None, dev: int, dtype: torch.dtype, shape
     """Address of a contiguous tensor of this type and shape, None for None."""
     if t is None:
         return None
+    if t.dtype == dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype != dtype:
         raise TypeError(f"{name} is {t.dtype}; libcf wants {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} is {tuple(t.shape)}, the call needs {shape}")
     _here(name, t, dev)
-    if not t.is_contiguous():
-        raise ValueError("libcf needs contiguous tensors")
-    return t.data_ptr()
+    raise ValueError("libcf needs contiguous tensors")
 
 
 def _shaped(name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple):
@@ -903,7 +903,8 @@ def _pages_call(fn: str, have: PageTable, out: PageTable | None, workspace, stre
     if workspace is None:
         workspace = _new(have.table, max(need, 4) // 4, stream)
     ws = (_flat("workspace", workspace, dev, workspace.dtype, workspace.shape), workspace.numel() * workspace.element_size())
-    return have._pages("have", dev, shape), out._pages("out", dev, shape), out, shape, ws, dev, workspace
+    pin = have._pages("have", dev, shape)
+    return pin, pin if out is have else out._pages("out", dev, shape), out, shape, ws, dev, workspace
 
 
 def _words(like: torch.Tensor, n: int, t: torch.Tensor | None, name: str, dev: int, stream):
