@@ -252,53 +252,50 @@ __global__ __launch_bounds__(K::kGroup, K::kResident * K::Source::kWaves / 4) vo
                         }
                     }
             };
-            // masks new scores and moves the references to them: to whole numbers, so that what is moved with them stays as exact
-            const auto settle = [&](int g) {
-                if (edge) {
+            // hides what rows do not see
+            const auto mask = [&](int g) {
+                if (!edge) return;
 #pragma unroll
-                    for (int b = 0; b < RB; ++b)
+                for (int b = 0; b < RB; ++b)
 #pragma unroll
-                        for (int r = 0; r < 16; ++r) {
-                            const int run = 2 * g + r / 8, key = key0 + 8 * h + 16 * run + r % 8;
-                            if ((S::none(flag) >> run & 1u) || key < lo[b] || key >= hi[b]) x[g][b][r] = kNone;
-                        }
+                    for (int r = 0; r < 16; ++r) {
+                        const int run = 2 * g + r / 8, key = key0 + 8 * h + 16 * run + r % 8;
+                        if ((S::none(flag) >> run & 1u) || key < lo[b] || key >= hi[b]) x[g][b][r] = kNone;
+                    }
+            };
+            float top[RB];
+            const auto most = [&](int g, int r0, int r1) {
+#pragma unroll
+                for (int b = 0; b < RB; ++b) {
+#pragma unroll
+                    for (int r = r0; r < r1; ++r) top[b] = fmaxf(top[b], x[g][b][r]);
+                    here(top[b]);
                 }
-                float top[RB];
+            };
+            // Moves the references to the new scores, where those have risen: to whole numbers, so that what is moved with them
+            // stays as exact.  A tile's first half has its probabilities by then, from the old reference: nearly always
+            // that holds, and nothing waits for a decision between the two products.  Else they are made again.
+            const auto settle = [&](bool made) {
                 bool rise = false;
 #pragma unroll
                 for (int b = 0; b < RB; ++b) {
-                    top[b] = kNone;
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) top[b] = fmaxf(top[b], x[g][b][r]);
                     top[b] *= p.scale_log2;
                     rise |= top[b] > m[b] + kRise;
                 }
-                if (__any(rise))
+                if (__any(rise)) {
 #pragma unroll
                     for (int b = 0; b < RB; ++b) {
                         const float r = fmaxf(__builtin_ceilf(fmaxf(top[b], __shfl_xor(top[b], 32, 64))), m[b]);
                         const float f = m[b] == r ? 1.f : __builtin_amdgcn_exp2f(m[b] - r);
                         m[b] = r;
                         sum[b] *= f;
-                        if (g > 0) {
-                            more[b] *= f;
-#pragma unroll
-                            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                                for (int k = 0; k < QP; ++k)
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i) {
-                                        const uint32_t word = pf[0][b][t][k][i];  // a cast of the element itself reads the first one
-                                        const vb2 y = __builtin_bit_cast(vb2, word);
-                                        pf[0][b][t][k][i] = __builtin_bit_cast(
-                                            uint32_t, vb2{static_cast<__bf16>(static_cast<float>(y.x) * f), static_cast<__bf16>(static_cast<float>(y.y) * f)});
-                                    }
-                        }
+                        more[b] = 0.f;
 #pragma unroll
                         for (int j = 0; j < kDt; ++j) o[b][j] *= f;
+                        ref[b] = m[b] == kNone ? 0.f : -m[b];
                     }
-#pragma unroll
-                for (int b = 0; b < RB; ++b) ref[b] = m[b] == kNone ? 0.f : -m[b];
+                    if (made) exps(0, 0, 8);
+                }
             };
 
             // the next tile's stores go beside the last of K's products, the loads of the one behind it beside the first of V's
@@ -313,25 +310,34 @@ __global__ __launch_bounds__(K::kGroup, K::kResident * K::Source::kWaves / 4) vo
 #pragma unroll
             for (int f = 0; f < kC; ++f) {
                 key_product(f);
+                if (f == 0) __builtin_amdgcn_s_setprio(0);
                 if constexpr (kSub == 1) store_beside(f);
                 stay<S::kOrdered>();
             }
 #pragma unroll
-            for (int b = 0; b < RB; ++b) more[b] = 0.f;  // a tile's sum first by itself: one by one, small ones would be lost beside a large sum
-            settle(0);
+            for (int b = 0; b < RB; ++b) more[b] = 0.f, top[b] = kNone, ref[b] = m[b] == kNone ? 0.f : -m[b];
+            mask(0);
             if constexpr (kSub == 2) {
                 // a half's probabilities beside the other half's products
 #pragma unroll
                 for (int f = kC; f < 2 * kC; ++f) {
                     key_product(f);
                     exps(0, 8 * (f - kC) / kC, 8 * (f - kC + 1) / kC);
+                    most(0, 16 * (f - kC) / kC, 16 * (f - kC + 1) / kC);
                     store_beside(f - kC);
                     stay<S::kOrdered>();
                 }
-                settle(1);
+                mask(1);
+                most(1, 0, 16);
+                settle(true);
             } else {
+                most(0, 0, 16);
+                settle(false);
                 exps(0, 0, 4);
             }
+            // a wave in its second half goes before one in its first: the two of a SIMD drift apart, and one's vector work
+            // meets the other's products (1% of 16384 rows over 16384 keys)
+            __builtin_amdgcn_s_setprio(1);
             stored(next_buf, key0 + kKeys);
             src.next_tile(p, s, key0 + 2 * kKeys, t + 2 < tiles);
             share_barrier();
