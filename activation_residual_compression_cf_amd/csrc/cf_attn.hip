@@ -63,9 +63,9 @@ struct RowSource {
     static constexpr int kQueryParts = sizeof(T) == 4 ? 3 : 1, kKeyParts = kQueryParts;
     static constexpr int kKeys = sizeof(T) == 4 ? 32 : 64;
     static constexpr int kPad = 6, kLeast = 6;  // what an item costs besides its units, and the shortest run
-    // workgroups of a compute unit, by their registers and shared memory
-    // 64 tokens over 4000 keys each, of D = 64: 98 us with two, 150 with one, 110 with three, which spill
-    static constexpr int kResident = sizeof(T) == 2 && D == 64 && WAVES == 4 ? 2 : 1;
+    // Workgroups of a compute unit, by their registers and shared memory.  64 tokens over 4000 keys each, of D = 64: 98 us
+    // with two, 150 with one, 110 with three, which spill; 4096 fp32 rows over 4608 keys: 604 with two, 717 with one.
+    static constexpr int kResident = D == 64 && WAVES == 4 ? 2 : 1;
     static constexpr int kPlane = kKeys * D * 2;
     static constexpr int kBytes = 2 * kKeyParts * kPlane;
     // a thread's loads: 16 bytes of kPasses rows, kStep apart
