@@ -31,7 +31,7 @@ struct Kv8Source {
     static constexpr int kDim = D, kWaves = WAVES;
     static constexpr int kQueryParts = sizeof(T) == 4 ? 3 : 1, kKeyParts = 1;
     static constexpr int kKeys = 64;
-    static constexpr int kPad = 6, kLeast = 6;  // what an item costs besides its units, and the shortest run
+    static constexpr int kPad = 6, kLeast = 6;  // what an item costs besides its units, and the shortest run (as for rows)
     // workgroups of a compute unit: 1024 fp32 rows of D = 64 over 4608 keys take 102 us with two, 135 with one
     static constexpr int kResident = D == 64 && WAVES == 4 ? 2 : 1;
     static constexpr int kPlane = kKeys * D * 2;
