@@ -121,6 +121,25 @@ def test_ends_of_the_formats(cf, dev):
     s.check()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("new", [[16, 1, 0, 9], [40, 17, 0, 70]])
+def test_single_numbers_that_are_cut_off(cf, dev, dtype, dim, new):
+    """One value past the largest scale's last number, an infinity or NaN, in a call of few and of many tokens."""
+    say(f"kv8 append of large numbers {dtype} dim={dim} {new}")
+    rng = np.random.default_rng(dim)
+    s = Sequences(cf, dev, 4, 5, dim, 32, 8, seed=dim)
+    for big in (57344.0, -57344.0, 57856.0, 65536.0, -3e38, np.inf, -np.inf, np.nan, 1.0):
+        k, v = s.rows(new, dtype, rng, 2.0)
+        for x in (k, v):
+            x[rng.integers(len(x)), rng.integers(5), rng.integers(dim)] = big
+        s.append(new, k, v)
+        if s.lens.max() > 100:
+            s.check(dtype)
+            s = Sequences(cf, dev, 4, 5, dim, 32, 8, seed=dim)
+    s.check(dtype)
+
+
 def test_rolled_back_tokens_are_written_again(cf, dev):
     """A shorter length and other tokens in the places behind it: the block's scale stays, a block begun anew
     forgets its own."""
