@@ -72,7 +72,6 @@ struct RowSource {
     static constexpr int kBytes = 2 * kKeyParts * kPlane;
     // a thread's loads: 16 bytes of kPasses rows, kStep apart
     static constexpr int kChunks = D * sizeof(T) / 16, kStep = 64 * WAVES / kChunks, kPasses = kKeys / kStep;
-    static constexpr int kTurn = D == 128 ? 7 : 3;
 
     static constexpr int kGroup = 64 * WAVES, kBad = kGroup * kPasses;
     static constexpr bool kOrdered = true;
@@ -88,8 +87,11 @@ struct RowSource {
     // rounded parts: what the products leave out is then at most 2^-24 of their factors
     static __device__ __forceinline__ __bf16 part(float* rest) { return round_bf16(rest); }
 
-    // V's channels lie in runs of 16, turned by the row: a transposing read takes four rows of one run
-    static __device__ constexpr uint32_t run(int row, int r) { return row * (2 * D) + ((r ^ (row & kTurn)) << 5); }
+    // V's channels lie in runs of 16, turned by the row: a transposing read takes four rows of two runs with 32 lanes, which
+    // are then all of the banks (turned so that two runs met, LDS was busy a third longer).
+    static __device__ constexpr uint32_t run(int row, int r) {
+        return row * (2 * D) + ((r ^ (D == 128 ? 2 * (row & 3) : row & 3)) << 5);
+    }
 
     __device__ __forceinline__ void begin(const RowsArgs& p) {
         const int lane = threadIdx.x & 63, n = lane & 31, h = lane >> 5;
