@@ -518,7 +518,9 @@ def _flat(name: str, t: torch.Tensor | None, dev: int, dtype: torch.dtype, shape
     if t.shape != shape:
         raise ValueError(f"{name} is {tuple(t.shape)}, the call needs {shape}")
     _here(name, t, dev)
-    raise ValueError("libcf needs contiguous tensors")
+    if not t.is_contiguous():
+        raise ValueError("libcf needs contiguous tensors")
+    return t.data_ptr()
 
 
 def _shaped(name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple):
@@ -752,11 +754,13 @@ class KV8Cache:
                                     device=device or require_device()), page_size, head_dim)
 
     def _args(self, dev: int):
-        d = self.data
-        if d.dim() != 3 or d.shape[2] != 2 * self.page_size * self.head_dim + max(16, self.page_size // 8):
-            raise ValueError(f"cache data is {tuple(d.shape)}: want (pages, kv_heads, 2 * page_size * head_dim + max(16, page_size / 8))")
-        _fit("KV8Cache", -2, "iii", self.page_size, d.shape[1], self.head_dim)
-        return _flat("cache", d, dev, _U8, d.shape), d.shape[0], self.page_size, d.shape[1], self.head_dim
+        d, page_size, head_dim = self.data, self.page_size, self.head_dim
+        shape = d.shape
+        if len(shape) != 3 or shape[2] != 2 * page_size * head_dim + max(16, page_size // 8):
+            raise ValueError(f"cache data is {tuple(shape)}: want (pages, kv_heads, 2 * page_size * head_dim + max(16, page_size / 8))")
+        pages, heads, _ = shape
+        _fit("KV8Cache", -2, "iii", page_size, heads, head_dim)
+        return _flat("cache", d, dev, _U8, shape), pages, page_size, heads, head_dim
 
 
 def kv8_append(cache: KV8Cache, k: torch.Tensor, v: torch.Tensor, kv_lens: torch.Tensor, table: torch.Tensor | None = None,
@@ -857,6 +861,7 @@ def _workspace(workspace_bytes, dt, q, most, heads, kv_heads, workspace, dev, st
             return None, None, 0
         # freed when the call returns, possibly before the launch stream has used it
         workspace = _new(q, need, stream, _U8)
+        return workspace, workspace.data_ptr(), need
     return workspace, _flat("workspace", workspace, dev, workspace.dtype, workspace.shape), workspace.numel() * workspace.element_size()
 
 
@@ -896,20 +901,28 @@ def _pages_call(fn: str, have: PageTable, out: PageTable | None, workspace, stre
     rows, width = have.table.shape
     shape = (have.refs.numel(), rows, width)
     _fit(fn, -2, "qiii", *shape, have.page_size)
-    out = have._like(stream) if out is None else out
-    if out.page_size != have.page_size:
+    if out is not None and out.page_size != have.page_size:
         raise ValueError(f"pages of {have.page_size} tokens in, of {out.page_size} out")
+    pin = have._pages("have", dev, shape)
+    if out is None:
+        out = have._like(stream)
+        pout = Pages(out.refs.data_ptr(), out.table.data_ptr(), out.lens.data_ptr())
+    else:
+        pout = pin if out is have else out._pages("out", dev, shape)
     need = lib.cf_pages_workspace_bytes(shape[0], rows)
     if workspace is None:
         workspace = _new(have.table, max(need, 4) // 4, stream)
-    ws = (_flat("workspace", workspace, dev, workspace.dtype, workspace.shape), workspace.numel() * workspace.element_size())
-    pin = have._pages("have", dev, shape)
-    return pin, pin if out is have else out._pages("out", dev, shape), out, shape, ws, dev, workspace
+        ws = (workspace.data_ptr(), need)
+    else:
+        ws = (_flat("workspace", workspace, dev, workspace.dtype, workspace.shape), workspace.numel() * workspace.element_size())
+    return pin, pout, out, shape, ws, dev, workspace
 
 
 def _words(like: torch.Tensor, n: int, t: torch.Tensor | None, name: str, dev: int, stream):
     """(a buffer of n int32, its address)."""
-    t = _new(like, n, stream) if t is None else t
+    if t is None:
+        t = _new(like, n, stream)
+        return t, t.data_ptr()
     return t, _flat(name, t, dev, torch.int32, (n,))
 
 
