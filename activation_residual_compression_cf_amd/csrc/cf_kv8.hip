@@ -105,6 +105,7 @@ __device__ __forceinline__ uint32_t encode2(uint32_t c, float a, float b, float 
 }
 
 typedef float vf2 __attribute__((ext_vector_type(2)));
+typedef uint32_t vu4 __attribute__((ext_vector_type(4)));
 
 template <bool HIGH>
 __device__ __forceinline__ vf2 decode2(uint32_t c, float scale) {
@@ -316,10 +317,20 @@ __global__ __launch_bounds__(kThreads) void read_kernel(const ReadArgs p) {
         const Kv8Block blk{p.cache.block.page, D};
         const uint8_t* const base = p.cache.at(page, head);
         const vu2 kc = *reinterpret_cast<const vu2*>(base + blk.k_code(in) + 8 * lane);
-        const uint8_t* const vc = base + blk.v_code(in, 8 * lane);
-        uint32_t w[2] = {0, 0};
+        // V's eight channels lie together with those of seven other tokens, which other lanes read: four loads, and a byte of
+        // each eight (9218 tokens of 24 heads of 128 in bf16 28 us, 6.0 TB/s; eight loads of a byte took 59)
+        const vu4* const vc = reinterpret_cast<const vu4*>(base + blk.v_code(in & ~7, 8 * lane));
+        const uint32_t one = in & 3, low = one | (4 + one) << 8 | 0x0c0c0000u, high = 0x0c0cu | one << 16 | (4 + one) << 24;
+        uint32_t c[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i >> 2] |= static_cast<uint32_t>(vc[8 * i]) << (8 * (i & 3));
+        for (int i = 0; i < 4; ++i) {
+            const vu4 x = vc[i];
+            c[2 * i] = in & 4 ? x.y : x.x, c[2 * i + 1] = in & 4 ? x.w : x.z;
+        }
+        uint32_t w[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            w[i] = __builtin_amdgcn_perm(c[4 * i + 1], c[4 * i], low) | __builtin_amdgcn_perm(c[4 * i + 3], c[4 * i + 2], high);
         const float ks = __uint_as_float(uint32_t(base[blk.k_scale(in)]) << 23), vs = __uint_as_float(uint32_t(base[blk.v_scale(in)]) << 23);
         const auto get = [](uint32_t lo, uint32_t hi, float s, float (&x)[8]) {
             const vf2 a = decode2<false>(lo, s), b = decode2<true>(lo, s), c = decode2<false>(hi, s), d = decode2<true>(hi, s);
