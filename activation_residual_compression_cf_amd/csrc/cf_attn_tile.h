@@ -30,8 +30,12 @@ struct Tile {
     static constexpr bool kJoins = true;  // by itself
 };
 
-// The reference follows a row's largest score when that has risen by more than 2^kRise.
-constexpr float kRise = 8.f;
+// A row's reference follows its largest score when that has risen by more than 2^kRiseLog2, or (kSums) when its
+// probabilities of a tile add up to more than kRise in a lane: none is larger otherwise.  The sums are there, which
+// saves a tenth of the vector instructions at 64 channels, and they are looked at twice a tile.  For rows that pays
+// (all tokens of a video 3007 -> 2896 us; 16384 rows over 16384 keys of 128 channels 2043 -> 2008), for the
+// 8-bit cache it does not (2925 rows over 17550 keys of 64 channels 541 -> 559, prompts in chunks 170 -> 174).
+constexpr float kRise = 256.f, kRiseLog2 = 8.f;
 
 // Rows of keys, [key][D] bf16 in chunks of 16 bytes that lie turned by their row: the 16 rows that a product's lanes
 // read at once, and the consecutive chunks of the rows that are written at once, are then on different banks.
@@ -159,7 +163,7 @@ __global__ __launch_bounds__(K::kGroup, K::kResident * K::Source::kWaves / 4) vo
         float m[RB], sum[RB];  // m: reference in units of log2
 #pragma unroll
         for (int b = 0; b < RB; ++b) {
-            m[b] = kNone, sum[b] = 0.f;
+            m[b] = lo[b] < hi[b] ? kNone : 0.f, sum[b] = 0.f;  // rows that see nothing have nothing to follow
 #pragma unroll
             for (int j = 0; j < kDt; ++j)
 #pragma unroll
@@ -215,7 +219,7 @@ __global__ __launch_bounds__(K::kGroup, K::kResident * K::Source::kWaves / 4) vo
 
             vf16 x[kSub][RB];           // scores: r of half g is of key key0 + 32 g + 8 h + 16 (r / 8) + r % 8
             vu4 pf[kSub][RB][2][QP];    // their probabilities: bf16 in pairs
-            float ref[RB], more[RB];
+            float ref[RB], more[RB], before[RB];  // before: of more, what the first half gave
             const auto key_product = [&](int f) {
                 if (f % kC == 0)
 #pragma unroll
@@ -279,39 +283,75 @@ __global__ __launch_bounds__(K::kGroup, K::kResident * K::Source::kWaves / 4) vo
                         if ((S::none(flag) >> run & 1u) || key < lo[b] || key >= hi[b]) x[g][b][r] = kNone;
                     }
             };
-            float top[RB];
-            const auto most = [&](int g, int r0, int r1) {
+            // Moves the references up to half g's scores where a row sees its first key, or where its probabilities so far add
+            // up to more than kRise: to whole numbers, so that what is moved with them stays as exact.
+            // made: the probabilities have been made from the old references.  Nearly always those hold, nothing
+            // waits for a decision, and no maximum is taken; else they are made again.
+            // Rows decide for themselves, so that none depends on those beside it.
+            const auto settle = [&](int g, bool made) {
+                float top[RB];
+                bool rise[RB], any = false;
+                const auto largest = [&](int b) {
+                    top[b] = kNone;
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) top[b] = fmaxf(top[b], x[g][b][r]);
+                    top[b] *= p.scale_log2;
+                };
+#pragma unroll
+                for (int b = 0; b < RB; ++b) {
+                    if (!made) largest(b);
+                    rise[b] = made ? m[b] == kNone || more[b] > kRise : top[b] > m[b] + kRiseLog2;
+                    any |= rise[b];
+                }
+                if (!__any(any)) return;
+#pragma unroll
+                for (int b = 0; b < RB; ++b) {
+                    if (made) largest(b);
+                    // both lanes of a row, whatever either says
+                    const int others = __shfl_xor(static_cast<int>(rise[b]), 32, 64);
+                    const float most = fmaxf(top[b], __shfl_xor(top[b], 32, 64));
+                    const float r = rise[b] | others ? fmaxf(__builtin_ceilf(most), m[b]) : m[b];
+                    const float f = m[b] == r ? 1.f : __builtin_amdgcn_exp2f(m[b] - r);
+                    m[b] = r;
+                    sum[b] *= f;
+                    more[b] = before[b] * f;
+#pragma unroll
+                    for (int j = 0; j < kDt; ++j) o[b][j] *= f;
+                    ref[b] = m[b] == kNone ? 0.f : -m[b];
+                }
+                if (made) exps(g, 0, 8);
+            };
+
+            // The same where the maximum is taken, for both halves of a tile at once: the first half's probabilities have been made.
+            float most[RB];
+            const auto follow = [&](int g, int r0, int r1) {
 #pragma unroll
                 for (int b = 0; b < RB; ++b) {
 #pragma unroll
-                    for (int r = r0; r < r1; ++r) top[b] = fmaxf(top[b], x[g][b][r]);
-                    here(top[b]);
+                    for (int r = r0; r < r1; ++r) most[b] = fmaxf(most[b], x[g][b][r]);
+                    here(most[b]);
                 }
             };
-            // Moves the references to the new scores, where those have risen: to whole numbers, so that what is moved with them
-            // stays as exact.  A tile's first half has its probabilities by then, from the old reference: nearly always
-            // that holds, and nothing waits for a decision between the two products.  Else they are made again.
-            const auto settle = [&](bool made) {
+            const auto settle_both = [&]() {
                 bool rise = false;
 #pragma unroll
                 for (int b = 0; b < RB; ++b) {
-                    top[b] *= p.scale_log2;
-                    rise |= top[b] > m[b] + kRise;
+                    most[b] *= p.scale_log2;
+                    rise |= most[b] > m[b] + kRiseLog2;
                 }
-                if (__any(rise)) {
+                if (!__any(rise)) return;
 #pragma unroll
-                    for (int b = 0; b < RB; ++b) {
-                        const float r = fmaxf(__builtin_ceilf(fmaxf(top[b], __shfl_xor(top[b], 32, 64))), m[b]);
-                        const float f = m[b] == r ? 1.f : __builtin_amdgcn_exp2f(m[b] - r);
-                        m[b] = r;
-                        sum[b] *= f;
-                        more[b] = 0.f;
+                for (int b = 0; b < RB; ++b) {
+                    const float r = fmaxf(__builtin_ceilf(fmaxf(most[b], __shfl_xor(most[b], 32, 64))), m[b]);
+                    const float f = m[b] == r ? 1.f : __builtin_amdgcn_exp2f(m[b] - r);
+                    m[b] = r;
+                    sum[b] *= f;
+                    more[b] = 0.f;
 #pragma unroll
-                        for (int j = 0; j < kDt; ++j) o[b][j] *= f;
-                        ref[b] = m[b] == kNone ? 0.f : -m[b];
-                    }
-                    if (made) exps(0, 0, 8);
+                    for (int j = 0; j < kDt; ++j) o[b][j] *= f;
+                    ref[b] = m[b] == kNone ? 0.f : -m[b];
                 }
+                exps(0, 0, 8);
             };
 
             // the next tile's stores go beside the last of K's products, the loads of the one behind it beside the first of V's
@@ -332,7 +372,7 @@ __global__ __launch_bounds__(K::kGroup, K::kResident * K::Source::kWaves / 4) vo
                 stay<S::kOrdered>();
             }
 #pragma unroll
-            for (int b = 0; b < RB; ++b) more[b] = 0.f, top[b] = kNone, ref[b] = m[b] == kNone ? 0.f : -m[b];
+            for (int b = 0; b < RB; ++b) more[b] = before[b] = 0.f, most[b] = kNone, ref[b] = m[b] == kNone ? 0.f : -m[b];
             mask(0);
             if constexpr (kSub == 2) {
                 // a half's probabilities beside the other half's products
@@ -340,17 +380,22 @@ __global__ __launch_bounds__(K::kGroup, K::kResident * K::Source::kWaves / 4) vo
                 for (int f = kC; f < 2 * kC; ++f) {
                     key_product(f);
                     exps(0, 8 * (f - kC) / kC, 8 * (f - kC + 1) / kC);
-                    most(0, 16 * (f - kC) / kC, 16 * (f - kC + 1) / kC);
+                    if constexpr (!S::kSums) follow(0, 16 * (f - kC) / kC, 16 * (f - kC + 1) / kC);
                     store_beside(f - kC);
                     mix<kProducts, kBeside>();
                     stay<S::kOrdered>();
                 }
                 mask(1);
-                most(1, 0, 16);
-                settle(true);
+                if constexpr (S::kSums) {
+                    settle(0, true);
+#pragma unroll
+                    for (int b = 0; b < RB; ++b) before[b] = more[b];
+                } else {
+                    follow(1, 0, 16);
+                    settle_both();
+                }
             } else {
-                most(0, 0, 16);
-                settle(false);
+                settle(0, false);
                 exps(0, 0, 4);
             }
             // a wave in its second half goes before one in its first: the two of a SIMD drift apart, and one's vector work
@@ -365,6 +410,7 @@ __global__ __launch_bounds__(K::kGroup, K::kResident * K::Source::kWaves / 4) vo
                 if (kSub == 2 && v < 2 * kDt) exps(1, 8 * v / (2 * kDt), 8 * (v + 1) / (2 * kDt));
                 if (kSub == 1 && v < kDt) exps(0, 4 + 4 * v / kDt, 4 + 4 * (v + 1) / kDt);
                 if (v < 2 * kDt) load_beside(v);
+                if (S::kSums && kSub == 2 && v == 2 * kDt - 1) settle(1, true);
                 mix<kProducts, kBeside>();
                 stay<S::kOrdered>();
             }
