@@ -74,7 +74,7 @@ struct RowSource {
     static constexpr int kChunks = D * sizeof(T) / 16, kStep = 64 * WAVES / kChunks, kPasses = kKeys / kStep;
 
     static constexpr int kGroup = 64 * WAVES, kBad = kGroup * kPasses;
-    static constexpr bool kOrdered = true, kSums = true;
+    static constexpr bool kSums = true;
     static constexpr int kPieces = 2 * kPasses;  // of a thread's loads and stores of a tile: K's, and V's
 
     const char* k;  // the sequence's first key

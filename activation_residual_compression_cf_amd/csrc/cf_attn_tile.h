@@ -1,4 +1,4 @@
-// The attention kernel for many rows, over tiles of keys that a workgroup's four waves share through shared memory.
+// The attention kernel for many rows, over tiles of keys that a workgroup's waves share through shared memory.
 // A source S says where keys come from and how a tile lies in shared memory (cf_attn.hip: rows; cf_kv8_attn.hip: a
 // cache's pages).
 #pragma once
@@ -60,10 +60,7 @@ __device__ __forceinline__ __bf16 round_bf16(float* rest) {
 typedef uint64_t FlagWord;
 
 // Nothing moves across: what is read before is in flight while what stands before is worked on.
-template <bool ON>
-__device__ __forceinline__ void stay() {
-    if constexpr (ON) __builtin_amdgcn_sched_barrier(0);
-}
+__device__ __forceinline__ void stay() { __builtin_amdgcn_sched_barrier(0); }
 
 // Where values have several parts, a wave has the SIMD for itself and products and vector instructions take equally long:
 // each product is followed by some of the others, which run beside it.  Left alone, the compiler puts twenty and more
@@ -369,7 +366,7 @@ __global__ __launch_bounds__(K::kGroup, K::kResident * K::Source::kWaves / 4) vo
                 if (f == 0) __builtin_amdgcn_s_setprio(0);
                 if constexpr (kSub == 1) store_beside(f);
                 mix<kProducts, kBeside>();
-                stay<S::kOrdered>();
+                stay();
             }
 #pragma unroll
             for (int b = 0; b < RB; ++b) more[b] = before[b] = 0.f, most[b] = kNone, ref[b] = m[b] == kNone ? 0.f : -m[b];
@@ -383,7 +380,7 @@ __global__ __launch_bounds__(K::kGroup, K::kResident * K::Source::kWaves / 4) vo
                     if constexpr (!S::kSums) follow(0, 16 * (f - kC) / kC, 16 * (f - kC + 1) / kC);
                     store_beside(f - kC);
                     mix<kProducts, kBeside>();
-                    stay<S::kOrdered>();
+                    stay();
                 }
                 mask(1);
                 if constexpr (S::kSums) {
@@ -412,7 +409,7 @@ __global__ __launch_bounds__(K::kGroup, K::kResident * K::Source::kWaves / 4) vo
                 if (v < 2 * kDt) load_beside(v);
                 if (S::kSums && kSub == 2 && v == 2 * kDt - 1) settle(1, true);
                 mix<kProducts, kBeside>();
-                stay<S::kOrdered>();
+                stay();
             }
 #pragma unroll
             for (int b = 0; b < RB; ++b) sum[b] += more[b];

@@ -40,7 +40,7 @@ struct Kv8Source {
     static constexpr int kShare = D / WAVES, kChannels = kShare / 8, kPiece = kShare < 16 ? kShare : 16, kPieces = 2 * kShare / kPiece;
     static constexpr int kGroup = 64 * WAVES, kMine = kKeys / WAVES, kLanes = 8 * WAVES;  // keys of a wave; lanes of eight keys
     static constexpr int kBad = kGroup * kChannels;
-    static constexpr bool kOrdered = true, kSums = false;
+    static constexpr bool kSums = false;
 
     int b, head, wave;
     int pages;  // of the four runs of 16 keys of the tile to load next, in lanes 0 .. 3

@@ -428,7 +428,7 @@ size_t cf_kv8_attention_workspace_bytes(int a_dtype, int64_t max_q, int q_heads,
  *   q, out: total_q x q_heads rows of a_dtype;  k, v: total_k x kv_heads rows of a_dtype;
  *   q_starts, k_starts: batch + 1 int32, or NULL: total_q / batch queries, total_k / batch keys each, without a rest;
  *   max_q: the most query tokens of a sequence, as there;  lse: total_q x q_heads fp32, or NULL;
- *   workspace: cf_attention_workspace_bytes, 256-byte aligned, as there.
+ *   workspace: cf_attention_workspace_bytes, 256-byte aligned, as there: calls that may run at once need one each.
  * Rows of out and lse that belong to no sequence stay as they are.  head_dim is 64 or 128;  total_k <= 2^31 - 256, and
  * token strides of k and v are at most 2^26 bytes;  the other limits are cf_kv4_attention's.  total_k = 0 is a call whose rows see no key.
  * bf16: queries, keys and values enter the products exactly, probabilities rounded to bf16, off by at most 2^-8 of
