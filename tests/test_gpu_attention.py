@@ -315,6 +315,24 @@ def test_side_stream_and_graphs_that_share_a_workspace(cf, dev):
             assert torch.equal(o, want), f"replay {i}"
 
 
+def test_two_calls_at_once(cf, dev):
+    """Items in many parts on two streams, each with a workspace, while the other runs."""
+    say("attention on two streams at once")
+    cases = [Case(cf, dev, [9000, 700], [200, 31], 4, 2, 128, "bf16", seed=1), Case(cf, dev, [5000], [256], 2, 1, 64, "bf16", seed=2)]
+    wants = [c.run(causal=True) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(10):
+        outs = [[] for _ in cases]
+        for _ in range(4):
+            for c, s, o in zip(cases, streams, outs):
+                o.append(cf.attention(c.q, c.k, c.v, q_starts=c.q_starts, k_starts=c.k_starts, causal=True, stream=s))
+        torch.cuda.synchronize()
+        for o, (want, _) in zip(outs, wants):
+            assert all(torch.equal(x, want) for x in o)
+
+
 def test_decoded_shards(cf, dev):
     """A receiver's bf16 copies of its peers' reconstructions, attended to where they lie."""
     say("attention over decoded shards")
