@@ -24,7 +24,10 @@ constexpr int kBlockWaves = kBlock / 64;
 // Up to so many pages and so many table entries are one workgroup's work.
 constexpr int64_t kSmall = 1 << 15;
 
-__device__ __forceinline__ int pages_of(int len, int page_size) { return (len + page_size - 1) / page_size; }
+// The sum may pass 2^31, where page sizes are no powers of two, but not 2^32: a row has fewer than 2^31 - 256 tokens.
+__device__ __forceinline__ int pages_of(int len, int page_size) {
+    return static_cast<int>((static_cast<uint32_t>(len) + static_cast<uint32_t>(page_size) - 1) / static_cast<uint32_t>(page_size));
+}
 
 // A word that atomics have changed in this launch.
 __device__ __forceinline__ int fresh_load(const int32_t* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }

@@ -297,3 +297,24 @@ def test_search_with_beams(cf, dev):
     t, _ = cf.pages_resize(t, ints([0] * rows, dev), out=t)
     torch.cuda.synchronize()
     assert not t.refs.any() and not t.lens.any() and (t.table == -1).all()
+
+
+@pytest.mark.parametrize("page,width", [(10 ** 9, 2), (1500000000, 1), (2 ** 31 - 257, 1), (2 ** 30 + 3, 1), (715827797, 2), (1000, 2147483), (1, 50)])
+def test_page_sizes_up_to_the_largest(cf, dev, page, width):
+    """Rows that end near 2^31 tokens, where tokens and a page's together are more than that."""
+    say(f"pages of {page} tokens, width={width}")
+    most = width * page
+    rows, pages = (3, 3 * width + 2) if width < 100 else (1, width + 5)
+    t = cf.PageTable.create(pages, rows, width, page)
+    refs, table, lens = [0] * pages, [[-1] * width for _ in range(rows)], [0] * rows
+    for want in ([most, 1, most - page + 1], [most - 1, most, page - 1], [most + 1, 0, most], [1, page, 0])[:None if rows > 1 else 3]:
+        want = want[:rows]
+        t, missing = cf.pages_resize(t, ints(want, dev))
+        refs, table, lens, m = ref.resize(refs, table, lens, page, want)
+        same(t, refs, table, lens)
+        assert missing.item() == m
+        if rows > 1:
+            t, src, dst, missing = cf.pages_fork(t, ints([0, 0, 2], dev))
+            refs, table, lens, s, d, m = ref.fork(refs, table, lens, page, [0, 0, 2])
+            same(t, refs, table, lens)
+            assert host(src).tolist() == s and host(dst).tolist() == d and missing.item() == m
