@@ -768,7 +768,7 @@ def kv8_append(cache: KV8Cache, k: torch.Tensor, v: torch.Tensor, kv_lens: torch
     """Quantize rows k, v (tokens, kv_heads, head_dim), the last tokens of sequences, into the cache.  kv_lens (batch,) are the
     sequences' tokens with them, starts (batch + 1,) where each one's rows begin, table (batch, pages) their pages, all
     int32; without a table sequence b has pages b * table_width and on, without starts every sequence gets
-    tokens / batch."""
+    tokens / batch.  Behind a pages_resize that may have found too few pages kv_lens are its append_lens."""
     tokens = k.shape[0] if k.dim() == 3 else -1
     want = (tokens, cache.data.shape[1], cache.head_dim)
     dt, dev, batch = _act_dtype(k), _device(k), kv_lens.numel()
@@ -882,6 +882,11 @@ class PageTable:
                          torch.full((rows, width), -1, dtype=torch.int32, device=dev),
                          torch.zeros(rows, dtype=torch.int32, device=dev), page_size)
 
+    def append_lens(self, want: torch.Tensor) -> torch.Tensor:
+        """kv_lens for an append of the tokens that a resize to want (rows,) was for: want where a row has so many, and 0, so
+        that nothing is written, where it found too few pages and still has its old length.  On the current stream."""
+        return torch.where(self.lens == want, want, 0)
+
     def _pages(self, name: str, dev: int, shape: tuple) -> Pages:
         pages, rows, width = shape
         i32 = torch.int32
@@ -930,7 +935,7 @@ def pages_resize(have: PageTable, want: torch.Tensor, out: PageTable | None = No
                  workspace: torch.Tensor | None = None, stream=None):
     """Sequences of want (rows,) int32 tokens each (negative: as it is): those that shrink let go pages, then those that
     grow take the first free ones.  Returns (out, missing): missing (1,) int32 says how many rows found too few and stay as they
-    are.  out may be `have`."""
+    are; an append takes out.append_lens(want), since out.lens would place their new tokens over their last.  out may be `have`."""
     pin, pout, out, shape, ws, dev, workspace = _pages_call("cf_pages_resize", have, out, workspace, stream)
     missing, pm = _words(have.table, 1, missing, "missing", dev, stream)
     rc = lib.cf_pages_resize(pin, pout, *shape, have.page_size, _flat("want", want, dev, torch.int32, (shape[1],)), pm, *ws, _on(stream, dev))

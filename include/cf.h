@@ -393,7 +393,8 @@ size_t cf_kv4_attention_workspace_bytes(int a_dtype, int64_t max_q, int q_heads,
  *   byte = e + 127;  code = the nearest to x * 2^-e, ties to the even code, 448 above 448; 127 for NaN and infinities
  * So values are held with an error of at most 2^-4 of themselves or 2^(e - 10), and magnitudes beyond 448 * 2^7 saturate.
  * Places of a block behind the tokens that came hold nothing.  Rows with no place (kv_lens[b] is less than their number,
- * a page outside the cache, rows of no sequence) are not kept.  Sequences of a call must not share a page that gets tokens.
+ * a page outside the cache, rows of no sequence) are not kept.  A kv_lens beyond the table's pages is cut to them, and the rows
+ * then take their last places.  Sequences of a call must not share a page that gets tokens.
  *   k, v: tokens x kv_heads rows;  table, kv_lens, starts: as in cf_kv4_attention, the rows being the queries there;
  *   tokens <= 2^27, 1 <= batch <= 2^24, table_width * page_size < 2^31 - 256.
  * cf_kv8_read is as cf_kv4_read.
@@ -453,7 +454,9 @@ size_t cf_attention_workspace_bytes(int a_dtype, int64_t max_q, int q_heads, int
  * cf_pages_resize: row r gets want[r] tokens (negative: it stays as it is).  First rows that shrink let go the pages they
  *   no longer need (all of them at 0 tokens); then those that grow, in the order of rows, take free pages in the order of
  *   their numbers.  A row whose pages, behind those of the rows before it, are not all there, or that wants more than
- *   width * page_size, stays as it is.  missing: how many those are.
+ *   width * page_size, stays as it is.  missing: how many those are.  A row was served exactly if its length is the one
+ *   it wanted: one that was not has no places for what is to be appended to it, and cf_kv8_append with its length would
+ *   write over its last tokens.  A length of 0 there leaves them as they are and keeps nothing of the new ones.
  * cf_pages_fork: row r becomes a copy of row parents[r] as it was (itself: it stays; outside [0, rows): it becomes empty).
  *   Whole pages are shared.  A last, partly filled page goes on with the parent itself, or else the first of the rows; every
  *   other row, in the order of rows, takes the first free page in its place, src[r] and dst[r] being the pages to copy, for

@@ -318,3 +318,56 @@ def test_page_sizes_up_to_the_largest(cf, dev, page, width):
             refs, table, lens, s, d, m = ref.fork(refs, table, lens, page, [0, 0, 2])
             same(t, refs, table, lens)
             assert host(src).tolist() == s and host(dst).tolist() == d and missing.item() == m
+
+
+@pytest.mark.parametrize("starts", [True, False])
+def test_appends_where_pages_run_out(cf, dev, starts):
+    """A serving loop without a host wait, with too few pages and with rows that want more than the table holds: rows
+    that were not served keep every token, those that were get theirs, and later pages serve them all."""
+    say("pages: appends with too few pages")
+    rng = np.random.default_rng(21)
+    rows, width, page, heads, dim, pages = 5, 3, 16, 2, 64, 9
+    t = cf.PageTable.create(pages, rows, width, page)
+    cache = cf.KV8Cache.create(pages, page, heads, dim)
+    held = [[ref.Held(heads, dim) for _ in range(rows)] for _ in range(2)]
+    refs, table, lens = [0] * pages, [[-1] * width for _ in range(rows)], [0] * rows
+    short = 0
+
+    def step(want, new):
+        """Rows want so many tokens and bring `new`."""
+        nonlocal t, refs, table, lens, short
+        was = lens
+        refs, table, lens, m = ref.resize(refs, table, lens, page, want)
+        short += m
+        x = torch.from_numpy(rng.standard_normal((2, sum(new), heads, dim)).astype(np.float32)).to(dev)
+        w = ints(want, dev)
+        t, missing = cf.pages_resize(t, w, out=t)
+        cf.kv8_append(cache, x[0], x[1], t.append_lens(w), table=t.table, starts=ints(np.concatenate([[0], np.cumsum(new)]), dev) if starts else None)
+        at = 0
+        for r in range(rows):
+            for y, h in zip(x, held):
+                if lens[r] < was[r]:
+                    h[r].cut(lens[r])
+                if want[r] == lens[r] and 0 < new[r] <= lens[r]:
+                    h[r].append(host(y[at:at + new[r]].double()))
+            at += new[r]
+        same(t, refs, table, lens)
+        assert missing.item() == m
+        for r in range(rows):
+            if lens[r]:
+                pos = np.arange(lens[r])
+                slots = torch.from_numpy(np.asarray(table[r])[pos // page] * page + pos % page).to(dev)
+                for got, h in zip(cf.kv8_read(cache, slots, torch.float32), held):
+                    assert np.array_equal(host(got.double()), h[r].x), f"row {r}"
+
+    n = [16] * rows
+    step([16] * rows, n)
+    step([32] * rows, n)  # four rows find a page
+    for _ in range(3):
+        step([x + 1 for x in lens], [1] * rows)  # no page is left
+    assert lens == [32, 32, 32, 32, 16] and short == 16
+    step([0, -1, 33, 48 + 1, 17], [0, 0, 1, 1, 1] if starts else [1] * rows)
+    assert lens == [0, 32, 33, 32, 17]
+    if starts:
+        step([0, 0, 33 + 7, 10 ** 9, 17 + 20], [0, 0, 7, 5, 20])
+        assert lens == [0, 0, 40, 32, 37]

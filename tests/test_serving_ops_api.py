@@ -281,3 +281,12 @@ def test_binding_refuses(cf):
         cf.pages_copy(torch.zeros(8, 64, dtype=torch.uint8), want, want)
     with pytest.raises(ValueError, match="device tensors"):
         cf.pages_copy(torch.zeros(1, 8, 64, dtype=torch.uint8), want, want)
+
+
+def test_lengths_of_an_append_behind_a_short_resize(cf):
+    import torch
+
+    t = cf.PageTable.create(8, 4, 3, 16, device="cpu")
+    t.lens.copy_(torch.tensor([17, 16, 0, 5]))
+    got = t.append_lens(torch.tensor([17, 17, 0, -1], dtype=torch.int32))
+    assert got.tolist() == [17, 0, 0, 0] and got.dtype == torch.int32
