@@ -58,6 +58,7 @@ _SIG = {
     "cf_pages_workspace_bytes": ("z", "li"),
     "cf_pages_resize": ("i", "gg" "liii" "pp" "pzp"),
     "cf_pages_fork": ("i", "gg" "liii" "pppp" "pzp"),
+    "cf_pages_fork_own": ("i", "gg" "liii" "pppp" "pzp"),
     "cf_pages_compact": ("i", "gg" "lii" "ppp" "pzp"),
     "cf_pages_copy": ("i", "pllil" "pplpp"),
     "cf_strerror": ("s", "i"),
@@ -935,7 +936,8 @@ def pages_resize(have: PageTable, want: torch.Tensor, out: PageTable | None = No
                  workspace: torch.Tensor | None = None, stream=None):
     """Sequences of want (rows,) int32 tokens each (negative: as it is): those that shrink let go pages, then those that
     grow take the first free ones.  Returns (out, missing): missing (1,) int32 says how many rows found too few and stay as they
-    are; an append takes out.append_lens(want), since out.lens would place their new tokens over their last.  out may be `have`."""
+    are; an append takes out.append_lens(want), since out.lens would place their new tokens over their last.  Rows that shrink to
+    inside a page that others hold need pages_fork(own=True) before anything is appended to them.  out may be `have`."""
     pin, pout, out, shape, ws, dev, workspace = _pages_call("cf_pages_resize", have, out, workspace, stream)
     missing, pm = _words(have.table, 1, missing, "missing", dev, stream)
     rc = lib.cf_pages_resize(pin, pout, *shape, have.page_size, _flat("want", want, dev, torch.int32, (shape[1],)), pm, *ws, _on(stream, dev))
@@ -946,18 +948,20 @@ def pages_resize(have: PageTable, want: torch.Tensor, out: PageTable | None = No
 
 def pages_fork(have: PageTable, parents: torch.Tensor, out: PageTable | None = None, src: torch.Tensor | None = None,
                dst: torch.Tensor | None = None, missing: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
-               stream=None):
+               stream=None, own: bool = False):
     """Row r becomes a copy of row parents[r] (rows,) int32 (itself: it stays; outside the rows: empty).  Whole pages are
     shared.  Returns (out, src, dst, missing): pages src[r] have to be copied to dst[r], with pages_copy in every cache, before
-    anything is appended; missing (1,) says how many rows found no page for that and end before it."""
-    pin, pout, out, shape, ws, dev, workspace = _pages_call("cf_pages_fork", have, out, workspace, stream)
+    anything is appended; missing (1,) says how many rows found no page for that and end before it.  Where a pages_resize
+    may have shrunk rows to inside pages that others hold, own=True: every row's last, partly filled page is then its alone,
+    whoever its parent is (parents = 0, 1, 2, .. changes nothing else)."""
+    fn, call = ("cf_pages_fork_own", lib.cf_pages_fork_own) if own else ("cf_pages_fork", lib.cf_pages_fork)
+    pin, pout, out, shape, ws, dev, workspace = _pages_call(fn, have, out, workspace, stream)
     src, p1 = _words(have.table, shape[1], src, "src", dev, stream)
     dst, p2 = _words(have.table, shape[1], dst, "dst", dev, stream)
     missing, pm = _words(have.table, 1, missing, "missing", dev, stream)
-    rc = lib.cf_pages_fork(pin, pout, *shape, have.page_size, _flat("parents", parents, dev, torch.int32, (shape[1],)), p1, p2, pm,
-                           *ws, _on(stream, dev))
+    rc = call(pin, pout, *shape, have.page_size, _flat("parents", parents, dev, torch.int32, (shape[1],)), p1, p2, pm, *ws, _on(stream, dev))
     if rc:
-        raise CFError("cf_pages_fork", rc)
+        raise CFError(fn, rc)
     return out, src, dst, missing
 
 

@@ -335,6 +335,17 @@ int check_pages(const cf_pages* in, const cf_pages* out, int64_t pages, int rows
     return CF_OK;
 }
 
+int pages_fork(const cf_pages* in, const cf_pages* out, int64_t pages, int rows, int width, int page_size,
+               const int32_t* parents, int32_t* src, int32_t* dst, int32_t* missing, bool own, void* workspace,
+               size_t ws_bytes, void* stream) {
+    if (int rc = check_pages(in, out, pages, rows, width, page_size, false, parents, {src, dst, missing}, {rows, rows, 1}, workspace, ws_bytes))
+        return rc;
+    if (!parents) return CF_E_NULL;
+    if (int rc = check_device()) return rc;
+    const cf::PagesCall call{*in, *out, pages, rows, width, page_size, parents, src, dst, missing};
+    return cf::launch_pages_fork(call, own, workspace, static_cast<hipStream_t>(stream)) == hipSuccess ? CF_OK : CF_E_HIP;
+}
+
 }  // namespace
 
 extern "C" {
@@ -792,12 +803,13 @@ int cf_pages_resize(const cf_pages* in, const cf_pages* out, int64_t pages, int 
 int cf_pages_fork(const cf_pages* in, const cf_pages* out, int64_t pages, int rows, int width, int page_size,
                   const int32_t* parents, int32_t* src, int32_t* dst, int32_t* missing, void* workspace, size_t ws_bytes,
                   void* stream) {
-    if (int rc = check_pages(in, out, pages, rows, width, page_size, false, parents, {src, dst, missing}, {rows, rows, 1}, workspace, ws_bytes))
-        return rc;
-    if (!parents) return CF_E_NULL;
-    if (int rc = check_device()) return rc;
-    const cf::PagesCall call{*in, *out, pages, rows, width, page_size, parents, src, dst, missing};
-    return cf::launch_pages_fork(call, workspace, static_cast<hipStream_t>(stream)) == hipSuccess ? CF_OK : CF_E_HIP;
+    return pages_fork(in, out, pages, rows, width, page_size, parents, src, dst, missing, false, workspace, ws_bytes, stream);
+}
+
+int cf_pages_fork_own(const cf_pages* in, const cf_pages* out, int64_t pages, int rows, int width, int page_size,
+                      const int32_t* parents, int32_t* src, int32_t* dst, int32_t* missing, void* workspace, size_t ws_bytes,
+                      void* stream) {
+    return pages_fork(in, out, pages, rows, width, page_size, parents, src, dst, missing, true, workspace, ws_bytes, stream);
 }
 
 int cf_pages_compact(const cf_pages* in, const cf_pages* out, int64_t pages, int rows, int width, int32_t* src,

@@ -131,7 +131,7 @@ struct PagesCall {
 };
 size_t pages_workspace(int64_t pages, int rows);
 hipError_t launch_pages_resize(const PagesCall& call, void* workspace, hipStream_t stream);
-hipError_t launch_pages_fork(const PagesCall& call, void* workspace, hipStream_t stream);
+hipError_t launch_pages_fork(const PagesCall& call, bool own, void* workspace, hipStream_t stream);
 hipError_t launch_pages_compact(const PagesCall& call, void* workspace, hipStream_t stream);
 hipError_t launch_pages_copy(void* data, int64_t pages, int64_t page_bytes, int layers, int64_t layer_stride, const int32_t* src,
                              const int32_t* dst, int64_t n, const int32_t* count, hipStream_t stream);

@@ -59,6 +59,7 @@ struct PagesArgs {
     int32_t *src, *dst;      // fork, compact
     int32_t* count;          // missing, or moves
     int32_t *first, *offset, *list;  // workspace
+    int firsts;                      // how many of `first`
     __device__ __forceinline__ bool named(int page) const { return static_cast<uint32_t>(page) < static_cast<uint32_t>(pages); }
     __device__ __forceinline__ int len_of(int row) const { return min(max(lens_in[row], 0), width * page_size); }
     __device__ __forceinline__ int parent_of(int row) const { return static_cast<uint32_t>(want[row]) < static_cast<uint32_t>(rows) ? want[row] : -1; }
@@ -94,13 +95,22 @@ struct Resize {
     }
 };
 
+// OWN: a row's last, partly filled page is looked at whoever else holds it, not only rows with the same parent.
+template <bool OWN>
 struct Fork {
     static constexpr int kPhases = 2;
-    // Whether a row gets a page of its own for its last, partly filled one: all but one of the rows with that parent do,
-    // and the parent itself, or else the first of them, goes on with the one there is.
+    // A row's claim to go on with a partly filled page: the lowest of a parent's rows, or of a page's, does; the parent
+    // itself, or a row that stays, goes first.
+    static __device__ __forceinline__ int claim(const PagesArgs& p, int row, int parent) {
+        if (OWN) return row == parent ? row : p.rows + row;
+        return row == parent ? -1 : row;
+    }
+    // Whether a row gets a page of its own for its last, partly filled one: all but one of those that claim it do.
     static __device__ __forceinline__ bool fresh(const PagesArgs& p, int row, int parent, int size) {
-        if (parent < 0 || size % p.page_size == 0 || fresh_load(p.first + parent) == (row == parent ? -1 : row)) return false;
-        return p.named(p.table_in[int64_t(parent) * p.width + size / p.page_size]);
+        if (parent < 0 || size % p.page_size == 0) return false;
+        if (!OWN && fresh_load(p.first + parent) == claim(p, row, parent)) return false;
+        const int page = p.table_in[int64_t(parent) * p.width + size / p.page_size];
+        return p.named(page) && (!OWN || fresh_load(p.first + page) != claim(p, row, parent));
     }
     static __device__ __forceinline__ Ask ask(const PagesArgs& p, int row) {
         const int parent = p.parent_of(row), size = parent < 0 ? 0 : p.len_of(parent), whole = size / p.page_size;
@@ -114,22 +124,31 @@ struct Fork {
         if (!copies) p.dst[row] = -1;
     }
     static __device__ __forceinline__ void phase(const PagesArgs& p, int n, int64_t i, int64_t step) {
-        if (n == 0) {
+        if (n == 0 && !OWN) {
             for (; i < p.rows; i += step) {
                 const int row = static_cast<int>(i), parent = p.parent_of(row);
-                if (parent >= 0) atomicMin(p.first + parent, row == parent ? -1 : row);
+                if (parent >= 0) atomicMin(p.first + parent, claim(p, row, parent));
             }
             return;
         }
         for (; i < int64_t(p.rows) * p.width; i += step) {
             const int row = static_cast<int>(static_cast<uint32_t>(i) / static_cast<uint32_t>(p.width)), c = static_cast<int>(i) - row * p.width;
             const int parent = p.parent_of(row), size = parent < 0 ? 0 : p.len_of(parent);
+            const bool held = c < pages_of(size, p.page_size);
+            if (OWN && n == 0) {
+                const int page = held ? p.table_in[int64_t(parent) * p.width + c] : -1;
+                // nobody goes on with a page that is whole in some row
+                if (p.named(page)) atomicMin(p.first + page, c == size / p.page_size ? claim(p, row, parent) : INT32_MIN);
+                continue;
+            }
             const int old = p.table_in[i];
             if (parent != row && c < pages_of(p.len_of(row), p.page_size) && p.named(old)) atomicSub(p.refs + old, 1);
             int page = -1;
-            if (c < pages_of(size, p.page_size) && !(c == size / p.page_size && fresh(p, row, parent, size))) {
+            if (held && !(c == size / p.page_size && fresh(p, row, parent, size))) {
                 page = p.table_in[int64_t(parent) * p.width + c];
                 if (parent != row && p.named(page)) atomicAdd(p.refs + page, 1);
+            } else if (OWN && held && parent == row) {
+                atomicSub(p.refs + old, 1);  // a page that is left to those that go on with it
             }
             p.table[i] = page;
         }
@@ -142,7 +161,7 @@ __device__ __forceinline__ void begin(const PagesArgs& p, int64_t i, int64_t ste
     if (p.refs != p.refs_in)
         for (int64_t j = i; j < p.pages; j += step) p.refs[j] = p.refs_in[j];
     if (p.first)
-        for (int64_t j = i; j < p.rows; j += step) p.first[j] = INT32_MAX;
+        for (int64_t j = i; j < p.firsts; j += step) p.first[j] = INT32_MAX;
 }
 
 // Free pages for the rows that ask, by one workgroup.
@@ -406,7 +425,7 @@ __global__ __launch_bounds__(256) void copy_kernel(const CopyArgs p) {
 
 PagesArgs args_of(const PagesCall& c, void* workspace) {
     PagesArgs p{c.in.refs, c.in.table, c.in.lens, c.out.refs, c.out.table, c.out.lens, static_cast<int>(c.pages), c.rows, c.width, c.page_size,
-                c.want,    c.src,      c.dst,     c.count,    nullptr,     nullptr,    nullptr};
+                c.want,    c.src,      c.dst,     c.count,    nullptr,     nullptr,    nullptr,    0};
     p.offset = static_cast<int32_t*>(workspace);
     p.list = p.offset + c.rows + 1;
     return p;
@@ -416,17 +435,17 @@ PagesArgs args_of(const PagesCall& c, void* workspace) {
 
 size_t pages_workspace(int64_t pages, int rows) {
     const int64_t chunks = (pages + kChunk - 1) / kChunk;
-    return 4 * (static_cast<size_t>(pages) + 2 * static_cast<size_t>(rows) + chunks + 2);
+    return 4 * (2 * static_cast<size_t>(pages) + 2 * static_cast<size_t>(rows) + chunks + 2);
 }
 
 hipError_t launch_pages_resize(const PagesCall& c, void* workspace, hipStream_t stream) {
     return run<Resize>(args_of(c, workspace), stream);
 }
 
-hipError_t launch_pages_fork(const PagesCall& c, void* workspace, hipStream_t stream) {
+hipError_t launch_pages_fork(const PagesCall& c, bool own, void* workspace, hipStream_t stream) {
     PagesArgs p = args_of(c, workspace);
-    p.first = p.list + c.pages;
-    return run<Fork>(p, stream);
+    p.first = p.list + c.pages, p.firsts = own ? static_cast<int>(c.pages) : c.rows;
+    return own ? run<Fork<true>>(p, stream) : run<Fork<false>>(p, stream);
 }
 
 hipError_t launch_pages_compact(const PagesCall& c, void* workspace, hipStream_t stream) {

@@ -462,10 +462,16 @@ size_t cf_attention_workspace_bytes(int a_dtype, int64_t max_q, int q_heads, int
  *   other row, in the order of rows, takes the first free page in its place, src[r] and dst[r] being the pages to copy, for
  *   cf_pages_copy (-1 both where there is nothing to copy).  Pages that no row keeps are let go before that.  A row that
  *   finds no free page ends with its last whole page.  missing: how many those are.
+ *   Only rows with the same parent are told apart so.  Rows that have shrunk to inside a page that others hold still share
+ *   it, and must not be appended to then: cf_pages_fork_own parts them.
+ * cf_pages_fork_own: as cf_pages_fork, but every last, partly filled page is then one row's alone.  Of the rows that would end
+ *   in a page, whoever their parents are, the first of those that are their own parent goes on with it, or else the first, or
+ *   none where it is a whole page of some row; the others take free pages in its place as above.  With
+ *   parents[r] = r it is the call behind a cf_pages_resize that may have shrunk rows so.
  * cf_pages_compact: the pages that are held are made the first ones: the k-th of those behind, page src[k], goes to the
  *   k-th free one before, dst[k], for cf_pages_copy; refs and every table entry follow.  count: how many; src and dst have
  *   pages / 2 places, the rest -1.  lens stay.
- *   out may be in, array by array, for resize and compact; fork's table and lens must be other arrays.
+ *   out may be in, array by array, for resize and compact; the forks' table and lens must be other arrays.
  *   want, parents: rows int32;  src, dst: rows int32 (fork), pages / 2 (compact);  missing, count: one int32.
  *   workspace: cf_pages_workspace_bytes, 4-byte aligned.
  *   1 <= pages < 2^31, 1 <= rows <= 2^20, width >= 1, rows * width <= 2^30, width * page_size < 2^31 - 256, page_size >= 1.
@@ -491,6 +497,10 @@ int cf_pages_resize(const cf_pages* in, const cf_pages* out, int64_t pages, int 
 int cf_pages_fork(const cf_pages* in, const cf_pages* out, int64_t pages, int rows, int width, int page_size,
                   const int32_t* parents, int32_t* src, int32_t* dst, int32_t* missing, void* workspace, size_t ws_bytes,
                   void* stream);
+
+int cf_pages_fork_own(const cf_pages* in, const cf_pages* out, int64_t pages, int rows, int width, int page_size,
+                      const int32_t* parents, int32_t* src, int32_t* dst, int32_t* missing, void* workspace, size_t ws_bytes,
+                      void* stream);
 
 int cf_pages_compact(const cf_pages* in, const cf_pages* out, int64_t pages, int rows, int width, int32_t* src,
                      int32_t* dst, int32_t* count, void* workspace, size_t ws_bytes, void* stream);

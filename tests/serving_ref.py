@@ -191,3 +191,42 @@ def compact(refs, table):
     for p in used:
         out[to.get(p, p)] = refs[p]
     return out, [[to.get(p, p) for p in row] for row in table], pairs
+
+
+def fork_own(refs, table, lens, page, parents):
+    """The fork after which a last, partly filled page is one row's alone: (refs, table, lens, src, dst, missing)."""
+    pages, rows, width = len(refs), len(table), len(table[0])
+    held = [list(t[:-(-n // page)]) for t, n in zip(table, lens)]
+    par = [p if 0 <= p < rows else -1 for p in parents]
+    new, size = [list(held[p]) if p >= 0 else [] for p in par], [lens[p] if p >= 0 else 0 for p in par]
+    whole, claims = set(), {}
+    for r, h in enumerate(new):
+        for j, p in enumerate(h):
+            if 0 <= p < pages:
+                if (j + 1) * page > size[r]:
+                    claims.setdefault(p, []).append(r)
+                else:
+                    whole.add(p)
+    asks = {}
+    for p, of in claims.items():
+        stay = [r for r in of if par[r] == r] or of
+        for r in of:
+            if p in whole or r != stay[0]:
+                asks[r] = p
+                new[r].pop()
+    refs = [0] * pages
+    for h in new:
+        for p in h:
+            if 0 <= p < pages:
+                refs[p] += 1
+    free = [p for p, c in enumerate(refs) if c == 0]
+    src, dst, missing = [-1] * rows, [-1] * rows, 0
+    for r in sorted(asks):
+        if free:
+            src[r], dst[r] = asks[r], free.pop(0)
+            new[r].append(dst[r])
+            refs[dst[r]] = 1
+        else:
+            size[r] = size[r] // page * page
+            missing += 1
+    return refs, [h + [-1] * (width - len(h)) for h in new], size, src, dst, missing

@@ -371,3 +371,115 @@ def test_appends_where_pages_run_out(cf, dev, starts):
     if starts:
         step([0, 0, 33 + 7, 10 ** 9, 17 + 20], [0, 0, 7, 5, 20])
         assert lens == [0, 0, 40, 32, 37]
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_forks_that_part_rows(cf, dev, seed):
+    """Random resizes and forks of rows that share pages in any way, on states that one workgroup works on."""
+    rng = np.random.default_rng(300 + seed)
+    page, rows, width = int(rng.choice([1, 16, 24, 256])), int(rng.choice([1, 5, 70, 1100])), int(rng.choice([1, 3, 20]))
+    pages = int(rng.integers(1, rows * width + 20))
+    say(f"pages fork own rows={rows} width={width} pages={pages} page={page}")
+    refs, table, lens = random_state(rng, pages, rows, width, page)
+    t = put(cf, dev, refs, table, lens, page)
+    for i in range(5):
+        want = [int(rng.integers(-1, width * page + 2)) for _ in range(rows)]
+        t, _ = cf.pages_resize(t, ints(want, dev), out=t)
+        refs, table, lens, _ = ref.resize(refs, table, lens, page, want)
+        parents = [int(rng.integers(-1, rows + 1)) if rng.random() < (0, 0.3, 1)[i % 3] else r for r in range(rows)]
+        keep = [x.clone() for x in (t.table, t.lens)]
+        out = cf.PageTable(t.refs, torch.empty_like(t.table), torch.empty_like(t.lens), page) if i % 2 else None
+        new, src, dst, missing = cf.pages_fork(t, ints(parents, dev), out=out, own=True)
+        assert torch.equal(keep[0], t.table) and torch.equal(keep[1], t.lens)
+        t = new
+        refs, table, lens, s, d, m = ref.fork_own(refs, table, lens, page, parents)
+        same(t, refs, table, lens)
+        assert host(src).tolist() == s and host(dst).tolist() == d and missing.item() == m
+
+
+@pytest.mark.parametrize("pages,rows,width", [(40000, 300, 100), (5000, 700, 60), (32769, 1, 3), (12288, 3000, 11)])
+def test_forks_that_part_rows_large(cf, dev, pages, rows, width):
+    say(f"pages fork own rows={rows} width={width} pages={pages}")
+    rng = np.random.default_rng(pages)
+    page = 16
+    refs, table, lens = [0] * pages, [[-1] * width for _ in range(rows)], [0] * rows
+    t = put(cf, dev, refs, table, lens, page)
+    share = max(1, min(width, pages // rows))
+    for i in range(3):
+        want = rng.integers(0, share * page + 1, rows).tolist()
+        t, _ = cf.pages_resize(t, ints(want, dev))
+        refs, table, lens, _ = ref.resize(refs, table, lens, page, want)
+        parents = rng.integers(0, rows, rows).tolist() if i < 2 else list(range(rows))
+        t, src, dst, missing = cf.pages_fork(t, ints(parents, dev), own=True)
+        refs, table, lens, s, d, m = ref.fork_own(refs, table, lens, page, parents)
+        same(t, refs, table, lens)
+        assert host(src).tolist() == s and host(dst).tolist() == d and missing.item() == m
+
+
+def test_entries_that_are_no_page_own(cf, dev):
+    say("pages fork own: entries outside the cache")
+    page = 16
+    table, lens, refs = [[0, 99, 3], [-5, 2, -1], [2 ** 31 - 1, -2 ** 31, 1]], [40, 20, 40], [1, 1, 1, 1, 0, 0, 0, 0]
+    for parents in ([0, 0, 0], [2, 1, 1], [1, 2, 0], [0, 1, 2]):
+        t, src, dst, missing = cf.pages_fork(put(cf, dev, refs, table, lens, page), ints(parents, dev), own=True)
+        r, ta, le, s, d, m = ref.fork_own(refs, table, lens, page, parents)
+        same(t, r, ta, le)
+        assert host(src).tolist() == s and host(dst).tolist() == d and missing.item() == m
+
+
+def test_beams_that_go_back(cf, dev):
+    """Beams that share pages of a prompt go back to inside of it, are parted and grow on over an 8-bit cache: each reads its own
+    tokens, in a captured step too."""
+    say("pages: beams that go back")
+    rng = np.random.default_rng(31)
+    rows, width, page, heads, dim, pages = 4, 6, 16, 2, 64, 30
+    t = cf.PageTable.create(pages, rows, width, page)
+    cache = cf.KV8Cache.create(pages, page, heads, dim)
+    held = [[ref.Held(heads, dim) for _ in range(rows)] for _ in range(2)]
+
+    def rows_of(n):
+        return torch.from_numpy(rng.standard_normal((2, n, heads, dim)).astype(np.float32)).to(dev)
+
+    def check():
+        table, lens = host(t.table), host(t.lens)
+        for r in range(rows):
+            pos = np.arange(lens[r])
+            slots = torch.from_numpy(table[r][pos // page].astype(np.int64) * page + pos % page).to(dev)
+            for got, h in zip(cf.kv8_read(cache, slots, torch.float32), held):
+                assert np.array_equal(host(got.double()), h[r].x), f"row {r}"
+
+    x = rows_of(64)
+    t, _ = cf.pages_resize(t, ints([64, 0, 0, 0], dev))
+    cf.kv8_append(cache, x[0], x[1], t.lens, table=t.table, starts=ints([0, 64, 64, 64, 64], dev))
+    t, src, dst, _ = cf.pages_fork(t, ints([0] * rows, dev))
+    for h, y in zip(held, x):
+        for r in range(rows):
+            h[r].append(host(y.double()))
+    check()
+    back, want = ints([0] * rows, dev), ints([0] * rows, dev)
+    x = rows_of(rows)
+    stay = ints(range(rows), dev)
+    a, b, c = (cf.PageTable(*(y.clone() for y in (t.refs, t.table, t.lens)), page) for _ in range(3))
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        cf.pages_resize(a, back, out=b)
+        _, src, dst, m1 = cf.pages_fork(b, stay, out=c, own=True)
+        cf.pages_copy(cache.data.flatten(1)[None], src, dst)
+        _, m2 = cf.pages_resize(c, want, out=a)
+        cf.kv8_append(cache, x[0], x[1], a.append_lens(want), table=a.table)
+    for lens in ([50, 47, 64, 33], [51, 20, 36, 34], [20, 20, 37, 35], [21, 21, 17, 17]):
+        back.copy_(ints(lens, dev)), want.copy_(ints([n + 1 for n in lens], dev))
+        x.copy_(rows_of(rows))
+        for h, y in zip(held, x):
+            for r, n in enumerate(lens):
+                n0 = len(h[r].x)
+                if n < n0:
+                    h[r].cut(n)
+                h[r].append(host(y[r:r + 1].double()))
+        g.replay()
+        torch.cuda.synchronize()
+        assert m1.item() == 0 and m2.item() == 0
+        t = a
+        check()
+        assert all(host(t.refs)[p] == 1 for p in host(t.table)[np.arange(rows), (host(t.lens) - 1) // page])

@@ -290,3 +290,14 @@ def test_lengths_of_an_append_behind_a_short_resize(cf):
     t.lens.copy_(torch.tensor([17, 16, 0, 5]))
     got = t.append_lens(torch.tensor([17, 17, 0, -1], dtype=torch.int32))
     assert got.tolist() == [17, 0, 0, 0] and got.dtype == torch.int32
+
+
+def test_fork_own_refusals(cf, L, monkeypatch):
+    """All that a fork refuses."""
+    monkeypatch.setattr(cf.lib, "cf_pages_fork", cf.lib.cf_pages_fork_own)
+    test_pages_refusals(cf, L, "fork")
+    import torch
+
+    t = cf.PageTable.create(8, 2, 3, 16, device="cpu")
+    with pytest.raises(ValueError, match="device tensors"):
+        cf.pages_fork(t, torch.zeros(2, dtype=torch.int32), own=True)

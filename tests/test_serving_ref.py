@@ -93,3 +93,45 @@ def test_pages_stay_counted(seed):
         refs, table, pairs = ref.compact(refs, table)
         assert refs == ref.count_refs(pages, table, lens, page)
         assert all(c > 0 for c in refs[:sum(1 for c in refs if c)])
+
+
+def last_pages(table, lens, page):
+    """(row, page) of the last, partly filled ones."""
+    return [(r, t[n // page]) for r, (t, n) in enumerate(zip(table, lens)) if n % page]
+
+
+@pytest.mark.parametrize("seed", range(30))
+def test_a_fork_parts_rows_that_shrank_into_a_page(seed):
+    rng = np.random.default_rng(1000 + seed)
+    page, rows, width = int(rng.choice([1, 3, 16])), int(rng.integers(1, 9)), int(rng.integers(1, 7))
+    pages = int(rng.integers(1, rows * width + 5))
+    refs, table, lens = random_state(rng, pages, rows, width, page)
+    for _ in range(6):
+        want = [int(rng.integers(-1, width * page + 2)) for _ in range(rows)]
+        refs, table, lens, _ = ref.resize(refs, table, lens, page, want)
+        parents = [int(rng.integers(-1, rows)) if rng.random() < 0.5 else r for r in range(rows)]
+        old, o_lens = [list(t) for t in table], lens
+        refs, table, lens, src, dst, missing = ref.fork_own(refs, table, lens, page, parents)
+        assert refs == ref.count_refs(pages, table, lens, page)
+        assert all(refs[p] == 1 for _, p in last_pages(table, lens, page))
+        assert not set(dst) & set(src) - {-1} and all(refs[s] > 0 for s in src if s >= 0)
+        back = {d: s for s, d in zip(src, dst) if d >= 0}
+        for r, p in enumerate(parents):
+            n = -(-lens[r] // page)
+            assert lens[r] == (o_lens[p] if p >= 0 else 0) or lens[r] == o_lens[p] // page * page
+            assert [back.get(x, x) for x in table[r][:n]] == old[p][:n] if p >= 0 else n == 0
+        assert missing == sum(1 for n, p in zip(lens, parents) if p >= 0 and n != o_lens[p])
+
+
+def test_rows_that_shrank_share_a_page_until_they_are_parted():
+    # two beams of 48 tokens, all pages shared, go back to 20 and 25 tokens
+    refs, table, lens = [2, 2, 2, 0, 0], [[0, 1, 2], [0, 1, 2]], [48, 48]
+    refs, table, lens, _ = ref.resize(refs, table, lens, 16, [20, 25])
+    same = ref.fork(refs, table, lens, 16, [0, 1])
+    assert last_pages(same[1], same[2], 16) == [(0, 1), (1, 1)]  # both would write into page 1
+    refs, table, lens, src, dst, missing = ref.fork_own(refs, table, lens, 16, [0, 1])
+    assert (refs, table, lens, src, dst, missing) == ([2, 1, 1, 0, 0], [[0, 1, -1], [0, 2, -1]], [20, 25], [-1, 1], [-1, 2], 0)
+    # where a third row goes on past the page, both get another
+    refs, table, lens, _ = ref.resize([3, 3, 3, 0, 0], [[0, 1, 2]] * 3, [48] * 3, 16, [20, 25, -1])
+    refs, table, lens, src, dst, missing = ref.fork_own(refs, table, lens, 16, [0, 1, 2])
+    assert (refs, table, src, dst, missing) == ([3, 1, 1, 1, 1], [[0, 3, -1], [0, 4, -1], [0, 1, 2]], [1, 1, -1], [3, 4, -1], 0)
