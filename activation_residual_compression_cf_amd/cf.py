@@ -151,18 +151,28 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(int(stream))
 
 
-def _keep_for(t: torch.Tensor | None, stream) -> torch.Tensor | None:
-    """Tie a buffer this module allocated (on the current stream) to the launch stream.
-    PyTorch's caching allocator may hand a freed block to new work on the stream it was
-    allocated on at once; when the kernels run on another stream, record_stream makes it
-    wait for that stream's work first."""
-    if t is None or stream is None:
-        return t
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream))
-    if stream.cuda_stream != torch.cuda.current_stream().cuda_stream:
-        t.record_stream(stream)
-    return t
+def _allocate(make, stream, returned: bool = True):
+    """make(), one buffer or several, for the launch stream to write.
+
+    PyTorch's caching allocator hands a freed block to the stream it was allocated on, behind that stream's work and no
+    other's.  A block of the caller's stream may still be written by what is queued there, which the launch stream does
+    not wait for, so the buffer comes from the launch stream's own blocks: what used it before is done when the
+    launch gets there.  Of a buffer that the caller gets, the caller's stream is on record too, so that the block is not
+    reused before the work that is queued there when it is freed.  One that is freed when the call returns needs
+    no more."""
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream))
+        here = torch.cuda.current_stream()
+        if stream.cuda_stream != here.cuda_stream:
+            with torch.cuda.stream(stream):
+                made = make()
+            if returned:
+                for t in made if isinstance(made, tuple) else (made,):
+                    if t is not None:
+                        t.record_stream(here)
+            return made
+    return make()
 
 
 def _act_dtype(a: torch.Tensor) -> int:
@@ -219,9 +229,9 @@ def compress(bits: int, a: torch.Tensor, ahat: torch.Tensor, err: torch.Tensor |
     err None skips the (diagnostic) error buffer."""
     n = a.numel()
     if codes is None:
-        codes = _keep_for(torch.empty(max(n * bits // 8, 0), dtype=torch.uint8, device=a.device), stream)
+        codes = _allocate(lambda: torch.empty(max(n * bits // 8, 0), dtype=torch.uint8, device=a.device), stream)
     if scales is None:
-        scales = _keep_for(torch.empty(max(n // GROUP, 0), dtype=torch.float32, device=a.device), stream)
+        scales = _allocate(lambda: torch.empty(max(n // GROUP, 0), dtype=torch.float32, device=a.device), stream)
     for nm, t, dt in (("ahat", ahat, _F32), ("err", err, _F32), ("codes", codes, _U8), ("scales", scales, _F32)):
         _dtype(nm, t, dt)
     for nm, t, nb in (("ahat", ahat, 4 * n), ("err", err, 4 * n), ("codes", codes, n * bits // 8),
@@ -257,9 +267,9 @@ def compress_ablation(mode: int, bits: int, a: torch.Tensor, ahat: torch.Tensor,
     """Ablation sender step (CF_MODE_NOEF needs a_prev); returns (codes, scales)."""
     n = a.numel()
     if codes is None:
-        codes = _keep_for(torch.empty(n * bits // 8, dtype=torch.uint8, device=a.device), stream)
+        codes = _allocate(lambda: torch.empty(n * bits // 8, dtype=torch.uint8, device=a.device), stream)
     if scales is None:
-        scales = _keep_for(torch.empty(n // GROUP, dtype=torch.float32, device=a.device), stream)
+        scales = _allocate(lambda: torch.empty(n // GROUP, dtype=torch.float32, device=a.device), stream)
     for nm, t, dt in (("ahat", ahat, _F32), ("a_prev", a_prev, a.dtype), ("codes", codes, _U8),
                       ("scales", scales, _F32)):
         _dtype(nm, t, dt)
@@ -277,9 +287,9 @@ def topk_compress(k: int, a: torch.Tensor, ahat: torch.Tensor, err: torch.Tensor
     """One top-k sender step; returns (idx uint8[numel/128*k], vals bf16 bits int16[numel/128*k])."""
     slots = max(a.numel() // GROUP * k, 0)
     if idx is None:
-        idx = _keep_for(torch.empty(slots, dtype=torch.uint8, device=a.device), stream)
+        idx = _allocate(lambda: torch.empty(slots, dtype=torch.uint8, device=a.device), stream)
     if vals is None:
-        vals = _keep_for(torch.empty(slots, dtype=torch.int16, device=a.device), stream)
+        vals = _allocate(lambda: torch.empty(slots, dtype=torch.int16, device=a.device), stream)
     n = a.numel()
     for nm, t, dts in (("ahat", ahat, (_F32,)), ("err", err, (_F32,)), ("idx", idx, (_U8,)), ("vals", vals, _BITS16)):
         _dtype(nm, t, *dts)
@@ -435,12 +445,12 @@ def lowrank_compress(a: torch.Tensor, ahat: torch.Tensor, err: torch.Tensor | No
     (u, u_scales, v, v_scales).  q_state is (batch, n, rank) fp32, updated in place."""
     batch, m, n = a.shape
     if payload is None:
-        payload = tuple(_keep_for(t, stream) for t in lowrank_payload(batch, m, n, rank, factor_bits, a.device))
+        payload = _allocate(lambda: lowrank_payload(batch, m, n, rank, factor_bits, a.device), stream)
     u, us, v, vs = payload
     need = lowrank_workspace_bytes(m, n, rank, batch)
     if workspace is None:
         # freed when this call returns, possibly before the launch stream has used it
-        workspace = _keep_for(torch.empty(need, dtype=torch.uint8, device=a.device), stream)
+        workspace = _allocate(lambda: torch.empty(need, dtype=torch.uint8, device=a.device), stream, False)
     _check_lowrank_buffers(batch, m, n, rank, factor_bits, payload)
     numel = batch * m * n
     for nm, t in (("ahat", ahat), ("err", err), ("q_state", q_state)):
@@ -550,14 +560,14 @@ def _on(stream, dev: int):
 
 
 def _like(t: torch.Tensor, stream) -> torch.Tensor:
-    o = torch.empty_like(t)
-    return o if stream is None else _keep_for(o, stream)
+    return torch.empty_like(t) if stream is None else _allocate(lambda: torch.empty_like(t), stream)
 
 
-def _new(like: torch.Tensor, shape, stream, dtype: torch.dtype | None = None) -> torch.Tensor:
+def _new(like: torch.Tensor, shape, stream, dtype: torch.dtype | None = None, returned: bool = True) -> torch.Tensor:
     """A buffer for the launch stream to write."""
-    t = like.new_empty(shape, dtype=dtype)
-    return t if stream is None else _keep_for(t, stream)
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    return _allocate(lambda: like.new_empty(shape, dtype=dtype), stream, returned)
 
 
 def qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, norm: int = CF_NORM_RMS,
@@ -861,7 +871,7 @@ def _workspace(workspace_bytes, dt, q, most, heads, kv_heads, workspace, dev, st
         if not need or not q.shape[0]:
             return None, None, 0
         # freed when the call returns, possibly before the launch stream has used it
-        workspace = _new(q, need, stream, _U8)
+        workspace = _new(q, need, stream, _U8, False)
         return workspace, workspace.data_ptr(), need
     return workspace, _flat("workspace", workspace, dev, workspace.dtype, workspace.shape), workspace.numel() * workspace.element_size()
 
@@ -917,7 +927,7 @@ def _pages_call(fn: str, have: PageTable, out: PageTable | None, workspace, stre
         pout = pin if out is have else out._pages("out", dev, shape)
     need = lib.cf_pages_workspace_bytes(shape[0], rows)
     if workspace is None:
-        workspace = _new(have.table, max(need, 4) // 4, stream)
+        workspace = _new(have.table, max(need, 4) // 4, stream, returned=False)
         ws = (workspace.data_ptr(), need)
     else:
         ws = (_flat("workspace", workspace, dev, workspace.dtype, workspace.shape), workspace.numel() * workspace.element_size())

@@ -133,3 +133,53 @@ def test_slab_calls_over_two_streams_match_one_stream(cf):
         out.append([x.cpu() for x in (slab.ahat, slab.err, slab.codes, slab.scales)])
     for x, y in zip(*out):
         assert torch.equal(x, y)
+
+
+def test_work_queued_on_the_callers_stream_does_not_reach_a_calls_buffers(cf):
+    """Blocks that the caller's stream is still to write are freed right before calls on a side stream allocate their
+    results and workspaces."""
+    dev = cf.require_device()
+    say("calls on a side stream behind late work of the caller's")
+    g = torch.Generator(device="cuda").manual_seed(4)
+    q, k, v = (torch.randn(n, h, 128, generator=g, device=dev).bfloat16() for n, h in ((300, 8), (900, 2), (900, 2)))
+    cache = cf.KV8Cache.create(60, 16, 2, 128)
+    lens, slots = torch.tensor([900], dtype=torch.int32, device=dev), torch.arange(900, device=dev)
+    cf.kv8_append(cache, k, v, lens, table_width=60)
+    pt = cf.PageTable.create(60, 4, 30, 16)
+    want = torch.tensor([100, 200, 33, 0], dtype=torch.int32, device=dev)
+    a = torch.randn(1, 256, 256, generator=g, device=dev)
+    basis = torch.randn(1, 256, 8, generator=g, device=dev)
+
+    def all_calls(stream):
+        ah, basis_of = a * 0.5, basis.clone()
+        torch.cuda.synchronize()
+        late()
+        out = [cf.attention(q, k, v, causal=True, stream=stream)]
+        late()
+        out += [cf.kv8_attention(q[:1], cache, lens, table_width=60, stream=stream)]
+        late()
+        out += cf.kv8_read(cache, slots, stream=stream)
+        late()
+        t, missing = cf.pages_resize(pt, want, stream=stream)
+        out += [t.refs, t.table, t.lens, missing]
+        late()
+        out += cf.lowrank_compress(a, ah, None, basis_of, 8, 2, 4, stream=stream)
+        torch.cuda.synchronize()
+        return out
+
+    big = torch.empty(1 << 28, device=dev)
+    sizes = [q.numel() * 2, k.numel() * 2, 8 * 128 * 2, 16, 240, 480, 512, cf.attention_workspace_bytes(torch.bfloat16, 300, 8, 2, 128),
+             cf.kv8_attention_workspace_bytes(torch.bfloat16, 1, 8, 2, 128), cf.lowrank_workspace_bytes(256, 256, 8, 1), 256 * 4, 32]
+
+    def late():
+        for _ in range(8):
+            big.mul_(1.0)  # a third of a millisecond each
+        junk = [torch.empty(n, dtype=torch.uint8, device=dev).fill_(0x7F) for n in sizes for _ in range(3)]
+        del junk
+
+    expect = all_calls(None)
+    side = torch.cuda.Stream()
+    for _ in range(2):
+        got = all_calls(side)
+        for x, y in zip(got, expect):
+            assert torch.equal(x, y)
