@@ -230,3 +230,39 @@ def fork_own(refs, table, lens, page, parents):
             size[r] = size[r] // page * page
             missing += 1
     return refs, [h + [-1] * (width - len(h)) for h in new], size, src, dst, missing
+
+
+# ---- rounding by rounding
+
+def one_key(q, k, v, scale):
+    """(out, lse, bound of out, bound of lse) of rows (n, D) that see one key each, fp32 operands of which q and k have one
+    channel that is not zero, |score| at least 64 and scale a power of two: few roundings, so that products of
+    parts that are left out show.  In units of 2^-24 of the value:
+      score: 1 of what six products leave out, 2 of the last sum (the sums before it are 2^-8 of it), 2 of scale * log2 e
+      lse: the score, 1 of m + log2 p, 2 of the product with ln 2, and 8 of a unit (p's exponent below one, exp2 and log2 within 2 of
+           their last places each), an eighth of one of 64
+      out: 1 of what is left out, 2 of the last sum, 2 of the reciprocal of p, 1 of the product with it"""
+    q, k, v = (np.asarray(x, np.float64) for x in (q, k, v))
+    lse = (q * k).sum(-1) * scale
+    assert (np.abs(lse) >= 64).all()
+    return v, lse, 6 * attn_ref.F24 * np.abs(v), 9 * attn_ref.F24 * np.abs(lse)
+
+
+def one_key_rows(rng, n, dim):
+    """q, k, v (n, dim) fp32 for it, with a score of 64 to 256 at a scale of 1/4 whose parts are all there."""
+    q, k = (np.zeros((n, dim), np.float32) for _ in range(2))
+    at = np.arange(n), np.arange(n) % dim
+    q[at], k[at] = (rng.uniform(16, 32, n).astype(np.float32) * rng.choice([-1, 1], n).astype(np.float32) for _ in range(2))
+    return q, k, (rng.uniform(1, 2, (n, dim)) * rng.choice([-1, 1], (n, dim))).astype(np.float32)
+
+
+def two_keys(x, p_step):
+    """(out, bound) of rows of bf16 that see a key of score 0 and value 1 and one of score x, at most an eighth, and value -1:
+    the values all but cancel, so that the probabilities' rounding shows beside the result's.  A probability is off by at
+    most p_step of the larger of the two."""
+    x = np.asarray(x, np.float64)
+    assert (np.abs(x) <= 0.125).all()
+    w = 1 / (1 + np.exp(-np.abs(x)))
+    out = -np.tanh(x / 2)
+    # fp32: a handful of roundings of numbers up to one
+    return out, 2 * w * p_step + attn_ref.HALF_STEP["bf16"] * np.abs(out) + 16 * attn_ref.F24

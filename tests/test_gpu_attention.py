@@ -352,3 +352,23 @@ def test_decoded_shards(cf, dev):
     torch.cuda.synchronize()
     want = ref.attention(host(q.double()), host(kv[0].double()), host(kv[1].double()), d ** -0.5, False, 0, ref.P_BF16)
     compare(host(out.double()), host(lse.double()), *want, "shard")
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("alone", [True, False])
+def test_no_product_of_fp32_parts_is_left_out(cf, dev, dim, alone):
+    """Rows that see one key, in sequences of one token or through a window: nothing hides what a product adds."""
+    say(f"attention fp32, one key a row, dim={dim} alone={alone}")
+    n = 300
+    x = ref.one_key_rows(np.random.default_rng(dim), n, dim)
+    want = ref.one_key(*x, 0.25)
+    q, k, v = (torch.from_numpy(y).to(dev)[:, None] for y in x)
+    lse = torch.full((n, 1), CANARY, device=dev)
+    if alone:
+        starts = torch.arange(n + 1, dtype=torch.int32, device=dev)
+        out = cf.attention(q, k, v, q_starts=starts, k_starts=starts, max_q=1, scale=0.25, lse=lse)
+    else:
+        out = cf.attention(q, k, v, causal=True, window=1, scale=0.25, lse=lse)
+    torch.cuda.synchronize()
+    for got, y, b in ((host(out[:, 0].double()), want[0], want[2]), (host(lse[:, 0].double()), want[1], want[3])):
+        assert (np.abs(got - y) <= b).all(), f"{(np.abs(got - y) / b).max():.3g} of the bound"

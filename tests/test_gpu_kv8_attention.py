@@ -374,3 +374,51 @@ def test_two_graphs_share_a_workspace(cf, dev):
             want = cf.kv8_attention(c.q, c.cache, c.lens, table=c.table, q_starts=c.q_starts, max_q=n, causal=True)
             torch.cuda.synchronize()
             assert torch.equal(o, want), f"replay {i}"
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("max_q", [1, 17, 33])  # each kernel
+def test_fp32_queries_and_probabilities_are_whole(cf, dev, dim, max_q):
+    """Sequences of one key, which the cache holds exactly: every part of a query and of a probability shows."""
+    say(f"kv8 attention fp32, one key a row, dim={dim} max_q={max_q}")
+    rng = np.random.default_rng(dim + max_q)
+    n = 300
+    q, k, v = ref.one_key_rows(rng, n, dim)
+    k = np.sign(k) * (16 + 2 * rng.integers(0, 8, (n, 1))).astype(np.float32)  # numbers of three binary places
+    v = np.sign(v) * (1 + rng.integers(0, 8, v.shape) / 8).astype(np.float32)
+    want = ref.one_key(q, k, v, 0.25)
+    cache = cf.KV8Cache.create(n, 16, 1, dim)
+    lens = torch.ones(n, dtype=torch.int32, device=dev)
+    q, k, v = (torch.from_numpy(x).to(dev)[:, None] for x in (q, k, v))
+    cf.kv8_append(cache, k, v, lens, table_width=1)
+    kk, vv = cf.kv8_read(cache, torch.arange(n, device=dev) * 16, torch.float32)
+    starts = torch.arange(n + 1, dtype=torch.int32, device=dev)
+    lse = torch.full((n, 1), CANARY, device=dev)
+    out = cf.kv8_attention(q, cache, lens, q_starts=starts, max_q=max_q, scale=0.25, table_width=1, lse=lse)
+    torch.cuda.synchronize()
+    assert torch.equal(kk, k) and torch.equal(vv, v)
+    for got, y, b in ((host(out[:, 0].double()), want[0], want[2]), (host(lse[:, 0].double()), want[1], want[3])):
+        assert (np.abs(got - y) <= b).all(), f"{(np.abs(got - y) / b).max():.3g} of the bound"
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("max_q,p_step", [(1, ref.P_FP16), (17, ref.P_FP16), (33, ref.P_BF16)])
+def test_probabilities_are_as_exact_as_stated(cf, dev, dim, max_q, p_step):
+    """bf16 rows whose two values all but cancel: fp16 probabilities in calls of at most 32 rows."""
+    say(f"kv8 attention bf16, two keys a row, dim={dim} max_q={max_q}")
+    n = 300
+    x = torch.from_numpy(np.random.default_rng(dim).uniform(-0.125, 0.125, n)).to(torch.bfloat16)
+    want, bound = ref.two_keys(x.double().numpy(), p_step)
+    k, v = torch.zeros(2, n, 2, 1, dim, device=dev)
+    k[:, 1, 0, 0] = 1
+    v[:, 0], v[:, 1] = 1, -1
+    cache = cf.KV8Cache.create(n, 16, 1, dim)
+    lens = torch.full((n,), 2, dtype=torch.int32, device=dev)
+    cf.kv8_append(cache, k.flatten(0, 1), v.flatten(0, 1), lens, table_width=1)
+    q = torch.zeros(n, 1, dim, dtype=torch.bfloat16, device=dev)
+    q[:, 0, 0] = x.to(dev)
+    starts = torch.arange(n + 1, dtype=torch.int32, device=dev)
+    out = cf.kv8_attention(q, cache, lens, q_starts=starts, max_q=max_q, scale=1.0, table_width=1)
+    torch.cuda.synchronize()
+    far = np.abs(host(out[:, 0].double()) - want[:, None])
+    assert (far <= bound[:, None]).all(), f"{(far / bound[:, None]).max():.3g} of the bound"

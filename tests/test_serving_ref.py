@@ -135,3 +135,60 @@ def test_rows_that_shrank_share_a_page_until_they_are_parted():
     refs, table, lens, _ = ref.resize([3, 3, 3, 0, 0], [[0, 1, 2]] * 3, [48] * 3, 16, [20, 25, -1])
     refs, table, lens, src, dst, missing = ref.fork_own(refs, table, lens, 16, [0, 1, 2])
     assert (refs, table, src, dst, missing) == ([3, 1, 1, 1, 1], [[0, 3, -1], [0, 4, -1], [0, 1, 2]], [1, 1, -1], [3, 4, -1], 0)
+
+
+def bf16(x):
+    import torch
+
+    return torch.from_numpy(np.array(x, np.float32)).bfloat16().float().numpy()
+
+
+def parts(x):
+    x = np.asarray(x, np.float32)
+    a = bf16(x)
+    b = bf16(x - a)
+    return a, b, bf16(x - a - b)
+
+
+SIX = ((1, 1), (0, 2), (2, 0), (0, 1), (1, 0), (0, 0))
+
+
+def by_parts(x, y, products):
+    x, y, total = parts(x), parts(y), np.float32(0)
+    for i, j in products:
+        total = total + x[i] * y[j]  # a product of two bf16 numbers is one of fp32
+    return total
+
+
+@pytest.mark.parametrize("score,value,fits", [
+    (SIX, SIX, True),
+    (SIX[1:], SIX, False), (SIX, SIX[1:], False),                # without the product of the second parts
+    (SIX[:1] + SIX[2:], SIX, False), (SIX, SIX[:2] + SIX[3:], False),
+    (SIX[3:], SIX, False), (SIX, SIX[3:], False), (SIX[5:], SIX[5:], False)])
+def test_products_that_are_left_out_show(score, value, fits):
+    """The kernels' arithmetic for fp32 rows that see one key, in numpy's fp32, with all of the products and fewer."""
+    q, k, v = ref.one_key_rows(np.random.default_rng(3), 400, 64)
+    out, lse, b_out, b_lse = ref.one_key(q, k, v, 0.25)
+    f = np.float32
+    s = np.stack([by_parts(q[:, c], k[:, c], score) for c in range(64)], 1).sum(1, dtype=f)
+    log2e = f(0.25) * f(1.44269504088896341)
+    m = np.ceil(s * log2e)
+    p = np.exp2((s.astype(np.float64) * log2e - m).astype(f)).astype(f)
+    got_lse = (m + np.log2(p)) * f(0.693147180559945309)
+    got = by_parts(np.broadcast_to(p[:, None], v.shape), v, value) * (f(1) / p)[:, None]
+    assert got.dtype == got_lse.dtype == f
+    off_lse, off = np.abs(got_lse - lse) / b_lse, np.abs(got - out) / b_out
+    assert ((off_lse <= 1).all() and (off <= 1).all()) == fits
+    if score != SIX:
+        assert off_lse.max() > 4
+    if value != SIX:
+        assert off.max() > 4
+
+
+def test_probabilities_in_bf16_show():
+    x = bf16(np.random.default_rng(4).uniform(-0.125, 0.125, 300))
+    out, bound = ref.two_keys(x, ref.P_FP16)
+    p = np.exp(np.stack([0 * x, x]) - np.maximum(x, 0)).astype(np.float32) * 128
+    for rounded, fits in ((p.astype(np.float16).astype(np.float32), True), (bf16(p), False)):
+        got = bf16((rounded[0] - rounded[1]) / p.sum(0))
+        assert (np.abs(got - out) <= bound).all() == fits
