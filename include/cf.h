@@ -391,7 +391,10 @@ size_t cf_kv4_attention_workspace_bytes(int a_dtype, int64_t max_q, int q_heads,
  *   where the block's first token is not among those that come: no less than the block's e before; if that grows, the
  *     codes before those that come are rounded again, from what they stand for, as below;
  *   byte = e + 127;  code = the nearest to x * 2^-e, ties to the even code, 448 above 448; 127 for NaN and infinities
- * So values are held with an error of at most 2^-4 of themselves or 2^(e - 10), and magnitudes beyond 448 * 2^7 saturate.
+ * So values are held with an error of at most 2^-4 of themselves or 2^(e - 10), e being their block's when they came, and
+ * magnitudes beyond 448 * 2^7 saturate.  All that later calls raise a block's scale by costs values that it held at
+ * most 2^(e - 9) more, e being the block's then: each raise rounds them again, with an error only where they fall among the
+ * scale's smallest.
  * Places of a block behind the tokens that came hold nothing.  Rows with no place (kv_lens[b] is less than their number,
  * a page outside the cache, rows of no sequence) are not kept.  A kv_lens beyond the table's pages is cut to them, and the rows
  * then take their last places.  Sequences of a call must not share a page that gets tokens.

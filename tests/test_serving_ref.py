@@ -192,3 +192,34 @@ def test_probabilities_in_bf16_show():
     for rounded, fits in ((p.astype(np.float16).astype(np.float32), True), (bf16(p), False)):
         got = bf16((rounded[0] - rounded[1]) / p.sum(0))
         assert (np.abs(got - out) <= bound).all() == fits
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_what_is_held_is_within_the_stated_error(seed):
+    """At most 2^-4 of a value or 2^(e - 10) at the scale that it came at; raises add less than 2^(e - 9) at the last."""
+    rng = np.random.default_rng(seed)
+    raised = again = 0
+    for _ in range(200):
+        h, x, first = ref.Held(1, 8), [], []
+        while len(x) < ref.BLOCK:
+            n = min(int(rng.integers(1, 4)), ref.BLOCK - len(x))
+            new = rng.standard_normal((n, 1, 8)) * 2.0 ** rng.uniform(-10, -8 + len(x))
+            h.append(new)
+            x += list(new)
+            first += [int(h.e[0, 0])] * n
+        x, first, last = np.array(x), np.array(first)[:, None, None], int(h.e[0, 0])
+        far = np.abs(h.x - x)
+        once = np.maximum(2.0 ** -4 * np.abs(x), 2.0 ** (first - 10))
+        assert (far <= once + np.where(first < last, 2.0 ** (last - 9), 0)).all()
+        raised += (first < last).sum()
+        again += (far > np.maximum(2.0 ** -4 * np.abs(x), 2.0 ** (last - 10))).sum()
+    assert raised and again  # the last scale alone does not bound it
+
+
+def test_a_raise_adds_to_the_error():
+    u = 2.0 ** -9  # the last scale's smallest step
+    h = ref.Held(1, 1)
+    h.append(np.array([[[448 / 2]], [[3.3 * u]]]))
+    assert h.e[0, 0] == -1 and h.x[1, 0, 0] == 3.5 * u
+    h.append(np.array([[[448.0]]]))
+    assert h.e[0, 0] == 0 and h.x[1, 0, 0] == 4 * u  # 0.7 steps off
