@@ -978,7 +978,8 @@ def pages_fork(have: PageTable, parents: torch.Tensor, out: PageTable | None = N
 def pages_compact(have: PageTable, out: PageTable | None = None, src: torch.Tensor | None = None, dst: torch.Tensor | None = None,
                   count: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
     """The pages that are held become the first ones.  Returns (out, src, dst, count): the first count (1,) of src and dst
-    (pages / 2 each) are the pages to copy, with pages_copy in every cache.  out may be `have`."""
+    (pages / 2 each) are the pages to copy, with pages_copy in every cache.  Every entry of the table is renumbered, behind a
+    row's last page too.  out may be `have`."""
     pin, pout, out, shape, ws, dev, workspace = _pages_call("cf_pages_compact", have, out, workspace, stream)
     src, p1 = _words(have.table, shape[0] // 2, src, "src", dev, stream)
     dst, p2 = _words(have.table, shape[0] // 2, dst, "dst", dev, stream)

@@ -451,8 +451,9 @@ size_t cf_attention_workspace_bytes(int a_dtype, int64_t max_q, int q_heads, int
  * Who holds which page of a cache.  `rows` sequences of up to `width` pages of page_size tokens: row r has lens[r] tokens
  * in pages table[r * width] .. ; refs[p] counts the entries that hold page p, and a page with 0 is free.  The same
  * three arrays serve every cache whose pages they number (4 or 8 bits, each layer's).  The calls below read `in` and write
- * `out`; entries behind a row's last page are written as -1.  Entries that are no page of the cache are handed on and counted
- * nowhere, and lens are taken within [0, width * page_size].  refs not less than 0.
+ * `out`.  Resize and the forks take lens within [0, width * page_size] and write entries behind a row's last page as -1;
+ * compact, which has no page size, looks at no length: it hands on lens, and every entry, under its page's new number.
+ * Entries that are no page of the cache are handed on and counted nowhere.  refs not less than 0.
  *
  * cf_pages_resize: row r gets want[r] tokens (negative: it stays as it is).  First rows that shrink let go the pages they
  *   no longer need (all of them at 0 tokens); then those that grow, in the order of rows, take free pages in the order of
@@ -473,7 +474,7 @@ size_t cf_attention_workspace_bytes(int a_dtype, int64_t max_q, int q_heads, int
  *   parents[r] = r it is the call behind a cf_pages_resize that may have shrunk rows so.
  * cf_pages_compact: the pages that are held are made the first ones: the k-th of those behind, page src[k], goes to the
  *   k-th free one before, dst[k], for cf_pages_copy; refs and every table entry follow.  count: how many; src and dst have
- *   pages / 2 places, the rest -1.  lens stay.
+ *   pages / 2 places, the rest -1.
  *   out may be in, array by array, for resize and compact; the forks' table and lens must be other arrays.
  *   want, parents: rows int32;  src, dst: rows int32 (fork), pages / 2 (compact);  missing, count: one int32.
  *   workspace: cf_pages_workspace_bytes, 4-byte aligned.

@@ -483,3 +483,17 @@ def test_beams_that_go_back(cf, dev):
         t = a
         check()
         assert all(host(t.refs)[p] == 1 for p in host(t.table)[np.arange(rows), (host(t.lens) - 1) // page])
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+def test_compact_renumbers_entries_behind_the_last_page(cf, dev, in_place):
+    """Entries that a length has left behind, of pages that move, that are free and of none, and lengths of any size."""
+    say("pages compact: stale entries")
+    refs = [0, 1, 0, 0, 2, 0, 1, 1]
+    table, lens = [[4, 7, 1], [4, 6, 3], [1, -1, 8], [7, 0, 5]], [16, 32, 10 ** 6, -4]
+    t = put(cf, dev, refs, table, lens, 16)
+    got, src, dst, count = cf.pages_compact(t, out=t if in_place else None)
+    r, ta, pairs = ref.compact(refs, table)
+    assert pairs == [(4, 0), (6, 2), (7, 3)] and ta == [[0, 3, 1], [0, 2, 3], [1, -1, 8], [3, 0, 5]]
+    same(got, r, ta, lens)
+    assert count.item() == 3
