@@ -216,11 +216,11 @@ template <typename T, int D, typename F>
 auto with_kernel(int64_t max_rows, F f) {
     if constexpr (sizeof(T) == 2) {
         if (max_rows > 128) {
-            using K = Tile<RowSource<T, D, 8>, 1>;
+            using K = Tile<RowSource<T, D, 8>>;
             return f(K(), tile_kernel<K>);
         }
     }
-    using K = Tile<RowSource<T, D, 4>, 1>;
+    using K = Tile<RowSource<T, D, 4>>;
     return f(K(), tile_kernel<K>);
 }
 

@@ -8,20 +8,19 @@
 namespace cf {
 namespace {
 
-// Shape of a kernel: source SRC with its types, RB blocks of 32 rows a wave, work-groups of a compute unit.
+// Shape of a kernel: source SRC with its types, 32 rows a wave.
 //
 // What a wave does with 32 keys and 32 rows (matrix products of 32 x 32 with 16 terms; lane = 32 h + n):
 //   S^T = K Q^T   K's rows are keys, in such an order that lane (h, n) ends up with the scores of keys 8 h .. 8 h + 7
 //                 and 16 + 8 h .. for row n
 //   O^T = V^T P^T the terms are keys: the lane has them.
-template <typename SRC, int RB>
+template <typename SRC>
 struct Tile {
     static constexpr int kGroup = 64 * SRC::kWaves;  // threads
     using Source = SRC;
     using Type = typename SRC::Type;
     static constexpr int kDim = SRC::kDim;
-    static constexpr int kRB = RB;
-    static constexpr int kRows = 32 * RB * SRC::kWaves;
+    static constexpr int kRows = 32 * SRC::kWaves;
     static constexpr int kKeys = SRC::kKeys;  // of a tile: 32 or 64
     static constexpr int kSub = kKeys / 32;
     static constexpr int kPad = SRC::kPad;
@@ -94,7 +93,7 @@ template <typename K>
 __global__ __launch_bounds__(K::kGroup, K::kResident * K::Source::kWaves / 4) void tile_kernel(const typename K::Source::Args p) {
     using S = typename K::Source;
     using T = typename K::Type;
-    constexpr int D = K::kDim, RB = K::kRB, kRows = K::kRows, kKeys = K::kKeys, kSub = K::kSub, kPad = K::kPad;
+    constexpr int D = K::kDim, kRows = K::kRows, kKeys = K::kKeys, kSub = K::kSub, kPad = K::kPad;
     constexpr int QP = S::kQueryParts, KP = S::kKeyParts, kMost = (QP > KP ? QP : KP) - 1;
     constexpr int kC = D / 16, kDt = D / 32;
     constexpr int kProducts = KP == 1 ? QP : QP * (QP + 1) / 2, kBeside = KP == 1 ? 6 : 8;
@@ -120,7 +119,7 @@ __global__ __launch_bounds__(K::kGroup, K::kResident * K::Source::kWaves / 4) vo
         w.at += take;
         if (z <= 0) break;  // the next workgroup begins this item
         const int rows = s.nq * p.share;
-        const int row0 = w.tile * kRows + wave * 32 * RB;  // the wave's first
+        const int row0 = w.tile * kRows + wave * 32;  // the wave's first
         const int tiles = z - a, base = (u0 + a) * kKeys;   // the run's first key
 
         src.item(p, s, w.b, w.head, base);
@@ -128,11 +127,10 @@ __global__ __launch_bounds__(K::kGroup, K::kResident * K::Source::kWaves / 4) vo
 #pragma unroll
         for (int i = 0; i < S::kPieces; ++i) src.load(i);
 
-        vb8 q[RB][QP][kC];
-        int lo[RB], hi[RB];
-#pragma unroll
-        for (int b = 0; b < RB; ++b) {
-            const int row = row0 + 32 * b + n;
+        vb8 q[QP][kC];
+        int lo, hi;  // keys that the lane's row sees
+        {
+            const int row = row0 + n;
             const bool on = row < rows;
             const int token = on ? token_of(p, row) : 0, q_head = w.head * p.share + (on ? row - token * p.share : 0);
 #pragma unroll
@@ -147,29 +145,24 @@ __global__ __launch_bounds__(K::kGroup, K::kResident * K::Source::kWaves / 4) vo
                 for (int j = 0; j < 8; ++j) {
                     float rest = on ? f[j] : 0.f;
 #pragma unroll
-                    for (int k = 0; k < QP; ++k) q[b][k][c][j] = S::part(&rest);
+                    for (int k = 0; k < QP; ++k) q[k][c][j] = S::part(&rest);
                 }
             }
-            lo[b] = on ? seen_lo(p, s, token) : 0, hi[b] = on ? seen_hi(p, s, token) : 0;
+            lo = on ? seen_lo(p, s, token) : 0, hi = on ? seen_hi(p, s, token) : 0;
         }
         int full_lo = 0, full_hi = INT32_MAX;  // keys that all of the wave's rows see
-        const int row1 = min(row0 + 32 * RB, rows) - 1;
+        const int row1 = min(row0 + 32, rows) - 1;
         if (row1 >= row0) full_lo = seen_lo(p, s, token_of(p, row1)), full_hi = seen_hi(p, s, token_of(p, row0));
 
-        vf16 o[RB][kDt];
-        float m[RB], sum[RB];  // m: reference in units of log2
+        vf16 o[kDt];
+        // m: reference in units of log2; rows that see nothing have nothing to follow
+        float m = lo < hi ? kNone : 0.f, sum = 0.f;
 #pragma unroll
-        for (int b = 0; b < RB; ++b) {
-            m[b] = lo[b] < hi[b] ? kNone : 0.f, sum[b] = 0.f;  // rows that see nothing have nothing to follow
+        for (int j = 0; j < kDt; ++j)
 #pragma unroll
-            for (int j = 0; j < kDt; ++j)
-#pragma unroll
-                for (int k = 0; k < 16; ++k) o[b][j][k] = 0.f;
-        }
+            for (int k = 0; k < 16; ++k) o[j][k] = 0.f;
 
-        uint64_t bad[RB];  // the lane's channels (a bit for each of o) that an infinity or NaN of V has reached
-#pragma unroll
-        for (int b = 0; b < RB; ++b) bad[b] = 0;
+        uint64_t bad = 0;  // the lane's channels (a bit for each of o) that an infinity or NaN of V has reached
         int wg_lo = 0, wg_hi = INT32_MAX;  // keys that all of the item's rows see
         {
             const int r0 = w.tile * kRows, r1 = min(r0 + kRows, rows) - 1;
@@ -214,24 +207,20 @@ __global__ __launch_bounds__(K::kGroup, K::kResident * K::Source::kWaves / 4) vo
             if constexpr (S::kWaves > 4) flag |= static_cast<FlagWord>(static_cast<uint32_t>(uniform(static_cast<int>(*reinterpret_cast<const uint32_t*>(flags[buf] + 4))))) << 32;
             const bool edge = key0 < full_lo || key0 + kKeys > full_hi || S::none(flag) != 0;
 
-            vf16 x[kSub][RB];           // scores: r of half g is of key key0 + 32 g + 8 h + 16 (r / 8) + r % 8
-            vu4 pf[kSub][RB][2][QP];    // their probabilities: bf16 in pairs
-            float ref[RB], more[RB], before[RB];  // before: of more, what the first half gave
+            vf16 x[kSub];             // scores: r of half g is of key key0 + 32 g + 8 h + 16 (r / 8) + r % 8
+            vu4 pf[kSub][2][QP];      // their probabilities: bf16 in pairs
+            float ref, more, before;  // before: of more, what the first half gave
             const auto key_product = [&](int f) {
                 if (f % kC == 0)
 #pragma unroll
-                    for (int b = 0; b < RB; ++b)
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) x[f / kC][b][r] = 0.f;
+                    for (int r = 0; r < 16; ++r) x[f / kC][r] = 0.f;
                 fetch(f + kAhead, buf, next_buf);
 #pragma unroll
                 for (int i = kMost; i >= 0; --i)  // the smallest parts first
 #pragma unroll
                     for (int k = 0; k < KP; ++k) {
                         if (i - k < 0 || i - k >= QP) continue;
-#pragma unroll
-                        for (int b = 0; b < RB; ++b)
-                            x[f / kC][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ring[f % kRing][k], q[b][i - k][f % kC], x[f / kC][b], 0, 0, 0);
+                        x[f / kC] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ring[f % kRing][k], q[i - k][f % kC], x[f / kC], 0, 0, 0);
                     }
             };
             const auto value_product = [&](int v) {
@@ -241,44 +230,38 @@ __global__ __launch_bounds__(K::kGroup, K::kResident * K::Source::kWaves / 4) vo
 #pragma unroll
                     for (int k = 0; k < KP; ++k) {
                         if (i - k < 0 || i - k >= QP) continue;
-#pragma unroll
-                        for (int b = 0; b < RB; ++b)
-                            o[b][v % kDt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ring[(kKs + v) % kRing][k], __builtin_bit_cast(vb8, pf[v / (2 * kDt)][b][v / kDt % 2][i - k]),
-                                                                                    o[b][v % kDt], 0, 0, 0);
+                        o[v % kDt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                            ring[(kKs + v) % kRing][k], __builtin_bit_cast(vb8, pf[v / (2 * kDt)][v / kDt % 2][i - k]), o[v % kDt], 0, 0, 0);
                     }
             };
             // pairs i0 .. i1 - 1 of half g's probabilities
             const auto exps = [&](int g, int i0, int i1) {
 #pragma unroll
-                for (int i = i0; i < i1; ++i)
+                for (int i = i0; i < i1; ++i) {
+                    float e[2];
 #pragma unroll
-                    for (int b = 0; b < RB; ++b) {
-                        float e[2];
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            e[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[g][b][2 * i + j], p.scale_log2, ref[b]));
-                            more[b] += e[j];
-                        }
-                        here(more[b]);
-#pragma unroll
-                        for (int k = 0; k < QP; ++k) {
-                            const vb2 y = QP == 1 ? vb2{static_cast<__bf16>(e[0]), static_cast<__bf16>(e[1])} : vb2{S::part(&e[0]), S::part(&e[1])};
-                            uint32_t word = __builtin_bit_cast(uint32_t, y);
-                            here(word);
-                            pf[g][b][i / 4][k][i % 4] = word;
-                        }
+                    for (int j = 0; j < 2; ++j) {
+                        e[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[g][2 * i + j], p.scale_log2, ref));
+                        more += e[j];
                     }
+                    here(more);
+#pragma unroll
+                    for (int k = 0; k < QP; ++k) {
+                        const vb2 y = QP == 1 ? vb2{static_cast<__bf16>(e[0]), static_cast<__bf16>(e[1])} : vb2{S::part(&e[0]), S::part(&e[1])};
+                        uint32_t word = __builtin_bit_cast(uint32_t, y);
+                        here(word);
+                        pf[g][i / 4][k][i % 4] = word;
+                    }
+                }
             };
             // hides what rows do not see
             const auto mask = [&](int g) {
                 if (!edge) return;
 #pragma unroll
-                for (int b = 0; b < RB; ++b)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const int run = 2 * g + r / 8, key = key0 + 8 * h + 16 * run + r % 8;
-                        if ((S::none(flag) >> run & 1u) || key < lo[b] || key >= hi[b]) x[g][b][r] = kNone;
-                    }
+                for (int r = 0; r < 16; ++r) {
+                    const int run = 2 * g + r / 8, key = key0 + 8 * h + 16 * run + r % 8;
+                    if ((S::none(flag) >> run & 1u) || key < lo || key >= hi) x[g][r] = kNone;
+                }
             };
             // Moves the references up to half g's scores where a row sees its first key, or where its probabilities so far add
             // up to more than kRise: to whole numbers, so that what is moved with them stays as exact.
@@ -286,68 +269,49 @@ __global__ __launch_bounds__(K::kGroup, K::kResident * K::Source::kWaves / 4) vo
             // waits for a decision, and no maximum is taken; else they are made again.
             // Rows decide for themselves, so that none depends on those beside it.
             const auto settle = [&](int g, bool made) {
-                float top[RB];
-                bool rise[RB], any = false;
-                const auto largest = [&](int b) {
-                    top[b] = kNone;
+                float top;
+                const auto largest = [&]() {
+                    top = kNone;
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) top[b] = fmaxf(top[b], x[g][b][r]);
-                    top[b] *= p.scale_log2;
+                    for (int r = 0; r < 16; ++r) top = fmaxf(top, x[g][r]);
+                    top *= p.scale_log2;
                 };
+                if (!made) largest();
+                const bool rise = made ? m == kNone || more > kRise : top > m + kRiseLog2;
+                if (!__any(rise)) return;
+                if (made) largest();
+                // both lanes of a row, whatever either says
+                const int others = __shfl_xor(static_cast<int>(rise), 32, 64);
+                const float most = fmaxf(top, __shfl_xor(top, 32, 64));
+                const float r = rise | others ? fmaxf(__builtin_ceilf(most), m) : m;
+                const float f = m == r ? 1.f : __builtin_amdgcn_exp2f(m - r);
+                m = r;
+                sum *= f;
+                more = before * f;
 #pragma unroll
-                for (int b = 0; b < RB; ++b) {
-                    if (!made) largest(b);
-                    rise[b] = made ? m[b] == kNone || more[b] > kRise : top[b] > m[b] + kRiseLog2;
-                    any |= rise[b];
-                }
-                if (!__any(any)) return;
-#pragma unroll
-                for (int b = 0; b < RB; ++b) {
-                    if (made) largest(b);
-                    // both lanes of a row, whatever either says
-                    const int others = __shfl_xor(static_cast<int>(rise[b]), 32, 64);
-                    const float most = fmaxf(top[b], __shfl_xor(top[b], 32, 64));
-                    const float r = rise[b] | others ? fmaxf(__builtin_ceilf(most), m[b]) : m[b];
-                    const float f = m[b] == r ? 1.f : __builtin_amdgcn_exp2f(m[b] - r);
-                    m[b] = r;
-                    sum[b] *= f;
-                    more[b] = before[b] * f;
-#pragma unroll
-                    for (int j = 0; j < kDt; ++j) o[b][j] *= f;
-                    ref[b] = m[b] == kNone ? 0.f : -m[b];
-                }
+                for (int j = 0; j < kDt; ++j) o[j] *= f;
+                ref = m == kNone ? 0.f : -m;
                 if (made) exps(g, 0, 8);
             };
 
             // The same where the maximum is taken, for both halves of a tile at once: the first half's probabilities have been made.
-            float most[RB];
+            float most;
             const auto follow = [&](int g, int r0, int r1) {
 #pragma unroll
-                for (int b = 0; b < RB; ++b) {
-#pragma unroll
-                    for (int r = r0; r < r1; ++r) most[b] = fmaxf(most[b], x[g][b][r]);
-                    here(most[b]);
-                }
+                for (int r = r0; r < r1; ++r) most = fmaxf(most, x[g][r]);
+                here(most);
             };
             const auto settle_both = [&]() {
-                bool rise = false;
+                most *= p.scale_log2;
+                if (!__any(most > m + kRiseLog2)) return;
+                const float r = fmaxf(__builtin_ceilf(fmaxf(most, __shfl_xor(most, 32, 64))), m);
+                const float f = m == r ? 1.f : __builtin_amdgcn_exp2f(m - r);
+                m = r;
+                sum *= f;
+                more = 0.f;
 #pragma unroll
-                for (int b = 0; b < RB; ++b) {
-                    most[b] *= p.scale_log2;
-                    rise |= most[b] > m[b] + kRiseLog2;
-                }
-                if (!__any(rise)) return;
-#pragma unroll
-                for (int b = 0; b < RB; ++b) {
-                    const float r = fmaxf(__builtin_ceilf(fmaxf(most[b], __shfl_xor(most[b], 32, 64))), m[b]);
-                    const float f = m[b] == r ? 1.f : __builtin_amdgcn_exp2f(m[b] - r);
-                    m[b] = r;
-                    sum[b] *= f;
-                    more[b] = 0.f;
-#pragma unroll
-                    for (int j = 0; j < kDt; ++j) o[b][j] *= f;
-                    ref[b] = m[b] == kNone ? 0.f : -m[b];
-                }
+                for (int j = 0; j < kDt; ++j) o[j] *= f;
+                ref = m == kNone ? 0.f : -m;
                 exps(0, 0, 8);
             };
 
@@ -368,8 +332,7 @@ __global__ __launch_bounds__(K::kGroup, K::kResident * K::Source::kWaves / 4) vo
                 mix<kProducts, kBeside>();
                 stay();
             }
-#pragma unroll
-            for (int b = 0; b < RB; ++b) more[b] = before[b] = 0.f, most[b] = kNone, ref[b] = m[b] == kNone ? 0.f : -m[b];
+            more = before = 0.f, most = kNone, ref = m == kNone ? 0.f : -m;
             mask(0);
             if constexpr (kSub == 2) {
                 // a half's probabilities beside the other half's products
@@ -385,8 +348,7 @@ __global__ __launch_bounds__(K::kGroup, K::kResident * K::Source::kWaves / 4) vo
                 mask(1);
                 if constexpr (S::kSums) {
                     settle(0, true);
-#pragma unroll
-                    for (int b = 0; b < RB; ++b) before[b] = more[b];
+                    before = more;
                 } else {
                     follow(1, 0, 16);
                     settle_both();
@@ -411,96 +373,76 @@ __global__ __launch_bounds__(K::kGroup, K::kResident * K::Source::kWaves / 4) vo
                 mix<kProducts, kBeside>();
                 stay();
             }
-#pragma unroll
-            for (int b = 0; b < RB; ++b) sum[b] += more[b];
+            sum += more;
             if (S::found(flag)) {
                 // infinities and NaN of V, zeros in the products, reach the rows that see their keys, and only those
 #pragma unroll 1
                 for (int i = 0; i < kKeys; ++i)
 #pragma unroll 1
                     for (int c = 0; c < 16 * kDt; ++c)  // register c % 16 of o[c / 16]
-                        if (S::bad(flag, bads[buf], i, c / 16 * 32 + c % 16 / 4 * 8 + 4 * h + c % 4))
-#pragma unroll
-                            for (int b = 0; b < RB; ++b)
-                                if (key0 + i >= lo[b] && key0 + i < hi[b]) bad[b] |= uint64_t(1) << c;
+                        if (S::bad(flag, bads[buf], i, c / 16 * 32 + c % 16 / 4 * 8 + 4 * h + c % 4) && key0 + i >= lo && key0 + i < hi)
+                            bad |= uint64_t(1) << c;
             }
             buf = next_buf;
             next_buf = next_buf == 2 ? 0 : next_buf + 1;
         }
+        if (__any(bad != 0))
 #pragma unroll
-        for (int b = 0; b < RB; ++b)
-            if (__any(bad[b] != 0))
-#pragma unroll
-                for (int c = 0; c < 16 * kDt; ++c)
-                    if (bad[b] >> c & 1) o[b][c / 16][c % 16] = __builtin_nanf("");
+            for (int c = 0; c < 16 * kDt; ++c)
+                if (bad >> c & 1) o[c / 16][c % 16] = __builtin_nanf("");
 
-        float l[RB];
-#pragma unroll
-        for (int b = 0; b < RB; ++b) l[b] = sum[b] + __shfl_xor(sum[b], 32, 64);
+        float l = sum + __shfl_xor(sum, 32, 64);
         // A part: a wave's values in its own order, side by side over the lanes, and behind all waves' each row's m and l.
-        const auto part_at = [&](int64_t slot, int b) {
-            return p.part + slot * part_floats<D>(kRows) + int64_t(wave * RB + b) * (32 * D) + 2 * lane;
-        };
-        const auto row_at = [&](int64_t slot, int b) {
-            return p.part + slot * part_floats<D>(kRows) + kRows * D + 2 * ((wave * RB + b) * 32 + n);
-        };
+        const auto part_at = [&](int64_t slot) { return p.part + slot * part_floats<D>(kRows) + int64_t(wave) * (32 * D) + 2 * lane; };
+        const auto row_at = [&](int64_t slot) { return p.part + slot * part_floats<D>(kRows) + kRows * D + 2 * (wave * 32 + n); };
         const bool whole = a == 0 && z == count;
         const bool mine = whole || join_parts(p, w, z, count,
             [&](int64_t slot) {
+                if (row0 >= rows) return;
+                float* const y = part_at(slot);
 #pragma unroll
-                for (int b = 0; b < RB; ++b) {
-                    if (row0 + 32 * b >= rows) continue;
-                    float* const y = part_at(slot, b);
-#pragma unroll
-                    for (int i = 0; i < 8 * kDt; ++i) store_far(y + 128 * i, o[b][i / 8][2 * (i % 8)], o[b][i / 8][2 * (i % 8) + 1]);
-                    if (h == 0) store_far(row_at(slot, b), m[b], l[b]);
-                }
+                for (int i = 0; i < 8 * kDt; ++i) store_far(y + 128 * i, o[i / 8][2 * (i % 8)], o[i / 8][2 * (i % 8) + 1]);
+                if (h == 0) store_far(row_at(slot), m, l);
             },
             [&](int64_t slot) {
+                if (row0 >= rows) return;
+                const float* const y = part_at(slot);
+                float2 x[8 * kDt];
+                const float2 ml = load_far(row_at(slot));
 #pragma unroll
-                for (int b = 0; b < RB; ++b) {
-                    if (row0 + 32 * b >= rows) continue;
-                    const float* const y = part_at(slot, b);
-                    float2 x[8 * kDt];
-                    const float2 ml = load_far(row_at(slot, b));
+                for (int i = 0; i < 8 * kDt; ++i) x[i] = load_far(y + 128 * i);
+                const float top = fmaxf(m, ml.x);
+                // zeros of a part that saw nothing, or NaN that must show
+                const float f = m == kNone ? 0.f : __builtin_amdgcn_exp2f(m - top), g = ml.x == kNone ? 0.f : __builtin_amdgcn_exp2f(ml.x - top);
+                m = top;
+                l = l * f + ml.y * g;
 #pragma unroll
-                    for (int i = 0; i < 8 * kDt; ++i) x[i] = load_far(y + 128 * i);
-                    const float top = fmaxf(m[b], ml.x);
-                    // zeros of a part that saw nothing, or NaN that must show
-                    const float f = m[b] == kNone ? 0.f : __builtin_amdgcn_exp2f(m[b] - top), g = ml.x == kNone ? 0.f : __builtin_amdgcn_exp2f(ml.x - top);
-                    m[b] = top;
-                    l[b] = l[b] * f + ml.y * g;
-#pragma unroll
-                    for (int i = 0; i < 8 * kDt; ++i) {
-                        o[b][i / 8][2 * (i % 8)] = o[b][i / 8][2 * (i % 8)] * f + x[i].x * g;
-                        o[b][i / 8][2 * (i % 8) + 1] = o[b][i / 8][2 * (i % 8) + 1] * f + x[i].y * g;
-                    }
+                for (int i = 0; i < 8 * kDt; ++i) {
+                    o[i / 8][2 * (i % 8)] = o[i / 8][2 * (i % 8)] * f + x[i].x * g;
+                    o[i / 8][2 * (i % 8) + 1] = o[i / 8][2 * (i % 8) + 1] * f + x[i].y * g;
                 }
             });
-        if (mine)
+        const int row = row0 + n;
+        if (mine && row < rows) {
+            const int token = token_of(p, row), q_head = w.head * p.share + row - token * p.share;
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            T* const dst = row_ptr<T>(p.out, s.q0 + token, q_head);
+            // registers 4 k .. are channels 8 k + 4 h ..
 #pragma unroll
-            for (int b = 0; b < RB; ++b) {
-                const int row = row0 + 32 * b + n;
-                if (row >= rows) continue;
-                const int token = token_of(p, row), q_head = w.head * p.share + row - token * p.share;
-                const float inv = l[b] == 0.f ? 0.f : 1.f / l[b];
-                T* const dst = row_ptr<T>(p.out, s.q0 + token, q_head);
-                // registers 4 k .. are channels 8 k + 4 h ..
+            for (int j = 0; j < kDt; ++j)
 #pragma unroll
-                for (int j = 0; j < kDt; ++j)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int c = 32 * j + 8 * k + 4 * h;
-                        const vf4 x{o[b][j][4 * k], o[b][j][4 * k + 1], o[b][j][4 * k + 2], o[b][j][4 * k + 3]};
-                        if constexpr (sizeof(T) == 4) {
-                            *reinterpret_cast<vf4*>(dst + c) = x * inv;
-                        } else {
-                            typedef __bf16 vb4 __attribute__((ext_vector_type(4)));
-                            *reinterpret_cast<vb4*>(dst + c) = __builtin_convertvector(x * inv, vb4);
-                        }
+                for (int k = 0; k < 4; ++k) {
+                    const int c = 32 * j + 8 * k + 4 * h;
+                    const vf4 x{o[j][4 * k], o[j][4 * k + 1], o[j][4 * k + 2], o[j][4 * k + 3]};
+                    if constexpr (sizeof(T) == 4) {
+                        *reinterpret_cast<vf4*>(dst + c) = x * inv;
+                    } else {
+                        typedef __bf16 vb4 __attribute__((ext_vector_type(4)));
+                        *reinterpret_cast<vb4*>(dst + c) = __builtin_convertvector(x * inv, vb4);
                     }
-                if (h == 0 && p.lse) p.lse[int64_t(s.q0 + token) * p.q_heads + q_head] = lse_of(m[b], l[b]);
-            }
+                }
+            if (h == 0 && p.lse) p.lse[int64_t(s.q0 + token) * p.q_heads + q_head] = lse_of(m, l);
+        }
 
         w.rest = 0;
         if (w.at >= w.end) break;

@@ -165,7 +165,7 @@ template <typename T, int D, typename F>
 auto with_kernel(int64_t max_rows, F f) {
     if (max_rows <= 16) return f(Few8<T, D, 1>(), few8_kernel<T, D, 1>);
     if (max_rows <= 32) return f(Few8<T, D, 2>(), few8_kernel<T, D, 2>);
-    using K = Tile<Kv8Source<T, D, sizeof(T) == 2 ? 8 : 4>, 1>;
+    using K = Tile<Kv8Source<T, D, sizeof(T) == 2 ? 8 : 4>>;
     return f(K(), tile_kernel<K>);
 }
 
