@@ -21,8 +21,11 @@ namespace {
 
 constexpr int kBlock = 1024;
 constexpr int kBlockWaves = kBlock / 64;
-// Up to so many pages and so many table entries are one workgroup's work.
-constexpr int64_t kSmall = 1 << 15;
+// Up to so many pages and so many table entries are one workgroup's work.  As graphs, in one launch and in several:
+// 32000 pages, 1600 entries: resize 22.7 and 23.9 us, fork 25.5 and 26.6, compact 19.6 and 20.8;  500 pages, 2048
+// entries: 18.0 and 19.9, 17.1 and 22.3;  2000 pages, 6400 entries: 20.8 and 20.0, 23.3 and 23.1, a fork that
+// parts all rows 29.5 and 23.5;  32000 pages, 32000 entries: 37 and 25, 61 and 27, 95 and 28.
+constexpr int64_t kSmall = 1 << 15, kSmallEntries = 1 << 12;
 
 // The sum may pass 2^31, where page sizes are no powers of two, but not 2^32: a row has fewer than 2^31 - 256 tokens.
 __device__ __forceinline__ int pages_of(int len, int page_size) {
@@ -263,7 +266,7 @@ uint32_t blocks_for(int64_t n) {
 template <typename OP>
 hipError_t run(const PagesArgs& p, hipStream_t stream) {
     const int64_t entries = int64_t(p.rows) * p.width, most = entries > p.pages ? entries : p.pages;
-    if (most <= kSmall) {
+    if (p.pages <= kSmall && entries <= kSmallEntries) {
         small_kernel<OP><<<1, kBlock, 0, stream>>>(p);
         return hipGetLastError();
     }
