@@ -165,7 +165,7 @@ constexpr int64_t kMaxRows = int64_t(1) << 28;
 constexpr wide kMaxExtent = wide(1) << 46;  // bytes: beyond any device's memory
 // Sequences of one attention call: every workgroup counts through them, 64 at a time and in 32 bits.
 constexpr int kMaxSequences = 1 << 24;
-// Query tokens times query heads of one: a tile of up to 128 rows behind the last still counts in 32 bits.
+// Query tokens times query heads of one: a tile of up to 256 rows behind the last still counts in 32 bits.
 constexpr int64_t kMaxAttnRows = (int64_t(1) << 31) - 256;
 // Tokens that cf_kv8_append takes at once: a wave for each in a dispatch of 2^32 - 1 work-items, and head by head.
 constexpr int64_t kMaxAppend = int64_t(1) << 27;

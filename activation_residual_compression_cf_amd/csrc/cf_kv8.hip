@@ -153,9 +153,10 @@ __device__ __forceinline__ int sequence_from(const AppendArgs& p, int b, int t0)
 // K's leave in runs of a row.  TILE tokens of the call are looked through for first tokens of blocks, each by a
 // lane: 16, or one where a call has few tokens of each sequence.
 // Bound by instructions and by how many waves hide the loads of starts, lengths, pages and rows that follow each other:
-// rows kept as they came (94 registers for bf16 and D = 128, 119 with fp32 values) and no value cut off that need not be
-// took 9180 prompt tokens of 24 heads from 57 to 35 us (169 MB, 4.9 TB/s), one token each of 61 sequences from 6.9
-// to 5.7.  Slower: a loop over heads, which saves their lookups and takes registers (72 us).
+// bf16 rows kept as they came (D = 128: 94 registers, widened 119; fp32 rows 167) and no value cut off that need not be
+// took 9180 prompt tokens of 24 heads from 57 to 35 us (169 MB, 4.9 TB/s; 33 to 45 us from box to box), one token each
+// of 61 sequences from 6.9 to 5.7.  fp32 rows: 52 us, 5.5 TB/s; D = 64: 22 and 29 us.  Slower: a loop over heads, which
+// saves their lookups and takes registers (72 us).
 template <typename T, int D, int TILE>
 __global__ __launch_bounds__(kThreads) void append_kernel(const AppendArgs p) {
     constexpr int CH = D / 32;

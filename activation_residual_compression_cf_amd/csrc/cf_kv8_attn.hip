@@ -6,7 +6,9 @@
 // Precision.  What the cache holds is exact in bf16, and in fp16 too (the scales' exponents see to that), and so are
 // bf16 queries; fp32 queries are split into three bf16 parts that add up to them, and so are their probabilities.
 // With bf16 queries probabilities are rounded to fp16 where rows are few (half a step is 2^-11 of each) and to
-// bf16 where they are many (2^-8).  Sums, references and O are fp32, and the sum is of unrounded probabilities.
+// bf16 where they are many (2^-8).  bf16 has fp32's range: each keeps its 2^-8 however far below its tile's others it
+// lies, where fp16's run out 2^-21 below (beside a key that outweighs the other 63 by e^22 these would be subnormals, by
+// e^30 nothing), and no reference has to fall.  Sums, references and O are fp32, and the sum is of unrounded probabilities.
 //
 // Work is cut as in cf_attn_plan.h.  The kernel for few rows (at most 32: decoding) is bound by the cache's bytes, the
 // one for many rows (cf_attn_tile.h) by the matrix and vector units.
