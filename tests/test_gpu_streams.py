@@ -183,3 +183,33 @@ def test_work_queued_on_the_callers_stream_does_not_reach_a_calls_buffers(cf):
         got = all_calls(side)
         for x, y in zip(got, expect):
             assert torch.equal(x, y)
+
+
+def test_captured_calls_on_a_side_stream(cf):
+    """Calls that allocate for themselves, on a stream that joins a capture: every replay gives what an eager call does."""
+    dev = cf.require_device()
+    say("captured calls on a side stream with the binding's own buffers")
+    g = torch.Generator(device="cuda").manual_seed(5)
+    q, k, v = (torch.randn(n, h, 64, generator=g, device=dev).bfloat16() for n, h in ((150, 4), (700, 2), (700, 2)))
+    pt = cf.PageTable.create(60, 4, 30, 16)
+    want = torch.tensor([100, 200, 33, 0], dtype=torch.int32, device=dev)
+
+    def calls(stream):
+        t, missing = cf.pages_resize(pt, want, stream=stream)
+        return [cf.attention(q, k, v, causal=True, stream=stream), t.refs, t.table, t.lens, missing]
+
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        got = calls(side)
+        more = q * 2  # the capture's own stream allocates beside it
+        torch.cuda.current_stream().wait_stream(side)
+    for i in range(4):
+        q.copy_(torch.randn(q.shape, generator=g, device=dev))
+        want.add_(i)
+        graph.replay()
+        torch.cuda.synchronize()
+        for x, y in zip(got + [more], calls(None) + [q * 2]):
+            assert torch.equal(x, y), f"replay {i}"
